@@ -297,6 +297,89 @@ dg_status dg_quantize_fp8_1x128_transposed(const float* x, void* q, float* s, in
 dg_status dg_swiglu_quantize_fp8_1x128(const void* c, void* q, float* s, int m, int i,
                                        hipStream_t stream);
 
+/* ---- linear layer: GEMM with bias, activation and residual --------------
+ *     pre = A . B^T + bias
+ *     C   = activation(pre) + residual
+ * with fp32 accumulation, the whole epilogue in fp32 and one rounding of C.
+ * Rows are strided: lda, ldb, ldc, ... are the elements between the starts of
+ * two rows (at least the row length); the last dimension is contiguous.  No
+ * operand may overlap C or pre, except residual == C with the same stride. */
+typedef enum {
+  DG_ACT_NONE = 0,
+  DG_ACT_RELU = 1,
+  DG_ACT_GELU = 2,      /* x * Phi(x), error below 1.5e-7 in Phi */
+  DG_ACT_GELU_TANH = 3, /* x/2 * (1 + tanh(sqrt(2/pi) * (x + 0.044715 x^3))) */
+  DG_ACT_SILU = 4       /* x / (1 + e^-x) */
+} dg_activation;
+
+typedef enum {
+  DG_TYPE_BF16 = 0,
+  DG_TYPE_F32 = 1
+} dg_type;
+
+typedef struct {
+  const void* bias;     /* [N] of bias_type, or null                        */
+  int bias_type;        /* dg_type                                          */
+  int activation;       /* dg_activation                                    */
+  const void* residual; /* [M,N] bf16, or null                              */
+  int64_t ld_residual;
+  void* pre;            /* [M,N] bf16: pre rounded, for the backward pass, or
+                           null (the activation sees the unrounded value)   */
+  int64_t ld_pre;
+} dg_epilogue;
+
+/* ---- a whole mixture-of-experts layer for a few tokens -------------------
+ * The decode form of an MoE layer, in two kernels: routing, the chosen
+ * experts' gate and up projections with SwiGLU, their down projections, and
+ * the weighted sum over a token's experts (DeepGEMM pages, "Ключевые функции:
+ * Mega MoE и индексация": the expert layers fused; the masked layout above is
+ * the decode case with rows already gathered per expert).  For token t with
+ * chosen experts e_j and weights w_j:
+ *     h_j  = silu(x.Wg[e_j]^T) * (x.Wu[e_j]^T)
+ *     y[t] = residual[t] + sum_j w_j * (h_j . W2[e_j]^T)
+ *   x [T,H] bf16; residual [T,H] bf16 or null; y [T,H] bf16, every element
+ *     written (y may be residual; no other overlap);
+ *   w13 [E,2I,H]: rows [0,I) the gate, [I,2I) the up projection of an expert
+ *     (the column layout of dg_swiglu_quantize_fp8_1x128); w2 [E,H,I];
+ *     fp8 e4m3 with s13 [E,2I/128,H/128], s2 [E,H/128,I/128] fp32 (128x128
+ *     blocks), or bf16 without scales;
+ *   routing, one of
+ *     logits [T,E] fp32 given: the top_k largest logits of a token, ties to
+ *       the lowest expert, -inf never chosen; weights e^l / sum (softmax) or
+ *       1 / (1 + e^-l) (sigmoid), the sum taken over the chosen experts
+ *       (renormalize != 0) or over all (softmax; sigmoid: no division), times
+ *       `scale`.  ids [T,k] int32 and weights [T,k] fp32 are written, in order
+ *       of falling logits; -1 and 0 where a token has no expert left.  A NaN
+ *       logit counts as the largest and makes its token's weights NaN.
+ *     logits null: ids and weights are read (scoring, renormalize and scale
+ *       are not used).  An id outside [0,E) drops out; an expert named twice by
+ *       a token counts with the sum of its weights.
+ *   workspace: T * top_k * I bf16 values (the weighted h), 16-byte aligned;
+ *     the call's until its kernels end.
+ * x stays bf16 (the weights are widened to bf16 exactly); sums are fp32, and
+ * w_j h_j is rounded to bf16 once.  A token never sees the values of the
+ * others (only the order of its fp32 sums follows the call's routing), and the
+ * call is deterministic.
+ * 1 <= T <= 64, top_k <= 16, top_k <= E <= 512, H and I multiples of 128 up to
+ * 2^20; x, w13, w2 16-byte aligned, y and residual 8-byte.  Nothing is
+ * allocated: the call can be captured. */
+typedef enum {
+  DG_SCORING_SOFTMAX = 0,
+  DG_SCORING_SIGMOID = 1
+} dg_scoring;
+
+dg_status dg_moe_few_tokens_fp8(const void* x, const float* logits, int32_t* ids, float* weights,
+                                const void* w13, const float* s13, const void* w2,
+                                const float* s2, const void* residual, void* y, void* workspace,
+                                int tokens, int hidden, int intermediate, int num_experts,
+                                int top_k, int scoring, int renormalize, float scale,
+                                hipStream_t stream);
+dg_status dg_moe_few_tokens_bf16(const void* x, const float* logits, int32_t* ids, float* weights,
+                                 const void* w13, const void* w2, const void* residual, void* y,
+                                 void* workspace, int tokens, int hidden, int intermediate,
+                                 int num_experts, int top_k, int scoring, int renormalize,
+                                 float scale, hipStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* dg_status_string(dg_status s);
 

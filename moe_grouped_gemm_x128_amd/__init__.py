@@ -55,6 +55,11 @@ for _f in ("dg_gemm_fp8_nt", "dg_grouped_fp8_contiguous", "dg_grouped_fp8_contig
            "dg_quantize_fp8_128x128", "dg_quantize_fp8_1x128_transposed", "dg_swiglu_quantize_fp8_1x128",
            "dg_quantize_fp8_1x128_ue8m0", "dg_quantize_fp8_128x128_ue8m0"):
     getattr(_lib, _f).restype = ctypes.c_int
+_f32c = ctypes.c_float
+_lib.dg_moe_few_tokens_fp8.argtypes = [_vp] * 11 + [_i32] * 7 + [_f32c, _vp]
+_lib.dg_moe_few_tokens_fp8.restype = ctypes.c_int
+_lib.dg_moe_few_tokens_bf16.argtypes = [_vp] * 9 + [_i32] * 7 + [_f32c, _vp]
+_lib.dg_moe_few_tokens_bf16.restype = ctypes.c_int
 _lib.dg_status_string.argtypes = [ctypes.c_int]
 _lib.dg_status_string.restype = ctypes.c_char_p
 _lib.dg_version.restype = ctypes.c_int
@@ -451,6 +456,78 @@ def dg_swiglu_quantize_fp8_1x128(c, q, s):
     _check(_lib.dg_swiglu_quantize_fp8_1x128(_ptr(c), _ptr(q), _ptr(s), m, i, _stream(c)),
            "dg_swiglu_quantize_fp8_1x128")
     return q, s
+
+
+# ------------------------------------- a whole MoE layer for a few tokens ---
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def _moe_few_tokens(name, fp8, x, w13, w2, out, ids, weights, logits, scoring, renormalize, scale, residual,
+                    workspace):
+    _bf16(x, "x"); _bf16(out, "out"); _f32(weights, "weights")
+    if fp8:
+        (w13, s13), (w2, s2) = w13, w2
+        _fp8(w13, "w13"); _fp8(w2, "w2"); _f32(s13, "s13"); _f32(s2, "s2")
+    else:
+        _bf16(w13, "w13"); _bf16(w2, "w2")
+    if ids.dtype != torch.int32:
+        raise TypeError("ids must be int32")
+    t, h = x.shape
+    e, n, _ = w13.shape
+    if n % 256:
+        raise ValueError(f"w13 must stack gate and up projections of a width that is a multiple of 128 (2I={n})")
+    i = n // 2
+    k = ids.shape[-1]
+    _shape(w13, (e, n, h), "w13"); _shape(w2, (e, h, i), "w2"); _shape(out, (t, h), "out")
+    _shape(ids, (t, k), "ids"); _shape(weights, (t, k), "weights")
+    tensors = [x, w13, w2, out, ids, weights]
+    if fp8:
+        _shape(s13, (e, n // 128, h // 128), "s13"); _shape(s2, (e, h // 128, i // 128), "s2")
+        tensors += [s13, s2]
+    if logits is not None:
+        _f32(logits, "logits"); _shape(logits, (t, e), "logits")
+        tensors.append(logits)
+    if residual is not None:
+        _bf16(residual, "residual"); _shape(residual, (t, h), "residual")
+        tensors.append(residual)
+    if workspace is None:
+        workspace = torch.empty(t * k * i, dtype=torch.bfloat16, device=x.device)
+    elif workspace.numel() * workspace.element_size() < 2 * t * k * i:
+        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, {2 * t * k * i} needed")
+    tensors.append(workspace)
+    _dev(*tensors)
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be one of {sorted(_SCORING)}, got {scoring!r}")
+    lg = None if logits is None else _ptr(logits)
+    rs = None if residual is None else _ptr(residual)
+    tail = (rs, _ptr(out), _ptr(workspace), t, h, i, e, k, _SCORING[scoring], 1 if renormalize else 0, scale,
+            _stream(x))
+    if fp8:
+        st = _lib.dg_moe_few_tokens_fp8(_ptr(x), lg, _ptr(ids), _ptr(weights), _ptr(w13), _ptr(s13), _ptr(w2),
+                                        _ptr(s2), *tail)
+    else:
+        st = _lib.dg_moe_few_tokens_bf16(_ptr(x), lg, _ptr(ids), _ptr(weights), _ptr(w13), _ptr(w2), *tail)
+    _check(st, name)
+    return out
+
+
+def moe_few_tokens_fp8(x, w13, w2, out, ids, weights, logits=None, scoring="softmax", renormalize=True, scale=1.0,
+                       residual=None, workspace=None):
+    """A whole MoE layer for 1..64 tokens on FP8 weights (see include/dg.h):
+    x bf16 [T,H], w13 = (fp8 [E,2I,H], fp32 [E,2I/128,H/128]) with the gate
+    rows first, w2 = (fp8 [E,H,I], fp32 [E,H/128,I/128]), out bf16 [T,H].
+    With logits fp32 [T,E] the call routes and writes ids int32 [T,k] and
+    weights fp32 [T,k]; without, it reads them."""
+    return _moe_few_tokens("dg_moe_few_tokens_fp8", True, x, w13, w2, out, ids, weights, logits, scoring,
+                           renormalize, scale, residual, workspace)
+
+
+def moe_few_tokens_bf16(x, w13, w2, out, ids, weights, logits=None, scoring="softmax", renormalize=True, scale=1.0,
+                        residual=None, workspace=None):
+    """moe_few_tokens_fp8 on BF16 weights w13 [E,2I,H] and w2 [E,H,I]."""
+    return _moe_few_tokens("dg_moe_few_tokens_bf16", False, x, w13, w2, out, ids, weights, logits, scoring,
+                           renormalize, scale, residual, workspace)
 
 
 # ------------------------------------------------------ page-style names ---
