@@ -328,6 +328,43 @@ typedef struct {
   int64_t ld_pre;
 } dg_epilogue;
 
+/* BF16: a [M,K], b [N,K]; c [M,N] of c_type.  K % 8 == 0, K <= 2^22; a, b 16-byte
+ * aligned with lda, ldb multiples of 8; lda, ldb <= 2^23; c, bias, residual and
+ * pre aligned to their element.  Few rows (M <= 64) run in one kernel that
+ * streams b; more run on tiles, with K split over workgroups (fp32 partials in the
+ * stream's split-K workspace, see above; not while capturing) where there are few.
+ * epi null: the plain product. */
+dg_status dg_gemm_bf16_nt_epilogue(const void* a, int64_t lda, const void* b, int64_t ldb, void* c,
+                                   int64_t ldc, int c_type, const dg_epilogue* epi, int m, int n,
+                                   int k, hipStream_t stream);
+
+/* FP8: operands and scales as dg_gemm_fp8_nt (contiguous rows, K % 128 == 0,
+ * K <= 2^22). */
+dg_status dg_gemm_fp8_nt_epilogue(const void* a, const float* sa, const void* b, const float* sb,
+                                  void* c, int64_t ldc, int c_type, const dg_epilogue* epi, int m,
+                                  int n, int k, hipStream_t stream);
+
+/* Backward pass of the BF16 linear layer.  With dc [M,N] bf16, the gradient
+ * of C, and pre [M,N] bf16, the stored pre-activation (null and unused for
+ * DG_ACT_NONE):
+ *     dpre  = dc * activation'(pre)
+ *     da    = dpre . B       [M,K] bf16
+ *     db    = dpre^T . A     [N,K] bf16
+ *     dbias = sum over rows of dpre  [N] fp32, in a fixed order
+ * (the residual's gradient is dc).  Outputs that are null are not computed; da,
+ * db and dbias are overwritten.  dpre enters the products rounded to bf16 once
+ * (dbias sums the unrounded values); sums are fp32.  A and B are read where they
+ * lie: no transposed copies.  a [M,K], b [N,K] as in the forward call; the
+ * gradients' rows are strided like the operands.  workspace: the bytes that
+ * dg_gemm_bf16_nt_epilogue_backward_workspace returns, 16-byte aligned, the
+ * call's until its kernels end. */
+dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const void* a, int64_t lda,
+                                            const void* b, int64_t ldb, const void* pre,
+                                            int64_t ld_pre, int activation, void* da, int64_t ldda,
+                                            void* db, int64_t lddb, float* dbias, void* workspace,
+                                            int m, int n, int k, hipStream_t stream);
+dg_status dg_gemm_bf16_nt_epilogue_backward_workspace(int m, int n, int64_t* bytes);
+
 /* ---- a whole mixture-of-experts layer for a few tokens -------------------
  * The decode form of an MoE layer, in two kernels: routing, the chosen
  * experts' gate and up projections with SwiGLU, their down projections, and

@@ -55,7 +55,23 @@ for _f in ("dg_gemm_fp8_nt", "dg_grouped_fp8_contiguous", "dg_grouped_fp8_contig
            "dg_quantize_fp8_128x128", "dg_quantize_fp8_1x128_transposed", "dg_swiglu_quantize_fp8_1x128",
            "dg_quantize_fp8_1x128_ue8m0", "dg_quantize_fp8_128x128_ue8m0"):
     getattr(_lib, _f).restype = ctypes.c_int
-_f32c = ctypes.c_float
+_f32c, _i64 = ctypes.c_float, ctypes.c_int64
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("bias", _vp), ("bias_type", _i32), ("activation", _i32), ("residual", _vp), ("ld_residual", _i64),
+                ("pre", _vp), ("ld_pre", _i64)]
+
+
+_lib.dg_gemm_bf16_nt_epilogue.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _i32, _vp]
+_lib.dg_gemm_bf16_nt_epilogue.restype = ctypes.c_int
+_lib.dg_gemm_fp8_nt_epilogue.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _i32, _i32, _i32, _vp]
+_lib.dg_gemm_fp8_nt_epilogue.restype = ctypes.c_int
+_lib.dg_gemm_bf16_nt_epilogue_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp,
+                                                   _i64, _vp, _vp, _i32, _i32, _i32, _vp]
+_lib.dg_gemm_bf16_nt_epilogue_backward.restype = ctypes.c_int
+_lib.dg_gemm_bf16_nt_epilogue_backward_workspace.argtypes = [_i32, _i32, ctypes.POINTER(_i64)]
+_lib.dg_gemm_bf16_nt_epilogue_backward_workspace.restype = ctypes.c_int
 _lib.dg_moe_few_tokens_fp8.argtypes = [_vp] * 11 + [_i32] * 7 + [_f32c, _vp]
 _lib.dg_moe_few_tokens_fp8.restype = ctypes.c_int
 _lib.dg_moe_few_tokens_bf16.argtypes = [_vp] * 9 + [_i32] * 7 + [_f32c, _vp]
@@ -456,6 +472,144 @@ def dg_swiglu_quantize_fp8_1x128(c, q, s):
     _check(_lib.dg_swiglu_quantize_fp8_1x128(_ptr(c), _ptr(q), _ptr(s), m, i, _stream(c)),
            "dg_swiglu_quantize_fp8_1x128")
     return q, s
+
+
+# -------------------------------------- linear layer with its epilogue ---
+
+_ACTIVATION = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _activation(name):
+    a = _ACTIVATION.get(name)
+    if a is None:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATION)}, got {name!r}")
+    return a
+
+
+def _ld(t, dev, name):
+    """Row stride of a 2-D tensor with contiguous rows on GPU `dev`."""
+    if t.get_device() != dev:  # -1 on the host
+        raise ValueError("all tensors must be on the same GPU")
+    ld, one = t.stride()
+    cols = t.shape[1]
+    if (one != 1 and cols > 1) or (ld < cols and t.shape[0] > 1):
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    return ld if ld >= cols else cols
+
+
+def _epilogue(out, bias, activation, residual, pre, m, n, dev):
+    e = _Epilogue()
+    e.activation = _activation(activation)
+    if bias is not None:
+        if bias.dtype not in _TYPE:
+            raise TypeError(f"bias must be bfloat16 or float32, got {bias.dtype}")
+        if bias.shape != (n,) or (n > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias must be contiguous with shape {(n,)}, got {tuple(bias.shape)}")
+        if bias.get_device() != dev:
+            raise ValueError("all tensors must be on the same GPU")
+        e.bias, e.bias_type = _ptr(bias), _TYPE[bias.dtype]
+    if residual is not None:
+        _bf16(residual, "residual"); _shape(residual, (m, n), "residual")
+        e.residual, e.ld_residual = _ptr(residual), _ld(residual, dev, "residual")
+    if pre is not None:
+        _bf16(pre, "pre"); _shape(pre, (m, n), "pre")
+        e.pre, e.ld_pre = _ptr(pre), _ld(pre, dev, "pre")
+    return e
+
+
+def _linear_out(out, m, n, dev):
+    if out.dtype not in _TYPE:
+        raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
+    _shape(out, (m, n), "out")
+    return _ld(out, dev, "out")
+
+
+def _gpu(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    return t.get_device()
+
+
+def gemm_bf16_nt_epilogue(a, b, out, bias=None, activation="none", residual=None, pre=None):
+    """out[M,N] = activation(a[M,K] . b[N,K]^T + bias) + residual in BF16 (see
+    dg_gemm_bf16_nt_epilogue in include/dg.h).  out bf16 or fp32; bias [N] bf16
+    or fp32; residual [M,N] bf16 (may be out); pre [M,N] bf16 receives the
+    pre-activation for the backward pass.  Rows may be strided."""
+    _bf16(a, "a"); _bf16(b, "b")
+    m, k = a.shape
+    n = b.shape[0]
+    _shape(b, (n, k), "b")
+    dev = _gpu(a)
+    ldc = _linear_out(out, m, n, dev)
+    e = _epilogue(out, bias, activation, residual, pre, m, n, dev)
+    _check(_lib.dg_gemm_bf16_nt_epilogue(_ptr(a), _ld(a, dev, "a"), _ptr(b), _ld(b, dev, "b"), _ptr(out), ldc,
+                                         _TYPE[out.dtype], ctypes.addressof(e), m, n, k, _stream(a)),
+           "dg_gemm_bf16_nt_epilogue")
+    return out
+
+
+def gemm_fp8_nt_epilogue(lhs, rhs, out, bias=None, activation="none", residual=None, pre=None):
+    """gemm_bf16_nt_epilogue on FP8 operands with their scales: lhs = (fp8
+    [M,K], fp32 [M,K/128]), rhs = (fp8 [N,K], fp32 [ceil(N/128),K/128])."""
+    (a, sa), (b, sb) = lhs, rhs
+    _fp8(a, "a"); _fp8(b, "b"); _f32(sa, "sa"); _f32(sb, "sb")
+    m, k = a.shape
+    n = b.shape[0]
+    _shape(b, (n, k), "b"); _shape(sa, (m, k // 128), "sa"); _shape(sb, ((n + 127) // 128, k // 128), "sb")
+    _dev(a, sa, b, sb)
+    dev = a.get_device()
+    ldc = _linear_out(out, m, n, dev)
+    e = _epilogue(out, bias, activation, residual, pre, m, n, dev)
+    _check(_lib.dg_gemm_fp8_nt_epilogue(_ptr(a), _ptr(sa), _ptr(b), _ptr(sb), _ptr(out), ldc, _TYPE[out.dtype],
+                                        ctypes.addressof(e), m, n, k, _stream(a)),
+           "dg_gemm_fp8_nt_epilogue")
+    return out
+
+
+def gemm_bf16_nt_epilogue_backward(dout, a, b, pre=None, activation="none", da=None, db=None, dbias=None,
+                                   workspace=None):
+    """Gradients of gemm_bf16_nt_epilogue from dout bf16 [M,N] and the stored
+    pre-activation (see include/dg.h): writes those of da bf16 [M,K], db bf16
+    [N,K] and dbias fp32 [N] that are given and returns the three.  The
+    residual's gradient is dout."""
+    _bf16(dout, "dout"); _bf16(a, "a"); _bf16(b, "b")
+    m, k = a.shape
+    n = b.shape[0]
+    _shape(b, (n, k), "b"); _shape(dout, (m, n), "dout")
+    dev = _gpu(dout)
+    act = _activation(activation)
+    if act and pre is None:
+        raise ValueError(f"activation {activation!r} needs the stored pre-activation")
+    pp, ldp = None, 0
+    if act:
+        _bf16(pre, "pre"); _shape(pre, (m, n), "pre")
+        pp, ldp = _ptr(pre), _ld(pre, dev, "pre")
+    pa = pb = pbias = None
+    lda = ldb = 0
+    if da is not None:
+        _bf16(da, "da"); _shape(da, (m, k), "da")
+        pa, lda = _ptr(da), _ld(da, dev, "da")
+    if db is not None:
+        _bf16(db, "db"); _shape(db, (n, k), "db")
+        pb, ldb = _ptr(db), _ld(db, dev, "db")
+    if dbias is not None:
+        _f32(dbias, "dbias"); _shape(dbias, (n,), "dbias")
+        if dbias.get_device() != dev or not dbias.is_contiguous():
+            raise ValueError("dbias must be contiguous, on the same GPU")
+        pbias = _ptr(dbias)
+    need = _i64()
+    _check(_lib.dg_gemm_bf16_nt_epilogue_backward_workspace(m, n, ctypes.byref(need)),
+           "dg_gemm_bf16_nt_epilogue_backward_workspace")
+    if workspace is None:
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=dout.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need.value:
+        raise ValueError(f"workspace must be contiguous, on the same GPU, with at least {need.value} bytes")
+    _check(_lib.dg_gemm_bf16_nt_epilogue_backward(
+        _ptr(dout), _ld(dout, dev, "dout"), _ptr(a), _ld(a, dev, "a"), _ptr(b), _ld(b, dev, "b"), pp, ldp, act,
+        pa, lda, pb, ldb, pbias, _ptr(workspace), m, n, k, _stream(dout)), "dg_gemm_bf16_nt_epilogue_backward")
+    return da, db, dbias
 
 
 # ------------------------------------- a whole MoE layer for a few tokens ---

@@ -55,7 +55,8 @@ int occupancy(int kind, const dg::TileShape& s) {
 // Dense kinds (C [M,N] bf16, one group, K may be split): FP8 with fp32 or
 // power-of-two scales, and BF16.
 bool dense_like(int kind) {
-  return kind == DG_KIND_DENSE || kind == DG_KIND_DENSE_POW2 || kind == DG_KIND_BF16;
+  return kind == DG_KIND_DENSE || kind == DG_KIND_DENSE_POW2 || kind == DG_KIND_BF16 ||
+         kind == dg::KIND_DENSE_LINEAR;
 }
 
 bool parse_forced(dg::TileShape* s) {
@@ -432,6 +433,35 @@ dg_status grouped_masked(const void* a, const float* sa, const void* b, const fl
   p.groups = num_groups;
   p.vec_out = (n % 4 == 0) && aligned(c, 8);
   return run(KIND_MASKED, p, m_max, n, k, num_groups, stream, scratch, scratch_floats);
+}
+
+dg_status linear_fp8(const void* a, const float* sa, const void* b, const float* sb, const Epilogue& e, int m, int n,
+                     int k, hipStream_t stream) {
+  Params p = base_params();
+  p.a = static_cast<const uint8_t*>(a);
+  p.sa = sa;
+  p.b = static_cast<const uint8_t*>(b);
+  p.sb = sb;
+  p.out = e.out;
+  p.epi = e;
+  p.m = m;
+  p.n = n;
+  p.lda = k;
+  p.kbs = k / 128;
+  p.groups = 1;
+  p.vec_out = n % 4 == 0;  // the split-K partials' rows; out goes by p.epi
+  return run(KIND_DENSE_LINEAR, p, m, n, k, 1, stream);
+}
+
+int compute_units() {
+  int cus = 0;
+  return device_cus(&cus) == 0 ? cus : 0;
+}
+
+bool is_capturing(hipStream_t stream) { return stream_capturing(stream); }
+
+void* split_workspace(hipStream_t stream, size_t bytes, bool* owned) {
+  return stream_workspace(stream, bytes, owned);
 }
 }  // namespace dg
 

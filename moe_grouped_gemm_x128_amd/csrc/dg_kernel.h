@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/dg.h"
+#include "dg_epilogue.h"
 
 namespace dg {
 
@@ -26,13 +27,14 @@ enum Kind : int {
   KIND_MASKED_POW2 = 9,    // KIND_MASKED with power-of-two scales applied by the block-scaled MFMA
   KIND_CONTIG_BF16 = 10,   // KIND_CONTIGUOUS with bf16 operands and no scales (as KIND_BF16)
   KIND_MASKED_BF16 = 11,   // KIND_MASKED with bf16 operands and no scales (as KIND_BF16)
+  KIND_DENSE_LINEAR = 12,  // KIND_DENSE with the linear layer's epilogue (Params::epi) on its outputs
 };
 
 // The operand layout and scheduling of a kind (the power-of-two and the
 // grouped bf16 kinds share their fp32-scale kind's; the dense bf16 kind
 // keeps its own).
 constexpr int layout_of(int kind) {
-  return kind == KIND_DENSE_POW2                                 ? KIND_DENSE
+  return kind == KIND_DENSE_POW2 || kind == KIND_DENSE_LINEAR   ? KIND_DENSE
          : kind == KIND_CONTIG_POW2 || kind == KIND_CONTIG_BF16 ? KIND_CONTIGUOUS
          : kind == KIND_MASKED_POW2 || kind == KIND_MASKED_BF16 ? KIND_MASKED
                                                                  : kind;
@@ -74,6 +76,7 @@ struct Params {
   int kchunk;            // K blocks per split
   float* ws;             // fp32 partials [splits][rows of all groups][n]
   int64_t ws_stride;     // floats per split
+  Epilogue epi;          // KIND_DENSE_LINEAR (its `out` is p.out)
   int kg_min_blocks;     // K-grouped: fewest K blocks of any non-empty group
   int kb_begin[kMaxKGroups + 1];  // K-grouped: first 128-block of each group
 };
@@ -90,6 +93,11 @@ hipError_t launch(int kind, const TileShape& shape, const Params& p, int grid,
 // Sums the split-K partials of p.ws in split order and writes bf16 p.out
 // (dense: every row; masked: rows below masked_m of each group).
 hipError_t launch_splitk_reduce(int kind, const Params& p, hipStream_t stream);
+
+// The same with the linear layer's epilogue: partials [splits][m][n],
+// ws_stride floats apart, 16-byte aligned.
+hipError_t launch_splitk_linear(const Epilogue& e, const float* ws, int64_t ws_stride, int splits, int m, int n,
+                                hipStream_t stream);
 
 // FP8 quantiser (dg_quant.hip).  mode 0: x [rows,cols] -> 1x128 groups
 // along cols; 1: 128x128 blocks; 2: x [rows=T, cols=F] -> q [F,T] with 1x128
@@ -108,6 +116,17 @@ hipError_t launch_quantize(int mode, const float* x, uint8_t* q, float* s, int r
 dg_status grouped_masked(const void* a, const float* sa, const void* b, const float* sb, void* c,
                          const int32_t* masked_m, int num_groups, int m_max, int n, int k, hipStream_t stream,
                          float* (*scratch)(), size_t scratch_floats);
+
+// What the linear layer's host code (dg_linear.hip) shares with dg_api.hip:
+// the FP8 product with an epilogue for more rows than the streaming kernel
+// takes (arguments validated), the current device's compute units (0: none to
+// be had), whether a stream is being captured, and a split-K buffer in the
+// stream's order (null: none; *owned: to be returned with hipFreeAsync).
+dg_status linear_fp8(const void* a, const float* sa, const void* b, const float* sb, const Epilogue& e, int m, int n,
+                     int k, hipStream_t stream);
+int compute_units();
+bool is_capturing(hipStream_t stream);
+void* split_workspace(hipStream_t stream, size_t bytes, bool* owned);
 
 // True if an instance exists for (kind, shape).
 bool has_instance(int kind, const TileShape& shape);

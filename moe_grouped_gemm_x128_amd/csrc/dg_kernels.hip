@@ -232,6 +232,7 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
   // in the DMA loop cost the 256x256 instances registers (spills in the loop).
   constexpr bool kStreamB =
       ((LAYOUT == KIND_DENSE || KIND == KIND_BF16) && BM <= 128) || LAYOUT == KIND_MASKED;
+  constexpr bool kLinear = (KIND == KIND_DENSE_LINEAR);  // bias, activation, residual in the epilogue
   constexpr bool kDirectAcc = kPow2 || kBf16;         // MFMAs accumulate into acc: no promotion
   constexpr bool kFp32Out = kRowScaleB;
   // the columns of one wave tile sit inside one 128-block: one sb per wave
@@ -293,7 +294,7 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
   // bf16 epilogue staging: a wave's 16-row fragment row goes through LDS so
   // that each store covers whole (64 columns) or half (32 columns) 128-byte
   // lines; rows padded by 16 bytes against bank conflicts
-  constexpr bool kStage = !kFp32Out && !kSwiGLU && (WTN == 64 || WTN == 32);
+  constexpr bool kStage = !kFp32Out && !kSwiGLU && !kLinear && (WTN == 64 || WTN == 32);
   constexpr int kStageRow = WTN * 2 + 16;
   __shared__ __attribute__((aligned(16))) uint8_t sOut[kStage ? NW : 1][kStage ? 16 * kStageRow : 16];
   // fused SwiGLU: each wave's |h| maximum over its columns, per tile row
@@ -539,7 +540,8 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
   // it; staged layouts: bf16 with N % 8 == 0 only, split-K partials take the
   // per-fragment path with the conservative wait)
   const bool staged = kStage && !(kCanSplit && splits > 1) && p.vec_out && (p.n % 8 == 0);
-  const bool exact_stores = kExactFits && (kStage ? staged : (!kFp32Out || (kCanSplit && splits > 1))) &&
+  // (nor for the linear layer, whose epilogue loads and stores what it is asked to)
+  const bool exact_stores = kExactFits && !(kLinear && splits == 1) && (kStage ? staged : (!kFp32Out || (kCanSplit && splits > 1))) &&
                             p.vec_out && (int64_t)BM * p.n * 4 < 0x7fffffffLL;
   bool stores_pending = false;  // the previous tile's epilogue stores may be in flight
 
@@ -1138,7 +1140,11 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
       for (int i = 0; i < FN; ++i) {
         const int n = n0 + wn * WTN + 16 * i + 4 * lq;
         if (n >= p.n) continue;
-        if constexpr (kFp32Out) {
+        if constexpr (kLinear) {
+          v4f v = acc[i][j];
+          v += epi::bias4(p.epi, n, p.n);
+          epi::finish4(p.epi, orow, n, p.n, v);
+        } else if constexpr (kFp32Out) {
           float* d = static_cast<float*>(p.out) + orow * p.n + n;
           if (p.vec_out && n + 3 < p.n) {
             __builtin_nontemporal_store(f4nt{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]},
@@ -1222,6 +1228,9 @@ hipError_t launch_shape(int kind, const Params& p, int grid, hipStream_t stream)
     case KIND_MASKED_BF16:
       launch_kind<BM, BN, WM, WN, S, KIND_MASKED_BF16>(g, b, stream, p);
       break;
+    case KIND_DENSE_LINEAR:
+      launch_kind<BM, BN, WM, WN, S, KIND_DENSE_LINEAR>(g, b, stream, p);
+      break;
     default:
       return hipErrorInvalidValue;
   }
@@ -1266,9 +1275,41 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(const Params p, int 
   }
 }
 
+// The same with the linear layer's epilogue on each sum.
+__global__ __launch_bounds__(256) void splitk_linear_kernel(const Epilogue e, const float* ws, int64_t ws_stride,
+                                                            int splits, int m, int n, int vec_ws) {
+  const int nq = (n + 3) / 4;
+  const int64_t items = (int64_t)m * nq;
+  for (int64_t it = blockIdx.x * 256LL + threadIdx.x; it < items; it += (int64_t)gridDim.x * 256) {
+    const int64_t row = it / nq;
+    const int c = (int)(it - row * nq) * 4;
+    const float* w = ws + row * n + c;
+    v4f v = epi::bias4(e, c, n);
+    if (vec_ws && c + 3 < n) {
+      for (int sp = 0; sp < splits; ++sp) v += *reinterpret_cast<const v4f*>(w + sp * ws_stride);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (c + r < n)
+          for (int sp = 0; sp < splits; ++sp) v[r] += w[sp * ws_stride + r];
+    }
+    epi::finish4(e, row, c, n, v);
+  }
+}
+
 }  // namespace
 
+hipError_t launch_splitk_linear(const Epilogue& e, const float* ws, int64_t ws_stride, int splits, int m, int n,
+                                hipStream_t stream) {
+  const int64_t blocks = ((int64_t)m * ((n + 3) / 4) + 255) / 256;
+  const int grid = (int)(blocks < 4096 ? blocks : 4096);
+  hipLaunchKernelGGL(splitk_linear_kernel, dim3(grid), dim3(256), 0, stream, e, ws, ws_stride, splits, m, n,
+                     n % 4 == 0 ? 1 : 0);
+  return hipGetLastError();
+}
+
 hipError_t launch_splitk_reduce(int kind, const Params& p, hipStream_t stream) {
+  if (kind == KIND_DENSE_LINEAR) return launch_splitk_linear(p.epi, p.ws, p.ws_stride, p.splits, p.m, p.n, stream);
   const int layout = layout_of(kind);
   if (layout != KIND_DENSE && layout != KIND_MASKED && kind != KIND_BF16) return hipErrorInvalidValue;
   const int64_t items = (int64_t)p.groups * p.m * ((p.n + 3) / 4);

@@ -1,0 +1,399 @@
+// dg_linear_gemm.hip -- BF16 GEMM tiles for the linear layer: the forward
+// product (NT) with its epilogue and the two products of the backward pass,
+// which read an operand with K as its row index (NN, TN) where it lies -- no
+// transposed copy is made.
+//
+// A workgroup of WM x WN waves owns a BM x BN tile; K goes in blocks of 64
+// values through a ring of S LDS stages filled by loads straight to LDS.
+// Stored layouts of a block in LDS:
+//   K contiguous: [row][64 k], 128-byte rows, 16-byte chunk c of row r at
+//     position c ^ swz(r); a fragment is one 16-byte read per lane;
+//   transposed:   [k][BX columns], 32-byte unit u of row k at u ^ hsw(k); a
+//     fragment is two transposing LDS reads (ds_read_b64_tr_b16: 16 lanes read
+//     4 k x 16 columns and each gets the 4 k of its column).
+// Both swizzles are applied on the global side of the load (the lane that lands
+// on a position fetches the chunk that belongs there) and spread the 64 lanes
+// of a fragment read over all banks.
+//
+// Per block a wave multiplies two halves of 32 k.  The fragments of the next
+// half are read while the current half is multiplied; the one barrier of a
+// block sits between the halves, where the last reads of a block's stage and the
+// arrival of the next block meet, so MFMAs are queued on both sides of it.
+//
+// The MFMA takes B rows first and A rows second: a lane holds 4 consecutive
+// columns of one row of C.
+#include <type_traits>
+
+#include "dg_dma.h"
+#include "dg_linear.h"
+
+namespace dg {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+constexpr int kGroupM = 8;  // tile rows per raster group
+constexpr uint32_t kOut = 0x80000000u;
+
+__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+__device__ __forceinline__ int hsw(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ v4f mfma(const v8bf& b, const v8bf& a, const v4f& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+}
+
+// One operand's share of the tile: BX rows of C (or columns), stored K
+// contiguous (TR = false) or transposed.
+template <int BX, int WX, int NW, bool TR>
+struct Operand {
+  static constexpr int kBytes = BX * 128;                    // LDS bytes per stage
+  static constexpr int kPieces = BX / 8;                     // 1 KB loads per stage
+  static constexpr int kQ = kPieces / NW;                    // per wave
+  static constexpr int WTX = BX / WX, F = WTX / 16;          // fragments per wave
+  static constexpr int RB = BX * 2;                          // transposed: bytes per LDS row
+  static constexpr int CPR = BX / 8, RP = 64 / CPR;          // chunks per row, rows per load
+  static_assert(kPieces % NW == 0, "the same loads on every wave");
+  static_assert(TR ? (NW * RP) % 16 == 0 && BX % 128 == 0 : (NW * 8) % 16 == 0, "swizzle fixed per lane");
+
+  // global side
+  uint32_t voff, step;  // this lane's offset in its first piece, bytes between a wave's pieces
+  int chunk;            // K contiguous: the lane's 8-value chunk of a block
+  // LDS side
+  uint32_t off[TR ? F : 2];
+
+  __device__ __forceinline__ void init(int64_t ld, int wave, int lane, int wx) {
+    if constexpr (!TR) {
+      const int r0 = wave * 8 + (lane >> 3);
+      chunk = (lane & 7) ^ swz(r0);
+      voff = (uint32_t)r0 * (uint32_t)ld + (uint32_t)chunk * 16u;
+      step = (uint32_t)(NW * 8) * (uint32_t)ld;
+    } else {
+      const int k0 = wave * RP + lane / CPR;
+      const int pc = lane % CPR;
+      chunk = 0;
+      voff = (uint32_t)k0 * (uint32_t)ld + (uint32_t)(((((pc >> 1) ^ hsw(k0)) << 1) | (pc & 1)) * 16);
+      step = (uint32_t)(NW * RP) * (uint32_t)ld;
+    }
+    const int l16 = lane & 15, lq = lane >> 4;
+    if constexpr (!TR) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        off[s] = (uint32_t)((wx * WTX + l16) * 128 + (((4 * s + lq) ^ swz(l16)) << 4));
+    } else {
+      const int h = (l16 >> 2) | ((lq & 1) << 2);  // hsw of the rows this lane addresses
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+        off[i] = (uint32_t)((8 * lq + (l16 >> 2)) * RB + (((wx * F + i) ^ h) << 5) + ((l16 & 3) << 3));
+    }
+  }
+
+  // The loads of one block: `left` K values from the block's start to the end
+  // of the item (<= 0: nothing is read), `base` the operand at the block's start
+  // and the tile's first row, `rows` the tile's rows that exist (TR: stored
+  // columns from the tile's first one).  K contiguous: rows are padded with
+  // zeros to a multiple of 8 values where K is not one (dpre).
+  __device__ __forceinline__ void issue(const uint8_t* base, int64_t ld, int rows, int left, uint32_t lds,
+                                        int wave) const {
+    const int kv = min(left, 64);
+    const bool live = left > 0 && rows > 0;
+    const uint32_t bytes = !live ? 0u
+                           : TR  ? (uint32_t)(kv - 1) * (uint32_t)ld + 2u * rows
+                                 : (uint32_t)(min(rows, BX) - 1) * (uint32_t)ld + 2u * ((kv + 7) & ~7);
+    const v4i r = dma::resource(base, bytes);
+    const uint32_t v = TR || 8 * chunk < kv ? voff : kOut;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) dma::load16(lds + (wave + NW * q) * 1024, r, v + q * step);
+  }
+
+  // Fragment i of half s from the stage at LDS address `lds`.
+  __device__ __forceinline__ v8bf frag(uint32_t lds, int i, int s) const {
+    typedef __attribute__((address_space(3))) const v4i* lp;
+    typedef __attribute__((address_space(3))) v4s* lt;
+    if constexpr (!TR) {
+      return __builtin_bit_cast(v8bf, *(lp)(uintptr_t)(lds + off[s] + i * 2048));
+    } else {
+      const uint32_t a = lds + off[i] + s * 32 * RB;
+      const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lt)(uintptr_t)a));
+      const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lt)(uintptr_t)(a + 4 * RB)));
+      return __builtin_bit_cast(v8bf, v4i{lo[0], lo[1], hi[0], hi[1]});
+    }
+  }
+};
+
+template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB>
+__global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmParams p) {
+  constexpr int NW = WM * WN;
+  using OpA = Operand<BM, WM, NW, TA>;
+  using OpB = Operand<BN, WN, NW, TB>;
+  constexpr int FM = OpA::F, FN = OpB::F;
+  constexpr int STAGE = OpA::kBytes + OpB::kBytes;
+  constexpr int LOADS = OpA::kQ + OpB::kQ;  // per wave and block
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = (int)uniform(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l16 = lane & 15, lq = lane >> 4;
+  const uint32_t lds0 = dma::lds_addr(smem);
+  OpA oa;
+  OpB ob;
+  oa.init(p.lda, wave, lane, wm);
+  ob.init(p.ldb, wave, lane, wn);
+
+  // ---- work items: (tile, K split); each XCD walks a contiguous run ----
+  const int items = p.tiles_m * p.tiles_n * p.splits;
+  const int per_xcd = (items + 7) >> 3;
+  struct Item {
+    bool live;
+    int m0, n0, split, k0, k1;
+  };
+  auto decode = [&](int t) -> Item {
+    Item x{false, 0, 0, 0, 0, 0};
+    const int L = (t & 7) * per_xcd + (t >> 3);
+    if (t >= per_xcd * 8 || L >= items) return x;
+    const int tile = L / p.splits;
+    x.split = L - tile * p.splits;
+    const int group = kGroupM * p.tiles_n;
+    const int gid = tile / group;
+    const int gm = min(p.tiles_m - gid * kGroupM, kGroupM);
+    const int r = tile - gid * group;
+    x.m0 = (gid * kGroupM + r % gm) * BM;
+    x.n0 = (r / gm) * BN;
+    x.k0 = x.split * p.kchunk * 64;
+    x.k1 = min(p.k, x.k0 + p.kchunk * 64);
+    x.live = true;
+    return x;
+  };
+  // (an id that maps past the items is followed by live ones of other XCDs'
+  // runs: a workgroup's own ids t, t + grid, ... with grid a multiple of 8
+  // stay on one XCD's run and end together)
+  auto next = [&](int& t) {
+    Item x = decode(t);
+    while (!x.live && t < per_xcd * 8) {
+      t += gridDim.x;
+      x = decode(t);
+    }
+    t += gridDim.x;
+    return x;
+  };
+
+  // ---- the stream of K blocks over the workgroup's items ----
+  int lt = blockIdx.x;
+  Item li{};
+  const uint8_t *pa = nullptr, *pb = nullptr;
+  int left = 0;
+  auto enter = [&]() {
+    li = next(lt);
+    left = li.live ? li.k1 - li.k0 : 0;
+    pa = p.a + (TA ? (int64_t)li.k0 * p.lda + 2 * li.m0 : (int64_t)li.m0 * p.lda + 2 * (int64_t)li.k0);
+    pb = p.b + (TB ? (int64_t)li.k0 * p.ldb + 2 * li.n0 : (int64_t)li.n0 * p.ldb + 2 * (int64_t)li.k0);
+  };
+  auto issue = [&](int slot) {
+    const uint32_t st = uniform(lds0 + slot * STAGE);
+    oa.issue(pa, p.lda, (TA ? p.wa : p.m) - li.m0, left, st, wave);
+    ob.issue(pb, p.ldb, (TB ? p.wb : p.n) - li.n0, left, st + OpA::kBytes, wave);
+    left -= 64;
+    if (left <= 0) {
+      if (li.live) enter();
+    } else {
+      pa += TA ? 64 * p.lda : 128;
+      pb += TB ? 64 * p.ldb : 128;
+    }
+  };
+
+  int ct = blockIdx.x;
+  Item cur = next(ct);
+  if (!cur.live) return;
+  enter();
+#pragma unroll
+  for (int s = 0; s < S; ++s) issue(s);
+  dma::wait<(S - 1) * LOADS>();
+  dma::barrier();
+
+  int q = 0;  // ring slot of the current block
+  while (cur.live) {
+    const int nkb = (cur.k1 - cur.k0 + 63) >> 6;
+    v4f acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    v8bf fa[2][FM], fb[2][FN];
+    auto read = [&](int set, int slot, int s) {
+      const uint32_t st = lds0 + slot * STAGE;
+#pragma unroll
+      for (int i = 0; i < FN; ++i) fb[set][i] = ob.frag(st + OpA::kBytes, i, s);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) fa[set][j] = oa.frag(st, j, s);
+    };
+    auto multiply = [&](int set) {
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int i = 0; i < FN; ++i) acc[i][j] = mfma(fb[set][i], fa[set][j], acc[i][j]);
+    };
+    read(0, q, 0);
+#pragma unroll 1
+    for (int kb = 0; kb < nkb; ++kb) {
+      read(1, q, 1);
+      multiply(0);
+      // this wave has read the block's stage (the barrier waits for its LDS
+      // reads) and its share of the next block has landed
+      dma::wait<(S - 2) * LOADS>();
+      dma::barrier();
+      issue(q);
+      q = q + 1 == S ? 0 : q + 1;
+      if (kb + 1 < nkb) read(0, q, 0);
+      multiply(1);
+    }
+
+    // ---- epilogue ----
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      const int n = cur.n0 + wn * OpB::WTX + 16 * i + 4 * lq;
+      if (n >= p.n) continue;
+      const v4f bias = p.splits > 1 ? v4f{0.f, 0.f, 0.f, 0.f} : epi::bias4(p.epi, n, p.n);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        const int m = cur.m0 + wm * OpA::WTX + 16 * j + l16;
+        if (m >= p.m) continue;
+        if (p.splits > 1) {
+          float* w = p.ws + cur.split * p.ws_stride + (int64_t)m * p.n + n;
+          if (p.n % 4 == 0) {
+            *reinterpret_cast<v4f*>(w) = acc[i][j];
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (n + r < p.n) w[r] = acc[i][j][r];
+          }
+        } else {
+          epi::finish4(p.epi, m, n, p.n, acc[i][j] + bias);
+        }
+      }
+    }
+    cur = next(ct);
+  }
+  dma::wait<0>();  // no load outlives the workgroup
+}
+
+template <int TILE, bool TA, bool TB>
+hipError_t launch_tile(const GemmParams& p, int grid, hipStream_t stream) {
+  constexpr GemmTile t = kGemmTiles[TILE];
+  linear_gemm_kernel<t.bm, t.bn, t.wm, t.wn, t.stages, TA, TB><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <int TILE>
+hipError_t launch_layout(int layout, const GemmParams& p, int grid, hipStream_t stream) {
+  if (layout == kNT) return launch_tile<TILE, false, false>(p, grid, stream);
+  if (layout == kNN) return launch_tile<TILE, false, true>(p, grid, stream);
+  if constexpr (gemm_has(kTN, TILE)) return launch_tile<TILE, true, true>(p, grid, stream);
+  return hipErrorInvalidValue;
+}
+
+// ---- the activation's backward pass and the bias gradient ----
+// A workgroup takes 256 columns x kBiasRows rows: 32 lanes of 8 columns by 8
+// rows in flight; the column sums of its 8 row lanes meet in LDS.  Bound by
+// HBM: dc and pre read, dpre written, once.
+__global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
+  __shared__ float sum[8][256];
+  const int lx = threadIdx.x & 31, ly = threadIdx.x >> 5;
+  const int c = blockIdx.x * 256 + lx * 8;
+  const int r0 = blockIdx.y * kBiasRows;
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.f;
+  if (c < p.ldp) {
+#pragma unroll 2
+    for (int r = r0 + ly; r < min(p.m, r0 + kBiasRows); r += 8) {
+      float d[8], x[8];
+      const uint16_t* dc = p.dc + (int64_t)r * p.lddc + c;
+      const uint16_t* pr = p.pre ? p.pre + (int64_t)r * p.ldpre + c : nullptr;
+      if (p.vec && c + 7 < p.n) {
+        const uint4 v = *reinterpret_cast<const uint4*>(dc);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          d[2 * e] = epi::from_bf16(w[e] & 0xffffu);
+          d[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+        if (pr) {
+          const uint4 u = *reinterpret_cast<const uint4*>(pr);
+          const uint32_t y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[2 * e] = epi::from_bf16(y[e] & 0xffffu);
+            x[2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          d[e] = c + e < p.n ? epi::from_bf16(dc[e]) : 0.f;
+          x[e] = pr && c + e < p.n ? epi::from_bf16(pr[e]) : 0.f;
+        }
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (pr) d[e] *= act::grad(x[e], p.act);
+        if (c + e >= p.n) d[e] = 0.f;  // the padding columns
+        s[e] += d[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        o[e] = (uint32_t)epi::to_bf16(d[2 * e]) | ((uint32_t)epi::to_bf16(d[2 * e + 1]) << 16);
+      if (p.dpre) *reinterpret_cast<uint4*>(p.dpre + (int64_t)r * p.ldp + c) = uint4{o[0], o[1], o[2], o[3]};
+    }
+  }
+  if (p.partial) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[ly][lx * 8 + e] = s[e];
+    __syncthreads();
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col < p.n) {
+      float v = 0.f;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) v += sum[y][threadIdx.x];
+      p.partial[(int64_t)blockIdx.y * p.n + col] = v;
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void bias_sum_kernel(const float* partial, float* dbias, int chunks, int n) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= n) return;
+  float v = 0.f;
+  for (int k = 0; k < chunks; ++k) v += partial[(int64_t)k * n + c];
+  dbias[c] = v;
+}
+
+}  // namespace
+
+hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipStream_t stream) {
+  switch (tile) {
+    case 0: return launch_layout<0>(layout, p, grid, stream);
+    case 1: return launch_layout<1>(layout, p, grid, stream);
+    case 2: return launch_layout<2>(layout, p, grid, stream);
+    case 3: return launch_layout<3>(layout, p, grid, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_dact(const DactParams& p, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.ldp + 255) / 256), (unsigned)((p.m + kBiasRows - 1) / kBiasRows));
+  dact_kernel<<<grid, 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_bias_sum(const float* partial, float* dbias, int chunks, int n, hipStream_t stream) {
+  bias_sum_kernel<<<(n + 255) / 256, 256, 0, stream>>>(partial, dbias, chunks, n);
+  return hipGetLastError();
+}
+
+}  // namespace dg
