@@ -1,5 +1,5 @@
 // dg_dma.h -- loads from memory straight into LDS through buffer resources,
-// and the waits that go with them (device code of the BF16 tile kernel).
+// and the waits that go with them (device code of the linear layer's and the MoE layer's kernels).
 //
 // Lane i's 16 bytes land at LDS address lds + 16 i; bytes at or past the
 // resource's range read as zero and touch no memory.  Issued through inline
@@ -34,7 +34,20 @@ __device__ __forceinline__ void load16(uint32_t lds, v4i rsrc, uint32_t voff) {
   asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(voff), "s"(rsrc) : "memory", "m0");
 }
+// The same for data that is read once (nontemporal cache policy).
+__device__ __forceinline__ void load16_nt(uint32_t lds, v4i rsrc, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+               :: "s"(lds), "v"(voff), "s"(rsrc) : "memory", "m0");
+}
+// 4 bytes per lane, to lds + 4 i.
+__device__ __forceinline__ void load4(uint32_t lds, v4i rsrc, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(rsrc) : "memory", "m0");
+}
 #pragma clang diagnostic pop
+
+// This wave's LDS reads have returned (before their place is loaded anew).
+__device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // At most N vector-memory operations of this wave in flight.
 template <int N>

@@ -25,6 +25,7 @@
 
 #include "../../include/dg.h"
 #include "dg_act.h"
+#include "dg_kernel.h"
 #include "dg_stream.h"
 
 namespace dg {
@@ -32,8 +33,6 @@ namespace {
 
 using namespace stream;
 
-constexpr int kWaves = 8;
-constexpr int kThreads = kWaves * 64;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
@@ -57,15 +56,14 @@ struct MoeParams {
 
 // ---- routing tables in LDS -------------------------------------------------
 // The (token, expert) pairs of the call, p = token * k + j, sorted by expert;
-// a segment is a run of at most 16 NT pairs of one expert, the columns of the
-// MFMA tiles that share one pass over that expert's weights.
+// a segment is the run of one expert's pairs: the columns of the MFMA tiles
+// that share one pass over that expert's weights (at most one pair per token).
 struct Tables {
-  int id[kMaxPairs];            // expert of each pair, -1: none
-  float w[kMaxPairs];           // its weight
-  uint16_t pair[kMaxPairs];     // sorted position -> pair
-  int16_t sid[kMaxPairs];       // sorted position -> expert
-  uint16_t rank[kMaxPairs];     // sorted position -> how many pairs of the expert come before
-  uint16_t seg[kMaxPairs];      // segment -> its first sorted position
+  float w[kMaxPairs];             // weight of each pair
+  int16_t id[kMaxPairs];          // its expert, -1: none
+  uint16_t pair[kMaxPairs];       // sorted position -> pair
+  int16_t sid[kMaxPairs];         // sorted position -> expert
+  uint16_t seg[kMaxExperts + 1];  // segment -> its first sorted position; the end after the last
   int npair, nseg;
 };
 
@@ -98,7 +96,7 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
 // keys and a ballot for the first lane that holds it.
 __device__ __forceinline__ void route(const MoeParams& p, Tables& tb, int wave, int lane, bool publish) {
   constexpr int NI = kMaxExperts / 64;
-  for (int t = wave; t < p.t; t += kWaves) {
+  for (int t = wave; t < p.t; t += (int)(blockDim.x >> 6)) {
     float l[NI];
     uint32_t key[NI];
 #pragma unroll
@@ -154,7 +152,7 @@ __device__ __forceinline__ void route(const MoeParams& p, Tables& tb, int wave, 
       w /= sum_all;
     w *= p.scale;
     if (lane < p.top_k) {
-      tb.id[t * p.top_k + lane] = my_id;
+      tb.id[t * p.top_k + lane] = (int16_t)my_id;
       tb.w[t * p.top_k + lane] = w;
       if (publish) {
         p.ids[t * p.top_k + lane] = my_id;
@@ -167,20 +165,20 @@ __device__ __forceinline__ void route(const MoeParams& p, Tables& tb, int wave, 
 // Fills the tables.  ROUTE: from the logits (published by workgroup 0), else
 // from ids / weights: ids outside [0, E) drop out, a token's repeated expert
 // keeps one pair with the sum of its weights.
-template <int NT, bool ROUTE>
+template <bool ROUTE>
 __device__ __forceinline__ void build_tables(const MoeParams& p, Tables& tb) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6), nthreads = blockDim.x;
   const int np = p.t * p.top_k;
   if constexpr (ROUTE) {
     route(p, tb, wave, lane, blockIdx.x == 0);
   } else {
-    for (int q = tid; q < np; q += kThreads) {
+    for (int q = tid; q < np; q += nthreads) {
       const int id = p.ids[q];
-      tb.id[q] = id >= 0 && id < p.experts ? id : -1;
+      tb.id[q] = (int16_t)(id >= 0 && id < p.experts ? id : -1);
       tb.w[q] = p.weights[q];
     }
   }
-  for (int q = np + tid; q < kMaxPairs && q < np + 4; q += kThreads) tb.id[q] = -1;  // the scan reads fours
+  if (tid < 8 && np + tid < kMaxPairs) tb.id[np + tid] = -1;  // the scan reads eights
   if (tid == 0) tb.npair = 0;
   __syncthreads();
   if constexpr (!ROUTE) {
@@ -201,25 +199,22 @@ __device__ __forceinline__ void build_tables(const MoeParams& p, Tables& tb) {
   }
   // sorted position of pair q: the pairs of lower experts and the earlier
   // pairs of its own
-  for (int q = tid; q < np; q += kThreads) {
-    const uint32_t id = (uint32_t)tb.id[q];
-    int lower = 0, same = 0;
-    for (int o = 0; o < np; o += 4) {
+  for (int q = tid; q < np; q += nthreads) {
+    const int id = tb.id[q];
+    if (id < 0) continue;
+    int pos = 0;
+    for (int o = 0; o < np; o += 8) {
       const int4 v = *reinterpret_cast<const int4*>(&tb.id[o]);
-      const uint32_t u[4] = {(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
+      const int u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        lower += u[c] < id;
-        same += u[c] == id && o + c < q;
+      for (int c = 0; c < 8; ++c) {
+        const int other = c & 1 ? u[c >> 1] >> 16 : (int)(int16_t)u[c >> 1];
+        pos += other >= 0 && (other < id || (other == id && o + c < q));
       }
     }
-    if (id != 0xffffffffu) {
-      const int pos = lower + same;
-      tb.pair[pos] = (uint16_t)q;
-      tb.sid[pos] = (int16_t)id;
-      tb.rank[pos] = (uint16_t)same;
-      atomicAdd(&tb.npair, 1);
-    }
+    tb.pair[pos] = (uint16_t)q;
+    tb.sid[pos] = (int16_t)id;
+    atomicAdd(&tb.npair, 1);
   }
   __syncthreads();
   if (wave == 0) {
@@ -227,297 +222,254 @@ __device__ __forceinline__ void build_tables(const MoeParams& p, Tables& tb) {
     int base = 0;
     for (int c = 0; c < n; c += 64) {
       const int q = c + lane;
-      const bool first = q < n && tb.rank[q] % (16 * NT) == 0;
+      const bool first = q < n && (q == 0 || tb.sid[q] != tb.sid[q - 1]);
       const uint64_t m = __ballot(first);
       if (first) tb.seg[base + __builtin_popcountll(m & ((1ull << lane) - 1))] = (uint16_t)q;
       base += __builtin_popcountll(m);
     }
-    if (lane == 0) tb.nseg = base;
+    if (lane == 0) {
+      tb.seg[base] = (uint16_t)n;
+      tb.nseg = base;
+    }
   }
   __syncthreads();
 }
 
-// The pair in MFMA column l16 of tile t of the segment that starts at sorted
-// position q0, -1 if the column is empty.
-__device__ __forceinline__ int column_pair(const Tables& tb, int q0, int e, int t, int l16) {
-  const int q = q0 + 16 * t + l16;
-  const int qc = q < kMaxPairs ? q : kMaxPairs - 1;
-  return q < tb.npair && tb.sid[qc] == e ? (int)tb.pair[qc] : -1;
+// The pair in column c of the segment [q0, q1), -1 past its end.
+__device__ __forceinline__ int column_pair(const Tables& tb, int q0, int q1, int c) {
+  return q0 + c < q1 ? (int)tb.pair[q0 + c] : -1;
 }
 
 // ---- first kernel ----------------------------------------------------------
 // Work item: one segment x 16 hidden columns (16 gate and the 16 matching up
-// rows of its expert's w13).  The 8 waves of a workgroup take K blocks round
-// robin and meet in LDS once per item.  The workgroup walks its items as one
-// stream of units, D of them in flight, so the loads of the next item are
-// already out while an item's sums meet.
-template <bool FP8W, int NT, bool ROUTE, int D>
-__global__ __launch_bounds__(kThreads) void moe_up_kernel(const MoeParams p) {
-  constexpr int WL = FP8W ? 2 : 4;
-  constexpr int ES = FP8W ? 1 : 2;
-  __shared__ Tables tb;
-  __shared__ __attribute__((aligned(16))) v4f red[kWaves][2 * NT][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
-  const int l16 = lane & 15, lq = lane >> 4;
-  build_tables<NT, ROUTE>(p, tb);
+// rows of its expert's w13: the unit's groups A and B).  The waves of a
+// workgroup take K blocks of 128 round robin and meet in LDS once per item.  A
+// wave walks its items as one stream of units, so the loads of the next item
+// are already out while an item's sums meet.
+struct UpCursor {
+  Unit u;
+  const MoeParams* p;
+  const Tables* tb;
+  int item, items, slabs, grid, kb, nb, waves, wave;
+  int q0, q1;
 
-  const int nb = p.hid >> 7, n = (nb + kWaves - 1) / kWaves;
-  const int slabs = p.inter >> 4;
-  const int items = (int)uniform(tb.nseg) * slabs;
-  const int grid = gridDim.x;
-  const int mine = items > (int)blockIdx.x ? (items - (int)blockIdx.x + grid - 1) / grid : 0;
-  const int total = mine * n;
-  const uint32_t row = (uint32_t)p.hid * ES;  // bytes per weight row
-  const uint32_t xrow = (uint32_t)p.hid * 2;
-  const uint32_t woff = (uint32_t)l16 * row + 16u * lq;
-
-  v4i wg[D][WL], wu[D][WL], xs[D][NT][4];
-  float sg[D], su[D];
-
-  // load cursor: the item and its wave-local block
-  int li = blockIdx.x, lj = 0;
-  const uint8_t* gate = nullptr;
-  const float* sgate = nullptr;
-  uint32_t xoff[NT];
-  auto enter = [&]() {  // the cursor's item
-    const bool live = li < items;
-    const int s = live ? li / slabs : 0;
-    const int n0 = live ? (li - s * slabs) * 16 : 0;
-    const int q0 = live ? tb.seg[s] : 0;
-    const int e = (int)uniform(live ? tb.sid[q0] : 0);
-    gate = p.w13 + ((int64_t)e * 2 * p.inter + n0) * row;
-    if constexpr (FP8W) sgate = p.s13 + ((int64_t)e * 2 * (p.inter >> 7) + (n0 >> 7)) * nb;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int pr = live ? column_pair(tb, q0, e, t, l16) : -1;
-      xoff[t] = pr >= 0 ? (uint32_t)(pr / p.top_k) * xrow + (FP8W ? 32u : 16u) * lq : kOut;
-    }
-  };
-  auto load = [&](int d) {
-    const int kb = wave + kWaves * lj;
-    const bool live = li < items && kb < nb;
-    const uint32_t wbytes = live ? 15u * row + 128u * ES : 0u;
-    const auto rg = rsrc(gate + (int64_t)kb * 128 * ES, wbytes);
-    const auto ru = rsrc(gate + (int64_t)p.inter * row + (int64_t)kb * 128 * ES, wbytes);
-    const auto rx = rsrc(p.x + (int64_t)kb * 128, live ? (uint32_t)(p.t - 1) * xrow + 256u : 0u);
-#pragma unroll
-    for (int i = 0; i < WL; ++i) {
-      wg[d][i] = load16<kNt>(rg, woff + 64u * i);
-      wu[d][i] = load16<kNt>(ru, woff + 64u * i);
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        xs[d][t][i] = load16<0>(rx, xoff[t] + (FP8W ? 128u * (i >> 1) + 16u * (i & 1) : 64u * i));
-    if constexpr (FP8W) {
-      const auto rs = rsrc(sgate + kb, live ? 4u : 0u);
-      const auto rt = rsrc(sgate + (int64_t)(p.inter >> 7) * nb + kb, live ? 4u : 0u);
-      sg[d] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, 0, 0, 0));
-      su[d] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rt, 0, 0, 0));
-    }
-    if (++lj == n) {
-      lj = 0;
-      li += grid;
-      enter();
-    }
-  };
-
-  v4f ag[NT], au[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) ag[t] = au[t] = v4f{0.f, 0.f, 0.f, 0.f};
-  enter();
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(d);
-
-  int ci = blockIdx.x, cj = 0;
-  for (int c = 0; c < total; c += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (c + d >= total) break;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const v4f g = unit_product<FP8W>(wg[d], xs[d][t]);
-        const v4f u = unit_product<FP8W>(wu[d], xs[d][t]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          ag[t][r] = FP8W ? __builtin_fmaf(sg[d], g[r], ag[t][r]) : ag[t][r] + g[r];
-          au[t][r] = FP8W ? __builtin_fmaf(su[d], u[r], au[t][r]) : au[t][r] + u[r];
-        }
-      }
-      load(d);
-      if (++cj == n) {
-        cj = 0;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          red[wave][2 * t][lane] = ag[t];
-          red[wave][2 * t + 1][lane] = au[t];
-          ag[t] = au[t] = v4f{0.f, 0.f, 0.f, 0.f};
-        }
-        __syncthreads();
-        if (tid < 64 * NT) {
-          const int t = wave;  // one wave per tile
-          v4f g = red[0][2 * t][lane], u = red[0][2 * t + 1][lane];
-#pragma unroll
-          for (int w = 1; w < kWaves; ++w) {
-            g += red[w][2 * t][lane];
-            u += red[w][2 * t + 1][lane];
-          }
-          const int s = ci / slabs, n0 = (ci - s * slabs) * 16, q0 = tb.seg[s];
-          const int pr = column_pair(tb, q0, tb.sid[q0], t, l16);
-          if (pr >= 0) {
-            const float w = tb.w[pr];
-            v4f hv;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) hv[r] = w * (g[r] * act::sigmoid(g[r]) * u[r]);
-            *reinterpret_cast<uint2*>(p.h + (int64_t)pr * p.inter + n0 + 4 * lq) = pack4(hv);
-          }
-        }
-        __syncthreads();
-        ci += grid;
-      }
+  __device__ __forceinline__ void seek() {  // the item and K block the cursor stands on
+    u.live = item < items && wave < nb;
+    if (!u.live) return;
+    const int s = item / slabs, n0 = (item - s * slabs) * 16;
+    q0 = (int)uniform(tb->seg[s]);
+    q1 = (int)uniform(tb->seg[s + 1]);
+    const int e = (int)uniform(tb->sid[q0]);
+    u.tiles = (q1 - q0 + 15) >> 4;
+    u.wa = p->w13 + ((int64_t)e * 2 * p->inter + n0) * u.wrow;
+    u.wb = u.wa + (int64_t)p->inter * u.wrow;
+    if (p->s13) u.s = p->s13 + ((int64_t)e * 2 * (p->inter >> 7) + (n0 >> 7)) * nb;
+    place(0);
+  }
+  __device__ __forceinline__ void place(int from) {  // from K block `from` of the item to kb
+    const int d = kb - from;
+    const int wb = p->s13 ? 128 : 256;
+    u.wa += d * wb;
+    u.wb += d * wb;
+    u.s += d;
+    u.x = reinterpret_cast<const uint8_t*>(p->x + kb * 128);
+  }
+  __device__ __forceinline__ void next() {
+    const int from = kb;
+    kb += waves;
+    if (kb < nb) {
+      place(from);
+    } else {
+      kb = wave;
+      item += grid;
+      seek();
     }
   }
+  __device__ __forceinline__ uint32_t row(int t, int r) const {
+    const int pr = column_pair(*tb, q0, q1, 16 * t + r);
+    return pr >= 0 ? (uint32_t)(pr / p->top_k) * (uint32_t)p->hid * 2u : kOut;
+  }
+  __device__ __forceinline__ uint32_t scale(int) const { return kOut; }
+};
+
+template <int MODE, bool ROUTE, int W, int D>
+__global__ __launch_bounds__(W * 64) void moe_up_kernel(const MoeParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(MODE, W, D)];
+  __shared__ __attribute__((aligned(16))) Tables tb;
+  __shared__ __attribute__((aligned(16))) v4f red[W][2][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+  build_tables<ROUTE>(p, tb);
+
+  UpCursor c{};
+  c.p = &p;
+  c.tb = &tb;
+  c.slabs = p.inter >> 4;
+  c.items = (int)uniform(tb.nseg) * c.slabs;
+  c.grid = gridDim.x;
+  c.item = blockIdx.x;
+  c.nb = p.hid >> 7;
+  c.waves = W;
+  c.wave = c.kb = wave;
+  c.u.ra = c.u.rb = 16;
+  c.u.wrow = (uint32_t)p.hid * (MODE == kBf16 ? 2 : 1);
+  c.u.kbytes = MODE == kBf16 ? 256 : 128;
+  c.u.xbytes = 256;
+  c.u.xrange = (uint32_t)(p.t - 1) * (uint32_t)p.hid * 2u + 256u;
+  c.u.s = p.s13;
+  c.u.so[1] = (uint32_t)(p.inter >> 7) * c.nb * 4u;
+  c.u.srange = c.u.so[1] + 4u;
+  c.seek();
+  const int mine = c.nb > wave ? (c.nb - wave + W - 1) / W : 0;  // units of an item on this wave
+  Pipe<MODE, D, UpCursor> pipe;
+  pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
+
+  for (int item = blockIdx.x; item < c.items; item += c.grid) {
+    const int s = item / c.slabs, n0 = (item - s * c.slabs) * 16;
+    const int q0 = (int)uniform(tb.seg[s]), q1 = (int)uniform(tb.seg[s + 1]);
+    const int tiles = (q1 - q0 + 15) >> 4;
+    v4f g[kMaxTiles], u[kMaxTiles];
+#pragma unroll
+    for (int t = 0; t < kMaxTiles; ++t) g[t] = u[t] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < mine; ++k) pipe.template unit<kMaxTiles>(tiles, g, u);
+#pragma unroll
+    for (int t = 0; t < kMaxTiles; ++t) {
+      if (t >= tiles) break;
+      red[wave][0][lane] = g[t];
+      red[wave][1][lane] = u[t];
+      dma::barrier();
+      if (wave == t % W) {
+        v4f a = red[0][0][lane], b = red[0][1][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+          a += red[w][0][lane];
+          b += red[w][1][lane];
+        }
+        const int pr = column_pair(tb, q0, q1, 16 * t + l16);
+        if (pr >= 0) {
+          const float w = tb.w[pr];
+          v4f hv;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) hv[r] = w * (a[r] * act::sigmoid(a[r]) * b[r]);
+          *reinterpret_cast<uint2*>(p.h + (int64_t)pr * p.inter + n0 + 4 * lq) = pack4(hv);
+        }
+      }
+      dma::barrier();
+    }
+  }
+  dma::wait<0>();  // no load outlives the workgroup
 }
 
 // ---- second kernel ---------------------------------------------------------
-// A workgroup owns 16 R rows of every chosen expert's w2 (16 R output
-// columns) and walks (segment, K block) units, the waves round robin.  A
-// wave's sums of a segment go to its own LDS rows [token][16 R] when it
-// leaves the segment, and the waves' rows meet at the end.
-template <bool FP8W, int NT, int R, int D>
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeParams p) {
-  constexpr int WL = FP8W ? 2 : 4;
-  constexpr int ES = FP8W ? 1 : 2;
-  constexpr int YS = 16 * R + 4;  // floats per token in LDS
-  __shared__ Tables tb;
-  extern __shared__ __attribute__((aligned(16))) float yacc[];  // [waves][T][YS]
+// A workgroup owns 32 rows of every chosen expert's w2 (32 output columns; the
+// unit's groups are 16 rows each) and walks (segment, K block) units, the
+// waves round robin.  A wave's sums of a segment go to its own LDS rows
+// [token][32] when it leaves the segment, and the waves' rows meet at the end.
+struct DownCursor {
+  Unit u;
+  const MoeParams* p;
+  const Tables* tb;
+  int seg, nseg, kb, nb, waves, h0;
+  int q0, q1;
+
+  __device__ __forceinline__ void seek() {
+    u.live = seg < nseg;
+    if (!u.live) return;
+    q0 = (int)uniform(tb->seg[seg]);
+    q1 = (int)uniform(tb->seg[seg + 1]);
+    const int e = (int)uniform(tb->sid[q0]);
+    const int wb = p->s2 ? 128 : 256;
+    u.tiles = (q1 - q0 + 15) >> 4;
+    u.wa = p->w2 + ((int64_t)e * p->hid + h0) * u.wrow + kb * wb;
+    u.wb = u.wa + 16 * (int64_t)u.wrow;
+    if (p->s2) u.s = p->s2 + ((int64_t)e * (p->hid >> 7) + (h0 >> 7)) * nb + kb;
+    u.x = reinterpret_cast<const uint8_t*>(p->h + kb * 128);
+  }
+  __device__ __forceinline__ void next() {
+    kb += waves;
+    while (kb >= nb) {
+      kb -= nb;
+      ++seg;
+    }
+    seek();
+  }
+  __device__ __forceinline__ uint32_t row(int t, int r) const {
+    const int pr = column_pair(*tb, q0, q1, 16 * t + r);
+    return pr >= 0 ? (uint32_t)pr * (uint32_t)p->inter * 2u : kOut;
+  }
+  __device__ __forceinline__ uint32_t scale(int) const { return kOut; }
+};
+
+constexpr int kYStride = 36;  // floats per token in LDS: 32 and a pad against bank conflicts
+
+// TMAX: the most tokens of the call (LDS rows).
+template <int MODE, int TMAX, int W, int D>
+__global__ __launch_bounds__(W * 64) void moe_down_kernel(const MoeParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(MODE, W, D)];
+  __shared__ __attribute__((aligned(16))) Tables tb;
+  __shared__ __attribute__((aligned(16))) float yacc[W][TMAX][kYStride];
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  for (int i = tid; i < kWaves * p.t * YS / 4; i += kThreads) reinterpret_cast<v4f*>(yacc)[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  build_tables<NT, false>(p, tb);
-  float* yw = yacc + wave * p.t * YS;
+  for (int i = tid; i < W * TMAX * kYStride / 4; i += W * 64)
+    reinterpret_cast<v4f*>(&yacc[0][0][0])[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  build_tables<false>(p, tb);
 
-  const int nb = p.inter >> 7;
-  const int nseg = (int)uniform(tb.nseg);
-  const int h0 = blockIdx.x * 16 * R;
-  const int units = nseg * nb;
-  const int total = units > wave ? (units - wave + kWaves - 1) / kWaves : 0;
-  const uint32_t row = (uint32_t)p.inter * ES;
-  const uint32_t hrow = (uint32_t)p.inter * 2;
-  const uint32_t woff = (uint32_t)l16 * row + 16u * lq;
-  const uint32_t hbytes = (uint32_t)(p.t * p.top_k - 1) * hrow + 256u;
+  DownCursor c{};
+  c.p = &p;
+  c.tb = &tb;
+  c.nseg = (int)uniform(tb.nseg);
+  c.nb = p.inter >> 7;
+  c.waves = W;
+  c.h0 = blockIdx.x * 32;
+  c.seg = wave / c.nb;
+  c.kb = wave - c.seg * c.nb;
+  c.u.ra = c.u.rb = 16;
+  c.u.wrow = (uint32_t)p.inter * (MODE == kBf16 ? 2 : 1);
+  c.u.kbytes = MODE == kBf16 ? 256 : 128;
+  c.u.xbytes = 256;
+  c.u.xrange = (uint32_t)(p.t * p.top_k - 1) * (uint32_t)p.inter * 2u + 256u;
+  c.u.s = p.s2;
+  c.u.srange = 4;
+  c.seek();
+  Pipe<MODE, D, DownCursor> pipe;
+  pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
 
-  v4i ws[D][R][WL], xs[D][NT][4];
-  float sc[D];
-  int seg_of[D], tok[D][NT];
-
-  int ls = wave / nb, lb = wave - ls * nb;  // load cursor: segment and K block
-  const uint8_t* wbase = nullptr;
-  const float* sbase = nullptr;
-  uint32_t hoff[NT];
-  int ltok[NT];
-  auto enter = [&]() {
-    const bool live = ls < nseg;
-    const int q0 = live ? tb.seg[ls] : 0;
-    const int e = (int)uniform(live ? tb.sid[q0] : 0);
-    wbase = p.w2 + ((int64_t)e * p.hid + h0) * row;
-    if constexpr (FP8W) sbase = p.s2 + ((int64_t)e * (p.hid >> 7) + (h0 >> 7)) * nb;
+  v4f a[kMaxTiles], b[kMaxTiles];
+  auto zero = [&]() {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int pr = live ? column_pair(tb, q0, e, t, l16) : -1;
-      ltok[t] = pr >= 0 ? pr / p.top_k : -1;
-      hoff[t] = pr >= 0 ? (uint32_t)pr * hrow + (FP8W ? 32u : 16u) * lq : kOut;
-    }
+    for (int t = 0; t < kMaxTiles; ++t) a[t] = b[t] = v4f{0.f, 0.f, 0.f, 0.f};
   };
-  auto load = [&](int d) {
-    const bool live = ls < nseg;
-    const auto rw = rsrc(wbase + (int64_t)lb * 128 * ES, live ? (16u * R - 1u) * row + 128u * ES : 0u);
-    const auto rh = rsrc(p.h + (int64_t)lb * 128, live ? hbytes : 0u);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int i = 0; i < WL; ++i) ws[d][r][i] = load16<kNt>(rw, woff + 16u * r * row + 64u * i);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        xs[d][t][i] = load16<0>(rh, hoff[t] + (FP8W ? 128u * (i >> 1) + 16u * (i & 1) : 64u * i));
-      tok[d][t] = ltok[t];
-    }
-    if constexpr (FP8W) {
-      const auto rs = rsrc(sbase + lb, live ? 4u : 0u);
-      sc[d] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, 0, 0, 0));
-    }
-    seg_of[d] = ls;
-    lb += kWaves;
-    if (lb >= nb) {
-      while (lb >= nb) {
-        lb -= nb;
-        ++ls;
-      }
-      enter();
-    }
-  };
-
-  v4f acc[R][NT];
-  int cur = -1, ctok[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    ctok[t] = -1;
-#pragma unroll
-    for (int r = 0; r < R; ++r) acc[r][t] = v4f{0.f, 0.f, 0.f, 0.f};
-  }
   // (a column's lanes add to its own token's row: an empty column, whose
   // products may be NaN if a weight is, adds nothing)
-  auto flush = [&]() {
+  auto flush = [&](int tiles) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      if (ctok[t] >= 0) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          v4f* a = reinterpret_cast<v4f*>(yw + ctok[t] * YS + 16 * r + 4 * lq);
-          *a = *a + acc[r][t];
-        }
+    for (int t = 0; t < kMaxTiles; ++t) {
+      if (t >= tiles) break;
+      const int pr = column_pair(tb, c.q0, c.q1, 16 * t + l16);
+      if (pr >= 0) {
+        v4f* y = reinterpret_cast<v4f*>(&yacc[wave][pr / p.top_k][4 * lq]);
+        y[0] += a[t];
+        y[4] += b[t];
       }
-  };
-  enter();
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(d);
-  for (int c = 0; c < total; c += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      if (c + d >= total) break;
-      if (seg_of[d] != cur) {
-        flush();
-        cur = seg_of[d];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          ctok[t] = tok[d][t];
-#pragma unroll
-          for (int r = 0; r < R; ++r) acc[r][t] = v4f{0.f, 0.f, 0.f, 0.f};
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const v4f v = unit_product<FP8W>(ws[d][r], xs[d][t]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[r][t][e] = FP8W ? __builtin_fmaf(sc[d], v[e], acc[r][t][e]) : acc[r][t][e] + v[e];
-        }
-      load(d);
     }
+  };
+  zero();
+  while (c.u.live) {
+    pipe.template unit<kMaxTiles>(c.u.tiles, a, b);
+    if (c.kb + W >= c.nb) {  // the wave's last unit of the segment
+      flush(c.u.tiles);
+      zero();
+    }
+    c.next();
   }
-  flush();
+  dma::wait<0>();  // no load outlives the workgroup
   __syncthreads();
-  for (int i = tid; i < p.t * 4 * R; i += kThreads) {
-    const int t = i / (4 * R), c = 4 * (i - t * 4 * R);
-    v4f s = *reinterpret_cast<const v4f*>(yacc + t * YS + c);
+  for (int i = tid; i < p.t * 8; i += W * 64) {
+    const int t = i >> 3, h = 4 * (i & 7);
+    v4f s = *reinterpret_cast<const v4f*>(&yacc[0][t][h]);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += *reinterpret_cast<const v4f*>(yacc + (w * p.t + t) * YS + c);
-    const int64_t o = (int64_t)t * p.hid + h0 + c;
+    for (int w = 1; w < W; ++w) s += *reinterpret_cast<const v4f*>(&yacc[w][t][h]);
+    const int64_t o = (int64_t)t * p.hid + c.h0 + h;
     if (p.residual) {
       const uint2 v = *reinterpret_cast<const uint2*>(p.residual + o);
       s += v4f{from_bf16((uint16_t)v.x), from_bf16((uint16_t)(v.x >> 16)), from_bf16((uint16_t)v.y),
@@ -529,23 +481,23 @@ __global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeParams p) {
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-template <bool FP8W, int NT>
-hipError_t launch_moe(const MoeParams& p, hipStream_t stream) {
-  constexpr int D = FP8W ? (NT == 1 ? 4 : 2) : 2;
-  constexpr int R = 1;
-  // at most min(E, pairs) experts are chosen; a segment more per full 16 NT pairs
+template <int MODE>
+hipError_t launch_moe(const MoeParams& p, int cus, hipStream_t stream) {
+  // at most min(E, pairs) experts are chosen; one workgroup per CU (LDS)
   const long pairs = (long)p.t * p.top_k;
-  const long segs = (pairs < p.experts ? pairs : p.experts) + pairs / (16 * NT);
-  const long items = segs * (p.inter / 16);
-  const int grid = (int)(items < 512 ? items : 512);
+  const long items = (pairs < p.experts ? pairs : p.experts) * (p.inter / 16);
+  const int grid = (int)(items < cus ? items : cus);
+  constexpr int W = 8, D = 4;
   if (p.logits)
-    moe_up_kernel<FP8W, NT, true, D><<<grid, kThreads, 0, stream>>>(p);
+    moe_up_kernel<MODE, true, W, D><<<grid, W * 64, 0, stream>>>(p);
   else
-    moe_up_kernel<FP8W, NT, false, D><<<grid, kThreads, 0, stream>>>(p);
+    moe_up_kernel<MODE, false, W, D><<<grid, W * 64, 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const size_t lds = (size_t)kWaves * p.t * (16 * R + 4) * sizeof(float);
-  moe_down_kernel<FP8W, NT, R, D><<<p.hid / (16 * R), kThreads, lds, stream>>>(p);
+  if (p.t <= 16)
+    moe_down_kernel<MODE, 16, 8, 4><<<p.hid / 32, 8 * 64, 0, stream>>>(p);
+  else
+    moe_down_kernel<MODE, kMaxTokens, 4, 6><<<p.hid / 32, 4 * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -586,11 +538,9 @@ dg_status moe(bool fp8, const void* x, const float* logits, int32_t* ids, float*
   p.renormalize = renormalize;
   p.scale = scale;
   (void)hipGetLastError();  // clear a stale error from unrelated work
-  hipError_t e;
-  if (tokens <= 16)
-    e = fp8 ? launch_moe<true, 1>(p, stream) : launch_moe<false, 1>(p, stream);
-  else
-    e = fp8 ? launch_moe<true, 2>(p, stream) : launch_moe<false, 2>(p, stream);
+  const int cus = compute_units();
+  if (cus <= 0) return DG_ERROR_LAUNCH;
+  const hipError_t e = fp8 ? launch_moe<kW8A16>(p, cus, stream) : launch_moe<kBf16>(p, cus, stream);
   return e == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 

@@ -1,16 +1,30 @@
-// dg_stream.h -- device helpers of the weight-streaming kernels (few rows
-// against a large weight matrix): wave-uniform buffer resources, streaming
-// loads into registers, and the operand fragments of one "unit".
+// dg_stream.h -- the weight-streaming pipeline of the kernels that multiply
+// few rows by large weights (the linear layer for few rows, the few-token MoE
+// layer), all bound by reading the weights once.
 //
-// A unit is 16 weight rows x 128 values along K, multiplied by up to 16
-// activation rows (one MFMA tile).  Lane l holds bytes [64 i + 16 (l / 16),
-// + 16) of weight row l % 16 and the same k of activation row l % 16: which k
-// a lane holds does not matter to the product as long as both operands agree,
-// and this assignment makes every load 16 bytes per lane.
+// A wave works alone on a stream of units.  A unit is 256 bytes of K (bf16
+// operands: 128 values; fp8 by fp8: 256) or, with fp8 weights and bf16
+// activations, 128 values of 32 weight rows -- two groups A and B of 16 rows --
+// and up to 4 tiles of 16 activation rows.  The wave has a private ring of D
+// entries in LDS, filled by loads straight to LDS and drained in order, so no
+// barrier separates loads from use: an entry is complete when at most the loads
+// of the D - 1 younger entries are in flight.  Every entry has the same number
+// of loads:
+//   weight entry: one 128-byte line of K of each group's 16 rows (4 KB);
+//   activation entry: two lines of K of one tile's 16 rows (4 KB);
+//   with scales, a 4-byte load of them in either (the lanes that have one).
+// Each load instruction covers 8 rows x one whole 128-byte line.  Loading the
+// same bytes in the MFMA's own lane order (16 rows x 64 bytes, straight to
+// registers) runs at 30 GB/s per CU from the L2 instead of 74 and streams HBM at
+// 5.7 instead of 7.0 TB/s: sixteen half lines per 16 lanes keep the address path
+// busy four times as long.  In LDS the 16-byte chunk c of row r sits at c ^ swz(r)
+// (applied on the global side), so the fragment reads meet no bank twice.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "dg_dma.h"
 
 namespace dg {
 namespace stream {
@@ -22,21 +36,10 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kOut = 0x80000000u;  // a lane offset past every resource's range: reads zero, touches no memory
-constexpr int kNt = 2;                  // cache policy: nontemporal (data read once)
+constexpr int kMaxTiles = 4;
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// Raw buffer resource over [base, base + bytes); bytes must be wave-uniform.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, uint32_t bytes) {
-  const uint64_t b = (uint64_t)base;
-  const uint64_t u = (uint64_t)uniform((uint32_t)b) | ((uint64_t)uniform((uint32_t)(b >> 32)) << 32);
-  return __builtin_amdgcn_make_buffer_rsrc((void*)u, (short)0, (int)uniform(bytes), 0x00020000);
-}
-
-template <int AUX>
-__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, AUX));
-}
+__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
 // 8 fp8 (e4m3) bytes as 8 bf16 values (exact: every e4m3 value is a bf16 value).
 __device__ __forceinline__ v8bf fp8_to_bf16(int lo, int hi) {
@@ -47,27 +50,14 @@ __device__ __forceinline__ v8bf fp8_to_bf16(int lo, int hi) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ v4f mfma_bf16(const v8bf& w, const v8bf& x, const v4f& acc) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, acc, 0, 0, 0);
+__device__ __forceinline__ v4f mfma_bf16(const v4i& w, const v4i& x, const v4f& acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, x), acc, 0, 0,
+                                                 0);
 }
-
-// The product of one unit with one activation tile, from a zero accumulator.
-// Weights in fp8: w[0..1], 16 values each; in bf16: w[0..3], 8 values each.
-// x[0..3]: 8 bf16 values each.
-template <bool FP8W>
-__device__ __forceinline__ v4f unit_product(const v4i* w, const v4i* x) {
-  v4f p = v4f{0.f, 0.f, 0.f, 0.f};
-  if constexpr (FP8W) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      p = mfma_bf16(fp8_to_bf16(w[i][0], w[i][1]), __builtin_bit_cast(v8bf, x[2 * i]), p);
-      p = mfma_bf16(fp8_to_bf16(w[i][2], w[i][3]), __builtin_bit_cast(v8bf, x[2 * i + 1]), p);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p = mfma_bf16(__builtin_bit_cast(v8bf, w[i]), __builtin_bit_cast(v8bf, x[i]), p);
-  }
-  return p;
+__device__ __forceinline__ v4f mfma_fp8(const v4i& w0, const v4i& w1, const v4i& x0, const v4i& x1) {
+  const v8i w = v8i{w0[0], w0[1], w0[2], w0[3], w1[0], w1[1], w1[2], w1[3]};
+  const v8i x = v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
 __device__ __forceinline__ uint16_t to_bf16(float x) {
@@ -79,6 +69,194 @@ __device__ __forceinline__ uint2 pack4(const v4f& v) {
   return uint2{(uint32_t)to_bf16(v[0]) | ((uint32_t)to_bf16(v[1]) << 16),
                (uint32_t)to_bf16(v[2]) | ((uint32_t)to_bf16(v[3]) << 16)};
 }
+
+// Operand types: bf16 by bf16; fp8 weights with bf16 activations; fp8 by fp8.
+enum Mode : int { kBf16 = 0, kW8A16 = 1, kFp8 = 2 };
+
+constexpr int entry_bytes(int mode) { return 4096 + (mode == kBf16 ? 0 : mode == kW8A16 ? 16 : 128); }
+constexpr int ring_bytes(int mode, int waves, int depth) { return waves * depth * entry_bytes(mode); }
+
+// The unit a cursor stands on, as wave-uniform values; Cursor adds
+//   uint32_t row(int tile, int r): this lane's byte offset of activation row r
+//     of a tile from `x`, or kOut;
+//   uint32_t scale(int tile): fp8 by fp8: the lane's byte offset into `xs`;
+//   void next(): the following unit (or !live).
+struct Unit {
+  bool live;
+  int tiles;            // activation tiles
+  const uint8_t* wa;    // group A's first row at the unit's K
+  const uint8_t* wb;
+  int ra, rb;           // rows of A and B that exist
+  uint32_t wrow;        // bytes between weight rows
+  const uint8_t* x;     // the activations at the unit's K
+  uint32_t xrange;      // bytes from x to the end of the last activation row's unit
+  int kbytes;           // bytes of K left in a weight row from here (lines past them read nothing)
+  int xbytes;           // the same of an activation row
+  const float* s;       // scales: group g's for the first line of K at byte so[g]; kFp8: the second line's after it
+  uint32_t so[2], srange;
+  const float* xs;      // kFp8: activation scales at the unit's K
+  uint32_t xsrange;
+};
+
+template <int MODE, int D, class Cursor>
+struct Pipe {
+  static constexpr int kEntry = entry_bytes(MODE);
+  static constexpr int kLoads = MODE == kBf16 ? 4 : 5;
+  static constexpr int WE = MODE == kW8A16 ? 1 : 2;  // weight entries (lines of K) per unit
+  static_assert((D - 1) * kLoads < 64, "vmcnt range");
+
+  uint32_t ring;       // LDS address
+  Cursor ic;           // the unit being loaded
+  int phase = 0;       // its next entry
+  int islot = 0, cslot = 0;
+  int lane, lrow, chunk;  // the lane's row (of 8) and chunk in a load
+  uint32_t o[4];       // LDS offsets of chunks lq, lq + 4, 2 lq, 2 lq + 1 of row l16
+
+  __device__ __forceinline__ void init(uint32_t lds, const Cursor& c, int lane_) {
+    ring = lds;
+    ic = c;
+    lane = lane_;
+    lrow = lane >> 3;
+    chunk = lane & 7;
+    const int l16 = lane & 15, lq = lane >> 4, s = swz(l16);
+    o[0] = (uint32_t)(l16 * 128 + ((lq ^ s) << 4));
+    o[1] = (uint32_t)(l16 * 128 + (((lq + 4) ^ s) << 4));
+    o[2] = (uint32_t)(l16 * 128 + (((2 * lq) ^ s) << 4));
+    o[3] = (uint32_t)(l16 * 128 + (((2 * lq + 1) ^ s) << 4));
+#pragma unroll
+    for (int d = 0; d < D; ++d) issue();
+  }
+
+  // The loads of the next entry, into the ring's next slot.
+  __device__ __forceinline__ void issue() {
+    const uint32_t lds = uniform(ring + islot * kEntry);
+    islot = islot + 1 == D ? 0 : islot + 1;
+    const Unit& u = ic.u;
+    if (phase < WE || !u.live) {
+      // one line of K of 16 rows of A and 16 of B
+      const int koff = u.live ? 128 * phase : 0;
+      const int left = u.live ? u.kbytes - koff : 0;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int rows = g ? u.rb : u.ra;
+        const dma::v4i r = dma::resource((g ? u.wb : u.wa) + koff,
+                                         left > 0 && rows > 0 ? (uint32_t)(rows - 1) * u.wrow + min(left, 128) : 0u);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c = chunk ^ swz(8 * j + lrow);
+          dma::load16_nt(lds + (2 * g + j) * 1024, r, 16 * c < left ? (uint32_t)(8 * j + lrow) * u.wrow + 16u * c : kOut);
+        }
+      }
+      if constexpr (MODE != kBf16) {
+        // lane 0: A's scale of this line, lane 1: B's
+        const uint32_t so = (lane ? u.so[1] : u.so[0]) + (MODE == kFp8 ? 4u * phase : 0u);
+        const dma::v4i r = dma::resource(u.s, left > 0 ? u.srange : 0u);
+        if (lane < 2) dma::load4(lds + 4096, r, so);
+      }
+    } else {
+      const int t = phase - WE;
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        const dma::v4i r = dma::resource(u.x + 128 * l, u.xrange > 128u * l ? u.xrange - 128u * l : 0u);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c = chunk ^ swz(8 * j + lrow);
+          const uint32_t off = ic.row(t, 8 * j + lrow);
+          dma::load16(lds + (2 * l + j) * 1024, r, 128 * l + 16 * c < u.xbytes ? off + 16u * c : kOut);
+        }
+      }
+      if constexpr (MODE != kBf16) {
+        if constexpr (MODE == kFp8) {
+          const dma::v4i r = dma::resource(u.xs, u.xsrange);
+          const uint32_t so = ic.scale(t);
+          if (lane < 32) dma::load4(lds + 4096, r, so);
+        } else {
+          const dma::v4i r = dma::resource(u.x, 0u);  // none: reads nothing
+          if (lane < 2) dma::load4(lds + 4096, r, 0u);
+        }
+      }
+    }
+    if (u.live && ++phase == WE + u.tiles) {
+      phase = 0;
+      ic.next();
+    }
+  }
+
+  typedef __attribute__((address_space(3))) const v4i* lv;
+  typedef __attribute__((address_space(3))) const float* lf;
+
+  __device__ __forceinline__ uint32_t arrive() {
+    const uint32_t lds = ring + cslot * kEntry;
+    cslot = cslot + 1 == D ? 0 : cslot + 1;
+    dma::wait<(D - 1) * kLoads>();
+    return lds;
+  }
+  // The entry's LDS reads are done: its slot is loaded anew.
+  __device__ __forceinline__ void release() {
+    dma::lds_done();
+    issue();
+  }
+
+  // One unit of `tiles` tiles into the sums of A and B (tile t's lanes: column
+  // l16, rows 4 lq .. 4 lq + 3 of the group).
+  template <int NT>
+  __device__ __forceinline__ void unit(int tiles, v4f* a, v4f* b) {
+    v4i w[2][WE][2];  // [group][line][chunk lq, lq + 4]
+    float s[2][WE];
+#pragma unroll
+    for (int e = 0; e < WE; ++e) {
+      const uint32_t lds = arrive();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[g][e][j] = *(lv)(uintptr_t)(lds + 2048 * g + o[j]);
+        s[g][e] = MODE != kBf16 ? *(lf)(uintptr_t)(lds + 4096 + 4 * g) : 1.f;
+      }
+      release();
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t >= tiles) break;
+      const uint32_t lds = arrive();
+      v4i x[2][2];
+      float xs[2];
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) x[l][j] = *(lv)(uintptr_t)(lds + 2048 * l + o[(MODE == kW8A16 ? 2 : 0) + j]);
+        xs[l] = MODE == kFp8 ? *(lf)(uintptr_t)(lds + 4096 + 4 * (16 * l + (lane & 15))) : 1.f;
+      }
+      release();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        v4f& acc = g ? b[t] : a[t];
+        if constexpr (MODE == kBf16) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc = mfma_bf16(w[g][e][j], x[e][j], acc);
+        } else if constexpr (MODE == kW8A16) {
+          v4f p = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            p = mfma_bf16(__builtin_bit_cast(v4i, fp8_to_bf16(w[g][0][j][0], w[g][0][j][1])), x[j][0], p);
+            p = mfma_bf16(__builtin_bit_cast(v4i, fp8_to_bf16(w[g][0][j][2], w[g][0][j][3])), x[j][1], p);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s[g][0], p[r], acc[r]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const v4f p = mfma_fp8(w[g][e][0], w[g][e][1], x[e][0], x[e][1]);
+            const float f = s[g][e] * xs[e];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(f, p[r], acc[r]);
+          }
+        }
+      }
+    }
+  }
+};
 
 }  // namespace stream
 }  // namespace dg
