@@ -55,31 +55,22 @@ struct MoeParams {
 };
 
 // ---- routing tables in LDS -------------------------------------------------
-// The (token, expert) pairs of the call, p = token * k + j, sorted by expert;
-// a segment is the run of one expert's pairs: the columns of the MFMA tiles
-// that share one pass over that expert's weights (at most one pair per token).
+// The (token, expert) pairs of the call, p = token * k + j, sorted by expert
+// and token; a segment is the run of one expert's pairs: the columns of the MFMA
+// tiles that share one pass over that expert's weights (at most one pair per
+// token).
+template <int TMAX>               // the most tokens of the call
 struct Tables {
-  float w[kMaxPairs];             // weight of each pair
-  int16_t id[kMaxPairs];          // its expert, -1: none
-  uint16_t pair[kMaxPairs];       // sorted position -> pair
-  int16_t sid[kMaxPairs];         // sorted position -> expert
-  uint16_t seg[kMaxExperts + 1];  // segment -> its first sorted position; the end after the last
-  int npair, nseg;
+  uint64_t tokens[kMaxExperts];   // bit t: token t has the expert
+  float w[TMAX * kMaxTopK];       // weight of each pair
+  int16_t id[TMAX * kMaxTopK];    // its expert, -1: none
+  uint16_t pair[TMAX * kMaxTopK]; // sorted position -> pair
+  uint16_t base[kMaxExperts];     // expert -> its first sorted position
+  uint16_t seg[kMaxExperts + 2];  // segment -> its first sorted position; the end after the last
+  int16_t sid[kMaxExperts];       // segment -> expert
+  int chunk_pairs[kMaxExperts / 64], chunk_segs[kMaxExperts / 64];
+  int nseg, repeated;
 };
-
-// Maximum over the wave, in every lane's scalar (DPP row shifts, then the two
-// row broadcasts; 0 is the identity).
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#define DG_DPP_MAX(ctrl) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xf, 0xf, false))
-  DG_DPP_MAX(0x111);
-  DG_DPP_MAX(0x112);
-  DG_DPP_MAX(0x114);
-  DG_DPP_MAX(0x118);
-  DG_DPP_MAX(0x142);
-  DG_DPP_MAX(0x143);
-#undef DG_DPP_MAX
-  return __builtin_amdgcn_readlane(v, 63);
-}
 
 // Order-preserving key of a logit: larger float, larger key; NaN above
 // everything (it reaches the token's output, as it would through a sort);
@@ -90,73 +81,96 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
   if (b == 0xff800000u) return 0;
   return (b >> 31) ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float(k == 0xffffffffu ? 0x7fc00000u : (k >> 31) ? k ^ 0x80000000u : ~k);
+}
 
-// Top-k of every token's logits, ties to the lowest expert: one wave per
-// token, the logits in registers; each round is a maximum over the wave's
-// keys and a ballot for the first lane that holds it.
-__device__ __forceinline__ void route(const MoeParams& p, Tables& tb, int wave, int lane, bool publish) {
-  constexpr int NI = kMaxExperts / 64;
-  for (int t = wave; t < p.t; t += (int)(blockDim.x >> 6)) {
-    float l[NI];
+// Maximum over each row of 16 lanes, in all of them (DPP rotations).
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#define DG_ROR_MAX(n) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 0xf, 0xf, false))
+  DG_ROR_MAX(1);
+  DG_ROR_MAX(2);
+  DG_ROR_MAX(4);
+  DG_ROR_MAX(8);
+#undef DG_ROR_MAX
+  return v;
+}
+__device__ __forceinline__ float row_sum(float v) {
+#define DG_ROR_ADD(n) \
+  v += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x120 + n, 0xf, 0xf, false))
+  DG_ROR_ADD(8);
+  DG_ROR_ADD(4);
+  DG_ROR_ADD(2);
+  DG_ROR_ADD(1);
+#undef DG_ROR_ADD
+  return v;
+}
+
+// Top-k of every token's logits, ties to the lowest expert: 16 lanes per
+// token (four tokens per wave at a time), 16 NI >= E logits in registers.  A
+// round is a maximum over the lanes and the lowest expert that holds it; lane j
+// of the row keeps round j's choice.  Every workgroup does this for all tokens
+// (two microseconds for 64) rather than waiting for a kernel that does it once.
+template <int NI, int TMAX>
+__device__ __forceinline__ void route_rows(const MoeParams& p, Tables<TMAX>& tb, bool publish) {
+  const int l16 = threadIdx.x & 15;
+  const int rows = (int)(blockDim.x >> 4);
+  for (int t0 = 0; t0 < p.t; t0 += rows) {
+    const int t = t0 + (int)(threadIdx.x >> 4);
+    const bool in = t < p.t;  // (rows past the last token work on empty keys)
     uint32_t key[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int e = lane + 64 * i;
-      l[i] = e < p.experts ? p.logits[(int64_t)t * p.experts + e] : 0.f;
-      key[i] = e < p.experts ? logit_key(l[i]) : 0;
+      const int e = l16 + 16 * i;
+      key[i] = in && e < p.experts ? logit_key(p.logits[(int64_t)t * p.experts + e]) : 0;
     }
-    float sum_all = 0.f;  // softmax over every expert (not renormalised)
-    float top = 0.f;
+    uint32_t top = 0, mine = 0;
     int my_id = -1;
-    float my_l = 0.f;
+    float all = 0.f;  // softmax over every expert (not renormalised)
     for (int j = 0; j < p.top_k; ++j) {
       uint32_t best = 0;
 #pragma unroll
       for (int i = 0; i < NI; ++i) best = max(best, key[i]);
-      best = wave_max(best);
-      int e = -1;
-      float v = 0.f;
-      if (best != 0) {
+      best = row_max(best);
+      uint32_t low = 0;  // kMaxExperts - (lowest expert with the key): a maximum again
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const uint64_t m = __ballot(key[i] == best);
-          if (m != 0 && e < 0) {
-            const int ln = __builtin_ctzll(m);
-            e = 64 * i + ln;
-            v = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(l[i]), ln));
-            if (lane == ln) key[i] = 0;
-          }
-        }
-      }
+      for (int i = 0; i < NI; ++i)
+        if (key[i] == best) low = max(low, (uint32_t)(kMaxExperts - (l16 + 16 * i)));
+      const int e = kMaxExperts - (int)row_max(low);
       if (j == 0) {
-        top = v;
-        if (e >= 0 && !p.renormalize && p.scoring == DG_SCORING_SOFTMAX) {
+        top = best;
+        if (!p.renormalize && p.scoring == DG_SCORING_SOFTMAX) {
 #pragma unroll
           for (int i = 0; i < NI; ++i)
-            if (lane + 64 * i < p.experts) sum_all += expf(l[i] - top);
-          for (int o = 32; o > 0; o >>= 1) sum_all += __shfl_xor(sum_all, o);
+            if (key[i] != 0) all += expf(key_logit(key[i]) - key_logit(top));
+          all = row_sum(all);
         }
       }
-      if (lane == j) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (e == l16 + 16 * i) key[i] = 0;
+      if (l16 == j && best != 0) {
         my_id = e;
-        my_l = v;
+        mine = best;
       }
     }
     float w = 0.f;
-    if (my_id >= 0) w = p.scoring == DG_SCORING_SOFTMAX ? expf(my_l - top) : 1.f / (1.f + expf(-my_l));
-    float sum = w;
-    for (int o = kMaxTopK / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    if (my_id >= 0)
+      w = p.scoring == DG_SCORING_SOFTMAX ? expf(key_logit(mine) - key_logit(top)) : 1.f / (1.f + expf(-key_logit(mine)));
+    const float sum = row_sum(w);
     if (p.renormalize)
       w = sum != 0.f ? w / sum : 0.f;  // sum is 0 where no expert is left (or every sigmoid underflows)
     else if (p.scoring == DG_SCORING_SOFTMAX && my_id >= 0)
-      w /= sum_all;
+      w /= all;
     w *= p.scale;
-    if (lane < p.top_k) {
-      tb.id[t * p.top_k + lane] = (int16_t)my_id;
-      tb.w[t * p.top_k + lane] = w;
+    if (in && l16 < p.top_k) {
+      const int q = t * p.top_k + l16;
+      tb.id[q] = (int16_t)my_id;
+      tb.w[q] = w;
+      if (my_id >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&tb.tokens[my_id]), 1ull << t);
       if (publish) {
-        p.ids[t * p.top_k + lane] = my_id;
-        p.weights[t * p.top_k + lane] = w;
+        p.ids[q] = my_id;
+        p.weights[q] = w;
       }
     }
   }
@@ -165,24 +179,38 @@ __device__ __forceinline__ void route(const MoeParams& p, Tables& tb, int wave, 
 // Fills the tables.  ROUTE: from the logits (published by workgroup 0), else
 // from ids / weights: ids outside [0, E) drop out, a token's repeated expert
 // keeps one pair with the sum of its weights.
-template <bool ROUTE>
-__device__ __forceinline__ void build_tables(const MoeParams& p, Tables& tb) {
+template <bool ROUTE, int TMAX>
+__device__ __forceinline__ void build_tables(const MoeParams& p, Tables<TMAX>& tb) {
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6), nthreads = blockDim.x;
   const int np = p.t * p.top_k;
+  for (int e = tid; e < p.experts; e += nthreads) tb.tokens[e] = 0;
+  if (tid == 0) tb.repeated = 0;
+  __syncthreads();
   if constexpr (ROUTE) {
-    route(p, tb, wave, lane, blockIdx.x == 0);
+    const bool publish = blockIdx.x == 0;
+    if (p.experts <= 64)
+      route_rows<4>(p, tb, publish);
+    else if (p.experts <= 128)
+      route_rows<8>(p, tb, publish);
+    else if (p.experts <= 256)
+      route_rows<16>(p, tb, publish);
+    else
+      route_rows<32>(p, tb, publish);
   } else {
     for (int q = tid; q < np; q += nthreads) {
       const int id = p.ids[q];
-      tb.id[q] = (int16_t)(id >= 0 && id < p.experts ? id : -1);
+      const bool ok = id >= 0 && id < p.experts;
+      tb.id[q] = (int16_t)(ok ? id : -1);
       tb.w[q] = p.weights[q];
+      if (ok) {
+        const uint64_t bit = 1ull << (q / p.top_k);
+        if (atomicOr(reinterpret_cast<unsigned long long*>(&tb.tokens[id]), bit) & bit) tb.repeated = 1;
+      }
     }
   }
-  if (tid < 8 && np + tid < kMaxPairs) tb.id[np + tid] = -1;  // the scan reads eights
-  if (tid == 0) tb.npair = 0;
   __syncthreads();
   if constexpr (!ROUTE) {
-    if (tid < p.t) {
+    if (tb.repeated && tid < p.t) {
       const int b = tid * p.top_k;
       for (int j = 1; j < p.top_k; ++j) {
         const int id = tb.id[b + j];
@@ -195,48 +223,67 @@ __device__ __forceinline__ void build_tables(const MoeParams& p, Tables& tb) {
           }
       }
     }
-    __syncthreads();
   }
-  // sorted position of pair q: the pairs of lower experts and the earlier
-  // pairs of its own
+  // per expert, its pairs and whether it is a segment, summed up to it: within
+  // chunks of 64 experts by one wave each, then over the chunks
+  const int nchunk = (p.experts + 63) >> 6, nwaves = nthreads >> 6;
+  int below[kMaxExperts / 64], segs[kMaxExperts / 64];
+#pragma unroll
+  for (int r = 0; r < kMaxExperts / 64; ++r) {
+    const int c = wave + r * nwaves;
+    if (c >= nchunk) break;
+    const int e = 64 * c + lane;
+    const int n = e < p.experts ? __builtin_popcountll(tb.tokens[e]) : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(sum, o);
+      if (lane >= o) sum += v;
+    }
+    const uint64_t used = __ballot(n > 0);
+    below[r] = sum - n;
+    segs[r] = __builtin_popcountll(used & ((1ull << lane) - 1));
+    if (lane == 63) {
+      tb.chunk_pairs[c] = sum;
+      tb.chunk_segs[c] = __builtin_popcountll(used);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kMaxExperts / 64; ++r) {
+    const int c = wave + r * nwaves;
+    if (c >= nchunk) break;
+    int pairs = 0, nsegs = 0;
+    for (int o = 0; o < c; ++o) {
+      pairs += tb.chunk_pairs[o];
+      nsegs += tb.chunk_segs[o];
+    }
+    const int e = 64 * c + lane;
+    if (e < p.experts) {
+      tb.base[e] = (uint16_t)(pairs + below[r]);
+      if (tb.tokens[e]) {
+        tb.seg[nsegs + segs[r]] = (uint16_t)(pairs + below[r]);
+        tb.sid[nsegs + segs[r]] = (int16_t)e;
+      }
+    }
+    if (c == nchunk - 1 && lane == 0) {
+      tb.nseg = nsegs + tb.chunk_segs[c];
+      tb.seg[tb.nseg] = (uint16_t)(pairs + tb.chunk_pairs[c]);
+    }
+  }
+  __syncthreads();
   for (int q = tid; q < np; q += nthreads) {
     const int id = tb.id[q];
     if (id < 0) continue;
-    int pos = 0;
-    for (int o = 0; o < np; o += 8) {
-      const int4 v = *reinterpret_cast<const int4*>(&tb.id[o]);
-      const int u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int other = c & 1 ? u[c >> 1] >> 16 : (int)(int16_t)u[c >> 1];
-        pos += other >= 0 && (other < id || (other == id && o + c < q));
-      }
-    }
-    tb.pair[pos] = (uint16_t)q;
-    tb.sid[pos] = (int16_t)id;
-    atomicAdd(&tb.npair, 1);
-  }
-  __syncthreads();
-  if (wave == 0) {
-    const int n = tb.npair;
-    int base = 0;
-    for (int c = 0; c < n; c += 64) {
-      const int q = c + lane;
-      const bool first = q < n && (q == 0 || tb.sid[q] != tb.sid[q - 1]);
-      const uint64_t m = __ballot(first);
-      if (first) tb.seg[base + __builtin_popcountll(m & ((1ull << lane) - 1))] = (uint16_t)q;
-      base += __builtin_popcountll(m);
-    }
-    if (lane == 0) {
-      tb.seg[base] = (uint16_t)n;
-      tb.nseg = base;
-    }
+    const int t = q / p.top_k;
+    tb.pair[tb.base[id] + __builtin_popcountll(tb.tokens[id] & ((1ull << t) - 1))] = (uint16_t)q;
   }
   __syncthreads();
 }
 
 // The pair in column c of the segment [q0, q1), -1 past its end.
-__device__ __forceinline__ int column_pair(const Tables& tb, int q0, int q1, int c) {
+template <int TMAX>
+__device__ __forceinline__ int column_pair(const Tables<TMAX>& tb, int q0, int q1, int c) {
   return q0 + c < q1 ? (int)tb.pair[q0 + c] : -1;
 }
 
@@ -249,9 +296,12 @@ __device__ __forceinline__ int column_pair(const Tables& tb, int q0, int q1, int
 struct UpCursor {
   Unit u;
   const MoeParams* p;
-  const Tables* tb;
+  const Tables<kMaxTokens>* tb;
   int item, items, slabs, grid, kb, nb, waves, wave;
   int q0, q1;
+  uint32_t rk;  // ceil(2^16 / k): pr / k = pr rk >> 16 for pr < 1024, k <= 16
+
+  __device__ __forceinline__ uint32_t div_k(int pr) const { return ((uint32_t)pr * rk) >> 16; }
 
   __device__ __forceinline__ void seek() {  // the item and K block the cursor stands on
     u.live = item < items && wave < nb;
@@ -259,7 +309,7 @@ struct UpCursor {
     const int s = item / slabs, n0 = (item - s * slabs) * 16;
     q0 = (int)uniform(tb->seg[s]);
     q1 = (int)uniform(tb->seg[s + 1]);
-    const int e = (int)uniform(tb->sid[q0]);
+    const int e = (int)uniform(tb->sid[s]);
     u.tiles = (q1 - q0 + 15) >> 4;
     u.wa = p->w13 + ((int64_t)e * 2 * p->inter + n0) * u.wrow;
     u.wb = u.wa + (int64_t)p->inter * u.wrow;
@@ -287,7 +337,7 @@ struct UpCursor {
   }
   __device__ __forceinline__ uint32_t row(int t, int r) const {
     const int pr = column_pair(*tb, q0, q1, 16 * t + r);
-    return pr >= 0 ? (uint32_t)(pr / p->top_k) * (uint32_t)p->hid * 2u : kOut;
+    return pr >= 0 ? div_k(pr) * ((uint32_t)p->hid * 2u) : kOut;
   }
   __device__ __forceinline__ uint32_t scale(int) const { return kOut; }
 };
@@ -295,11 +345,11 @@ struct UpCursor {
 template <int MODE, bool ROUTE, int W, int D>
 __global__ __launch_bounds__(W * 64) void moe_up_kernel(const MoeParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(MODE, W, D)];
-  __shared__ __attribute__((aligned(16))) Tables tb;
+  __shared__ __attribute__((aligned(16))) Tables<kMaxTokens> tb;
   __shared__ __attribute__((aligned(16))) v4f red[W][2][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  build_tables<ROUTE>(p, tb);
+  build_tables<ROUTE, kMaxTokens>(p, tb);
 
   UpCursor c{};
   c.p = &p;
@@ -311,6 +361,7 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(const MoeParams p) {
   c.nb = p.hid >> 7;
   c.waves = W;
   c.wave = c.kb = wave;
+  c.rk = (65536u + p.top_k - 1) / p.top_k;
   c.u.ra = c.u.rb = 16;
   c.u.wrow = (uint32_t)p.hid * (MODE == kBf16 ? 2 : 1);
   c.u.kbytes = MODE == kBf16 ? 256 : 128;
@@ -365,10 +416,11 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(const MoeParams p) {
 // unit's groups are 16 rows each) and walks (segment, K block) units, the
 // waves round robin.  A wave's sums of a segment go to its own LDS rows
 // [token][32] when it leaves the segment, and the waves' rows meet at the end.
+template <int TMAX>
 struct DownCursor {
   Unit u;
   const MoeParams* p;
-  const Tables* tb;
+  const Tables<TMAX>* tb;
   int seg, nseg, kb, nb, waves, h0;
   int q0, q1;
 
@@ -377,7 +429,7 @@ struct DownCursor {
     if (!u.live) return;
     q0 = (int)uniform(tb->seg[seg]);
     q1 = (int)uniform(tb->seg[seg + 1]);
-    const int e = (int)uniform(tb->sid[q0]);
+    const int e = (int)uniform(tb->sid[seg]);
     const int wb = p->s2 ? 128 : 256;
     u.tiles = (q1 - q0 + 15) >> 4;
     u.wa = p->w2 + ((int64_t)e * p->hid + h0) * u.wrow + kb * wb;
@@ -395,7 +447,7 @@ struct DownCursor {
   }
   __device__ __forceinline__ uint32_t row(int t, int r) const {
     const int pr = column_pair(*tb, q0, q1, 16 * t + r);
-    return pr >= 0 ? (uint32_t)pr * (uint32_t)p->inter * 2u : kOut;
+    return pr >= 0 ? (uint32_t)pr * ((uint32_t)p->inter * 2u) : kOut;
   }
   __device__ __forceinline__ uint32_t scale(int) const { return kOut; }
 };
@@ -406,15 +458,16 @@ constexpr int kYStride = 36;  // floats per token in LDS: 32 and a pad against b
 template <int MODE, int TMAX, int W, int D>
 __global__ __launch_bounds__(W * 64) void moe_down_kernel(const MoeParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(MODE, W, D)];
-  __shared__ __attribute__((aligned(16))) Tables tb;
+  __shared__ __attribute__((aligned(16))) Tables<TMAX> tb;
   __shared__ __attribute__((aligned(16))) float yacc[W][TMAX][kYStride];
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
   for (int i = tid; i < W * TMAX * kYStride / 4; i += W * 64)
     reinterpret_cast<v4f*>(&yacc[0][0][0])[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  build_tables<false>(p, tb);
+  build_tables<false, TMAX>(p, tb);
 
-  DownCursor c{};
+  using Cursor = DownCursor<TMAX>;
+  Cursor c{};
   c.p = &p;
   c.tb = &tb;
   c.nseg = (int)uniform(tb.nseg);
@@ -431,7 +484,7 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(const MoeParams p) {
   c.u.s = p.s2;
   c.u.srange = 4;
   c.seek();
-  Pipe<MODE, D, DownCursor> pipe;
+  Pipe<MODE, D, Cursor> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
 
   v4f a[kMaxTiles], b[kMaxTiles];

@@ -155,14 +155,14 @@ struct Pipe {
       }
     } else {
       const int t = phase - WE;
+      const uint32_t off[2] = {ic.row(t, lrow), ic.row(t, 8 + lrow)};
 #pragma unroll
       for (int l = 0; l < 2; ++l) {
         const dma::v4i r = dma::resource(u.x + 128 * l, u.xrange > 128u * l ? u.xrange - 128u * l : 0u);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int c = chunk ^ swz(8 * j + lrow);
-          const uint32_t off = ic.row(t, 8 * j + lrow);
-          dma::load16(lds + (2 * l + j) * 1024, r, 128 * l + 16 * c < u.xbytes ? off + 16u * c : kOut);
+          dma::load16(lds + (2 * l + j) * 1024, r, 128 * l + 16 * c < u.xbytes ? off[j] + 16u * c : kOut);
         }
       }
       if constexpr (MODE != kBf16) {
@@ -185,39 +185,45 @@ struct Pipe {
   typedef __attribute__((address_space(3))) const v4i* lv;
   typedef __attribute__((address_space(3))) const float* lf;
 
+  // The next entry to use, landed: `held` entries before it are still unreleased.
+  template <int HELD>
   __device__ __forceinline__ uint32_t arrive() {
+    static_assert(HELD < D, "the ring holds the unit's entries");
     const uint32_t lds = ring + cslot * kEntry;
     cslot = cslot + 1 == D ? 0 : cslot + 1;
-    dma::wait<(D - 1) * kLoads>();
+    dma::wait<(D - 1 - HELD) * kLoads>();
     return lds;
   }
-  // The entry's LDS reads are done: its slot is loaded anew.
+  // The LDS reads of N entries are done: their slots are loaded anew.
+  template <int N>
   __device__ __forceinline__ void release() {
     dma::lds_done();
-    issue();
+#pragma unroll
+    for (int i = 0; i < N; ++i) issue();
   }
 
   // One unit of `tiles` tiles into the sums of A and B (tile t's lanes: column
-  // l16, rows 4 lq .. 4 lq + 3 of the group).
+  // l16, rows 4 lq .. 4 lq + 3 of the group).  The last weight entry and the
+  // first tile are read together: one LDS latency for both.
   template <int NT>
   __device__ __forceinline__ void unit(int tiles, v4f* a, v4f* b) {
     v4i w[2][WE][2];  // [group][line][chunk lq, lq + 4]
     float s[2][WE];
 #pragma unroll
     for (int e = 0; e < WE; ++e) {
-      const uint32_t lds = arrive();
+      const uint32_t lds = arrive<0>();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) w[g][e][j] = *(lv)(uintptr_t)(lds + 2048 * g + o[j]);
         s[g][e] = MODE != kBf16 ? *(lf)(uintptr_t)(lds + 4096 + 4 * g) : 1.f;
       }
-      release();
+      if (e + 1 < WE) release<1>();
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if (t >= tiles) break;
-      const uint32_t lds = arrive();
+      if (t > 0 && t >= tiles) break;
+      const uint32_t lds = t == 0 ? arrive<1>() : arrive<0>();
       v4i x[2][2];
       float xs[2];
 #pragma unroll
@@ -226,7 +232,7 @@ struct Pipe {
         for (int j = 0; j < 2; ++j) x[l][j] = *(lv)(uintptr_t)(lds + 2048 * l + o[(MODE == kW8A16 ? 2 : 0) + j]);
         xs[l] = MODE == kFp8 ? *(lf)(uintptr_t)(lds + 4096 + 4 * (16 * l + (lane & 15))) : 1.f;
       }
-      release();
+      if (t == 0) release<2>(); else release<1>();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         v4f& acc = g ? b[t] : a[t];
