@@ -79,7 +79,7 @@ __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p)
   }
   c.place();
   const int mine = c.nb > wave ? (c.nb - wave + W - 1) / W : 0;
-  Pipe<MODE, D, RowsCursor> pipe;
+  Pipe<MODE, D, true, RowsCursor> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
   v4f a[NT], b[NT];
 #pragma unroll

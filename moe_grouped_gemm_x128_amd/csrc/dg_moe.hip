@@ -35,7 +35,6 @@ using namespace stream;
 
 constexpr int kMaxTokens = 64;
 constexpr int kMaxTopK = 16;
-constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
 constexpr int kMaxExperts = 512;
 
 struct MoeParams {
@@ -372,7 +371,7 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(const MoeParams p) {
   c.u.srange = c.u.so[1] + 4u;
   c.seek();
   const int mine = c.nb > wave ? (c.nb - wave + W - 1) / W : 0;  // units of an item on this wave
-  Pipe<MODE, D, UpCursor> pipe;
+  Pipe<MODE, D, false, UpCursor> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
 
   for (int item = blockIdx.x; item < c.items; item += c.grid) {
@@ -484,7 +483,7 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(const MoeParams p) {
   c.u.s = p.s2;
   c.u.srange = 4;
   c.seek();
-  Pipe<MODE, D, Cursor> pipe;
+  Pipe<MODE, D, false, Cursor> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
 
   v4f a[kMaxTiles], b[kMaxTiles];

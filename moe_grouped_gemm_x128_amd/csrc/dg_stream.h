@@ -98,7 +98,9 @@ struct Unit {
   uint32_t xsrange;
 };
 
-template <int MODE, int D, class Cursor>
+// PARTIAL: rows and lines may be cut (the linear layer); otherwise every unit
+// has 16 rows in both groups and whole lines.
+template <int MODE, int D, bool PARTIAL, class Cursor>
 struct Pipe {
   static constexpr int kEntry = entry_bytes(MODE);
   static constexpr int kLoads = MODE == kBf16 ? 4 : 5;
@@ -109,7 +111,8 @@ struct Pipe {
   Cursor ic;           // the unit being loaded
   int phase = 0;       // its next entry
   int islot = 0, cslot = 0;
-  int lane, lrow, chunk;  // the lane's row (of 8) and chunk in a load
+  int lane, lrow;      // the lane's row (of 8) in a load
+  uint32_t xc[2], wv[2];  // its chunk's byte in a line, and its offset in the weights, for the two loads of 16 rows
   uint32_t o[4];       // LDS offsets of chunks lq, lq + 4, 2 lq, 2 lq + 1 of row l16
 
   __device__ __forceinline__ void init(uint32_t lds, const Cursor& c, int lane_) {
@@ -117,7 +120,11 @@ struct Pipe {
     ic = c;
     lane = lane_;
     lrow = lane >> 3;
-    chunk = lane & 7;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      xc[j] = (uint32_t)(((lane & 7) ^ swz(8 * j + lrow)) << 4);
+      wv[j] = (uint32_t)(8 * j + lrow) * ic.u.wrow + xc[j];
+    }
     const int l16 = lane & 15, lq = lane >> 4, s = swz(l16);
     o[0] = (uint32_t)(l16 * 128 + ((lq ^ s) << 4));
     o[1] = (uint32_t)(l16 * 128 + (((lq + 4) ^ s) << 4));
@@ -135,17 +142,15 @@ struct Pipe {
     if (phase < WE || !u.live) {
       // one line of K of 16 rows of A and 16 of B
       const int koff = u.live ? 128 * phase : 0;
-      const int left = u.live ? u.kbytes - koff : 0;
+      const int left = u.live ? (PARTIAL ? u.kbytes - koff : 128) : 0;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int rows = g ? u.rb : u.ra;
+        const int rows = PARTIAL ? (g ? u.rb : u.ra) : 16;
         const dma::v4i r = dma::resource((g ? u.wb : u.wa) + koff,
                                          left > 0 && rows > 0 ? (uint32_t)(rows - 1) * u.wrow + min(left, 128) : 0u);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c = chunk ^ swz(8 * j + lrow);
-          dma::load16_nt(lds + (2 * g + j) * 1024, r, 16 * c < left ? (uint32_t)(8 * j + lrow) * u.wrow + 16u * c : kOut);
-        }
+        for (int j = 0; j < 2; ++j)
+          dma::load16_nt(lds + (2 * g + j) * 1024, r, !PARTIAL || (int)xc[j] < left ? wv[j] : kOut);
       }
       if constexpr (MODE != kBf16) {
         // lane 0: A's scale of this line, lane 1: B's
@@ -158,12 +163,11 @@ struct Pipe {
       const uint32_t off[2] = {ic.row(t, lrow), ic.row(t, 8 + lrow)};
 #pragma unroll
       for (int l = 0; l < 2; ++l) {
-        const dma::v4i r = dma::resource(u.x + 128 * l, u.xrange > 128u * l ? u.xrange - 128u * l : 0u);
+        const dma::v4i r = dma::resource(u.x + 128 * l, !PARTIAL || u.xrange > 128u * l ? u.xrange - 128u * l : 0u);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c = chunk ^ swz(8 * j + lrow);
-          dma::load16(lds + (2 * l + j) * 1024, r, 128 * l + 16 * c < u.xbytes ? off[j] + 16u * c : kOut);
-        }
+        for (int j = 0; j < 2; ++j)
+          dma::load16(lds + (2 * l + j) * 1024, r,
+                      !PARTIAL || 128 * l + (int)xc[j] < u.xbytes ? off[j] + xc[j] : kOut);
       }
       if constexpr (MODE != kBf16) {
         if constexpr (MODE == kFp8) {
