@@ -567,6 +567,14 @@ def gemm_fp8_nt_epilogue(lhs, rhs, out, bias=None, activation="none", residual=N
     return out
 
 
+def gemm_bf16_nt_epilogue_backward_workspace(m, n):
+    """Bytes of workspace that gemm_bf16_nt_epilogue_backward needs for dout [m,n]."""
+    need = _i64()
+    _check(_lib.dg_gemm_bf16_nt_epilogue_backward_workspace(m, n, ctypes.byref(need)),
+           "dg_gemm_bf16_nt_epilogue_backward_workspace")
+    return need.value
+
+
 def gemm_bf16_nt_epilogue_backward(dout, a, b, pre=None, activation="none", da=None, db=None, dbias=None,
                                    workspace=None):
     """Gradients of gemm_bf16_nt_epilogue from dout bf16 [M,N] and the stored
@@ -598,14 +606,12 @@ def gemm_bf16_nt_epilogue_backward(dout, a, b, pre=None, activation="none", da=N
         if dbias.get_device() != dev or not dbias.is_contiguous():
             raise ValueError("dbias must be contiguous, on the same GPU")
         pbias = _ptr(dbias)
-    need = _i64()
-    _check(_lib.dg_gemm_bf16_nt_epilogue_backward_workspace(m, n, ctypes.byref(need)),
-           "dg_gemm_bf16_nt_epilogue_backward_workspace")
+    need = gemm_bf16_nt_epilogue_backward_workspace(m, n)
     if workspace is None:
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dout.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dout.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous() or \
-            workspace.numel() * workspace.element_size() < need.value:
-        raise ValueError(f"workspace must be contiguous, on the same GPU, with at least {need.value} bytes")
+            workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be contiguous, on the same GPU, with at least {need} bytes")
     _check(_lib.dg_gemm_bf16_nt_epilogue_backward(
         _ptr(dout), _ld(dout, dev, "dout"), _ptr(a), _ld(a, dev, "a"), _ptr(b), _ld(b, dev, "b"), pp, ldp, act,
         pa, lda, pb, ldb, pbias, _ptr(workspace), m, n, k, _stream(dout)), "dg_gemm_bf16_nt_epilogue_backward")

@@ -45,39 +45,71 @@ __device__ __forceinline__ float tanh_arg2(float x) {  // 2u of gelu_tanh
   return 1.59576912160573071f * __builtin_fmaf(0.044715f * x * x, x, x);
 }
 
-__device__ __forceinline__ float apply(float x, int a) {
-  switch (a) {
-    case DG_ACT_RELU: return x > 0.f || x != x ? x : 0.f;  // NaN stays NaN
-    case DG_ACT_GELU: {
-      float e;
-      return x * phi(x, e);
-    }
-    case DG_ACT_GELU_TANH: return x * sigmoid(tanh_arg2(x));
-    case DG_ACT_SILU: return x * sigmoid(x);
-    default: return x;
+template <int A>
+__device__ __forceinline__ float apply_one(float x) {
+  if constexpr (A == DG_ACT_RELU) return x > 0.f || x != x ? x : 0.f;  // NaN stays NaN
+  if constexpr (A == DG_ACT_GELU) {
+    float e;
+    return x * phi(x, e);
   }
+  if constexpr (A == DG_ACT_GELU_TANH) return x * sigmoid(tanh_arg2(x));
+  if constexpr (A == DG_ACT_SILU) return x * sigmoid(x);
+  return x;
 }
 
-// d apply(x) / dx (relu: 0 at 0).
-__device__ __forceinline__ float grad(float x, int a) {
+// The activation `a` (wave-uniform) of N values: one branch for all of them.
+template <int N, class V>
+__device__ __forceinline__ void apply(V& v, int a) {
+#define DG_APPLY(A)                                            \
+  case A:                                                      \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = apply_one<A>(v[i]); \
+    break;
   switch (a) {
-    case DG_ACT_RELU: return x > 0.f ? 1.f : 0.f;
-    case DG_ACT_GELU: {
-      float e;
-      const float p = phi(x, e);
-      return __builtin_fmaf(x * 0.39894228040143268f, e, p);
-    }
-    case DG_ACT_GELU_TANH: {
-      const float s = sigmoid(tanh_arg2(x));
-      const float du2 = 1.59576912160573071f * __builtin_fmaf(0.134145f * x, x, 1.f);
-      return __builtin_fmaf(x * du2, s * (1.f - s), s);
-    }
-    case DG_ACT_SILU: {
-      const float s = sigmoid(x);
-      return __builtin_fmaf(x, s * (1.f - s), s);
-    }
-    default: return 1.f;
+    DG_APPLY(DG_ACT_RELU)
+    DG_APPLY(DG_ACT_GELU)
+    DG_APPLY(DG_ACT_GELU_TANH)
+    DG_APPLY(DG_ACT_SILU)
+    default: break;
   }
+#undef DG_APPLY
+}
+
+// The derivative (relu: 0 at 0).
+template <int A>
+__device__ __forceinline__ float grad_one(float x) {
+  if constexpr (A == DG_ACT_RELU) return x > 0.f ? 1.f : 0.f;
+  if constexpr (A == DG_ACT_GELU) {
+    float e;
+    const float p = phi(x, e);
+    return __builtin_fmaf(x * 0.39894228040143268f, e, p);
+  }
+  if constexpr (A == DG_ACT_GELU_TANH) {
+    const float s = sigmoid(tanh_arg2(x));
+    const float du2 = 1.59576912160573071f * __builtin_fmaf(0.134145f * x, x, 1.f);
+    return __builtin_fmaf(x * du2, s * (1.f - s), s);
+  }
+  if constexpr (A == DG_ACT_SILU) {
+    const float s = sigmoid(x);
+    return __builtin_fmaf(x, s * (1.f - s), s);
+  }
+  return 1.f;
+}
+
+// d[i] *= activation'(x[i]) for N values.
+template <int N>
+__device__ __forceinline__ void times_grad(float* d, const float* x, int a) {
+#define DG_GRAD(A)                                             \
+  case A:                                                      \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) d[i] *= grad_one<A>(x[i]); \
+    break;
+  switch (a) {
+    DG_GRAD(DG_ACT_RELU)
+    DG_GRAD(DG_ACT_GELU)
+    DG_GRAD(DG_ACT_GELU_TANH)
+    DG_GRAD(DG_ACT_SILU)
+    default: break;
+  }
+#undef DG_GRAD
 }
 
 }  // namespace act

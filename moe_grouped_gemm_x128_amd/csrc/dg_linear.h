@@ -42,23 +42,23 @@ enum GemmLayout : int { kNT = 0, kNN = 1, kTN = 2 };  // A, B stored: [m,k] [n,k
 struct GemmTile {
   int bm, bn, wm, wn, stages;
 };
-constexpr GemmTile kGemmTiles[] = {{256, 256, 2, 4, 2}, {256, 128, 4, 2, 3}, {128, 128, 2, 2, 2}, {64, 128, 2, 2, 3}};
-constexpr int kNumGemmTiles = 4;
-// workgroups of a tile that share a CU (LDS), and whether the layout has it
+constexpr GemmTile kGemmTiles[] = {
+    {256, 256, 2, 4, 2}, {256, 128, 4, 2, 3}, {128, 128, 2, 2, 2}, {64, 128, 2, 2, 3}, {64, 64, 2, 2, 4}};
+constexpr int kNumGemmTiles = 5;
+// workgroups of a tile that share a CU (LDS)
 constexpr int gemm_residents(int tile) { return tile >= 2 ? 2 : 1; }
-constexpr bool gemm_has(int layout, int tile) { return !(tile == 3 && layout == kTN); }
 hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipStream_t stream);
 
 // dpre = dc * act'(pre) as bf16 [m, ldp] (columns n .. ldp - 1 zero), unless
-// dpre is null, and the column sums of the unrounded dpre in chunks of
-// kBiasRows rows, partial [ceil(m / kBiasRows)][n], unless partial is null.
-constexpr int kBiasRows = 64;
+// dpre is null, and the column sums of the unrounded dpre in chunks of `rows`
+// rows, partial [ceil(m / rows)][n], unless partial is null.
 struct DactParams {
   const uint16_t* dc;
   const uint16_t* pre;  // null: no activation
   uint16_t* dpre;
   float* partial;
   int64_t lddc, ldpre, ldp;
+  int rows;             // a multiple of 8
   int m, n, act, vec;   // vec: rows of dc and pre start on 16-byte boundaries
 };
 hipError_t launch_dact(const DactParams& p, hipStream_t stream);

@@ -55,7 +55,8 @@ dg_status make_epilogue(void* c, int64_t ldc, int c_type, const dg_epilogue* in,
     }
   }
   e->vec = vec;
-  e->vec8 = vec8;
+  // 32-bit byte offsets over a tile's 256 rows
+  e->vec8 = vec8 && ldc <= kMaxLd / 4 && e->ldr <= kMaxLd / 4 && e->ldp <= kMaxLd / 4;
   return DG_SUCCESS;
 }
 
@@ -69,14 +70,13 @@ struct Plan {
 
 Plan plan(int layout, int m, int n, int k, int cus, bool may_split) {
   // TFLOP/s of the whole card when every CU works on this tile
-  static const double rate[kNumGemmTiles] = {1250., 1000., 850., 550.};
+  static const double rate[kNumGemmTiles] = {1350., 1150., 1080., 850., 600.};
   const int blocks = ceil_div(k, 64);
   const char* force = std::getenv("DG_FORCE_TILE");
   const char* fsplit = std::getenv("DG_FORCE_SPLITS");
   Plan best{-1, 1, blocks};
   double best_us = 1e300;
   for (int t = 0; t < kNumGemmTiles; ++t) {
-    if (!gemm_has(layout, t)) continue;
     const GemmTile g = kGemmTiles[t];
     if (force && *force) {
       int bm, bn, wm, wn;
@@ -144,6 +144,11 @@ dg_status gemm(int layout, GemmParams& p, int cus, hipStream_t stream) {
 
 bool bad_operand(const void* p, int64_t ld, int cols) { return ld < cols || !p; }
 bool unfit_operand(const void* p, int64_t ld) { return !aligned(p, 16) || ld % 8 != 0 || ld > kMaxLd; }
+
+// Rows of dc that one workgroup of the activation's backward pass takes: 64
+// (the bias partials are then 1/32 of the traffic) where that gives the card
+// work, else 16 (517 x 1161: 24 us with 45 workgroups of 64 rows).
+int dact_rows(int m, int n) { return (int64_t)ceil_div(m, 64) * ceil_div(n, 256) >= 512 ? 64 : 16; }
 
 // workspace of the backward pass: dpre bf16 [m, ldp], then the bias partials
 int64_t dpre_bytes(int m, int n) { return (2 * (int64_t)m * round8(n) + 15) & ~(int64_t)15; }
@@ -221,7 +226,7 @@ dg_status dg_gemm_fp8_nt_epilogue(const void* a, const float* sa, const void* b,
 
 dg_status dg_gemm_bf16_nt_epilogue_backward_workspace(int m, int n, int64_t* bytes) {
   if (!bytes || m <= 0 || n <= 0) return DG_ERROR_INVALID_VALUE;
-  *bytes = dpre_bytes(m, n) + 4 * (int64_t)ceil_div(m, kBiasRows) * n;
+  *bytes = dpre_bytes(m, n) + 4 * (int64_t)ceil_div(m, dact_rows(m, n)) * n;
   return DG_SUCCESS;
 }
 
@@ -259,10 +264,11 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
     d.ldp = round8(n);
     d.m = m;
     d.n = n;
+    d.rows = dact_rows(m, n);
     d.act = activation;
     d.vec = aligned(dc, 16) && lddc % 8 == 0 && (!act || (aligned(pre, 16) && ld_pre % 8 == 0));
     if (launch_dact(d, stream) != hipSuccess) return DG_ERROR_LAUNCH;
-    if (dbias && launch_bias_sum(partial, dbias, ceil_div(m, kBiasRows), n, stream) != hipSuccess)
+    if (dbias && launch_bias_sum(partial, dbias, ceil_div(m, d.rows), n, stream) != hipSuccess)
       return DG_ERROR_LAUNCH;
   }
   const uint8_t* g = in_place ? static_cast<const uint8_t*>(dc) : reinterpret_cast<const uint8_t*>(dpre);

@@ -16,8 +16,8 @@
 // of a fragment read over all banks.
 //
 // Per block a wave multiplies two halves of 32 k.  The fragments of the next
-// half are read while the current half is multiplied; the one barrier of a
-// block sits between the halves, where the last reads of a block's stage and the
+// half are read between the current half's MFMAs; the one barrier of a block
+// sits between the halves, where the last reads of a block's stage and the
 // arrival of the next block meet, so MFMAs are queued on both sides of it.
 //
 // The MFMA takes B rows first and A rows second: a lane holds 4 consecutive
@@ -40,7 +40,12 @@ constexpr int kGroupM = 8;  // tile rows per raster group
 constexpr uint32_t kOut = 0x80000000u;
 
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
-__device__ __forceinline__ int hsw(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+// transposed: RB bytes per k (128: 4 units of 32 bytes, and k's parity moves by
+// half the banks; 256 and more: 8 units or more, every k starts on bank 0)
+template <int RB>
+__device__ __forceinline__ int hsw(int k) {
+  return RB == 128 ? ((k >> 1) & 1) | (((k >> 3) & 1) << 1) : (k & 3) | (((k >> 3) & 1) << 2);
+}
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ v4f mfma(const v8bf& b, const v8bf& a, const v4f& c) {
@@ -58,7 +63,7 @@ struct Operand {
   static constexpr int RB = BX * 2;                          // transposed: bytes per LDS row
   static constexpr int CPR = BX / 8, RP = 64 / CPR;          // chunks per row, rows per load
   static_assert(kPieces % NW == 0, "the same loads on every wave");
-  static_assert(TR ? (NW * RP) % 16 == 0 && BX % 128 == 0 : (NW * 8) % 16 == 0, "swizzle fixed per lane");
+  static_assert(TR ? (NW * RP) % 16 == 0 && BX % 64 == 0 : (NW * 8) % 16 == 0, "swizzle fixed per lane");
 
   // global side
   uint32_t voff, step;  // this lane's offset in its first piece, bytes between a wave's pieces
@@ -76,7 +81,7 @@ struct Operand {
       const int k0 = wave * RP + lane / CPR;
       const int pc = lane % CPR;
       chunk = 0;
-      voff = (uint32_t)k0 * (uint32_t)ld + (uint32_t)(((((pc >> 1) ^ hsw(k0)) << 1) | (pc & 1)) * 16);
+      voff = (uint32_t)k0 * (uint32_t)ld + (uint32_t)(((((pc >> 1) ^ hsw<RB>(k0)) << 1) | (pc & 1)) * 16);
       step = (uint32_t)(NW * RP) * (uint32_t)ld;
     }
     const int l16 = lane & 15, lq = lane >> 4;
@@ -85,7 +90,7 @@ struct Operand {
       for (int s = 0; s < 2; ++s)
         off[s] = (uint32_t)((wx * WTX + l16) * 128 + (((4 * s + lq) ^ swz(l16)) << 4));
     } else {
-      const int h = (l16 >> 2) | ((lq & 1) << 2);  // hsw of the rows this lane addresses
+      const int h = hsw<RB>(8 * lq + (l16 >> 2));  // the same for all rows that this lane addresses
 #pragma unroll
       for (int i = 0; i < F; ++i)
         off[i] = (uint32_t)((8 * lq + (l16 >> 2)) * RB + (((wx * F + i) ^ h) << 5) + ((l16 & 3) << 3));
@@ -112,14 +117,16 @@ struct Operand {
 
   // Fragment i of half s from the stage at LDS address `lds`.
   __device__ __forceinline__ v8bf frag(uint32_t lds, int i, int s) const {
-    typedef __attribute__((address_space(3))) const v4i* lp;
-    typedef __attribute__((address_space(3))) v4s* lt;
+    // (constant parts added to a pointer: they go into the instruction's offset)
+    typedef __attribute__((address_space(3))) uint8_t* lp;
     if constexpr (!TR) {
-      return __builtin_bit_cast(v8bf, *(lp)(uintptr_t)(lds + off[s] + i * 2048));
+      const lp at = (lp)(uintptr_t)(lds + off[s]);
+      return __builtin_bit_cast(v8bf, *(__attribute__((address_space(3))) const v4i*)(at + i * 2048));
     } else {
-      const uint32_t a = lds + off[i] + s * 32 * RB;
-      const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lt)(uintptr_t)a));
-      const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lt)(uintptr_t)(a + 4 * RB)));
+      typedef __attribute__((address_space(3))) v4s* lt;
+      const lp at = (lp)(uintptr_t)(lds + off[i]);
+      const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lt)(at + s * 32 * RB)));
+      const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lt)(at + (s * 32 + 4) * RB)));
       return __builtin_bit_cast(v8bf, v4i{lo[0], lo[1], hi[0], hi[1]});
     }
   }
@@ -133,12 +140,20 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmPar
   constexpr int FM = OpA::F, FN = OpB::F;
   constexpr int STAGE = OpA::kBytes + OpB::kBytes;
   constexpr int LOADS = OpA::kQ + OpB::kQ;  // per wave and block
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+  // whole-line epilogue: 16 rows of a wave at a time, fp32, the 16-byte chunk c
+  // of row r at c ^ r
+  constexpr int RS = OpB::WTX * 4, RC = RS / 16;                        // bytes and chunks per row
+  constexpr int LPR = OpB::WTX / 8, RPR = 64 / LPR, ROUNDS = 16 / RPR;  // lanes per row, rows per round
+  constexpr int kStores = FM * ROUNDS;                                   // 16-byte bf16 stores of a wave
+  constexpr bool kOwnRows = S == 2;
+  constexpr int kBehind = kOwnRows ? S - 1 : S - 2;  // blocks of the next item loaded before the stores
+  static_assert(kOwnRows || 16 * RS <= STAGE / NW, "a wave's rows fit its share of the slot");
+  static_assert((S - 2) * LOADS + 2 * kStores < 64, "vmcnt range");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + (kOwnRows ? NW * 16 * RS : 0)];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = (int)uniform(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int l16 = lane & 15, lq = lane >> 4;
   const uint32_t lds0 = dma::lds_addr(smem);
   OpA oa;
   OpB ob;
@@ -215,7 +230,8 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmPar
   dma::wait<(S - 1) * LOADS>();
   dma::barrier();
 
-  int q = 0;  // ring slot of the current block
+  int q = 0;       // ring slot of the current block
+  int stores = 0;  // the previous item's stores per kStores, 0: not counted
   while (cur.live) {
     const int nkb = (cur.k1 - cur.k0 + 63) >> 6;
     v4f acc[FN][FM];
@@ -223,58 +239,170 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmPar
     for (int i = 0; i < FN; ++i)
 #pragma unroll
       for (int j = 0; j < FM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    v8bf fa[2][FM], fb[2][FN];
-    auto read = [&](int set, int slot, int s) {
-      const uint32_t st = lds0 + slot * STAGE;
+    // Fragments of half a block: B's twice (the half being multiplied and the
+    // next), A's once -- a row's fragment is read anew for the next half as soon
+    // as its MFMAs are issued.
+    v8bf fa[FM], fb[2][FN];
+    auto read_b = [&](int set, int slot, int s) {
 #pragma unroll
-      for (int i = 0; i < FN; ++i) fb[set][i] = ob.frag(st + OpA::kBytes, i, s);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) fa[set][j] = oa.frag(st, j, s);
+      for (int i = 0; i < FN; ++i) fb[set][i] = ob.frag(lds0 + slot * STAGE + OpA::kBytes, i, s);
     };
-    auto multiply = [&](int set) {
+    auto multiply = [&](int set, int slot, int s) {
+      read_b(set ^ 1, slot, s);
 #pragma unroll
-      for (int j = 0; j < FM; ++j)
+      for (int j = 0; j < FM; ++j) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i) acc[i][j] = mfma(fb[set][i], fa[set][j], acc[i][j]);
+        for (int i = 0; i < FN; ++i) acc[i][j] = mfma(fb[set][i], fa[j], acc[i][j]);
+        fa[j] = oa.frag(lds0 + slot * STAGE, j, s);
+      }
     };
-    read(0, q, 0);
+    read_b(0, q, 0);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) fa[j] = oa.frag(lds0 + q * STAGE, j, 0);
+    // (the epilogue passes the sums through LDS: through rows of its own where
+    // the ring has two stages, else through the ring slot of the item's last
+    // block, which is loaded anew only after it)
+    int last = q;  // the slot of the block multiplied last
 #pragma unroll 1
     for (int kb = 0; kb < nkb; ++kb) {
-      read(1, q, 1);
-      multiply(0);
+      multiply(0, q, 1);
       // this wave has read the block's stage (the barrier waits for its LDS
-      // reads) and its share of the next block has landed
-      dma::wait<(S - 2) * LOADS>();
+      // reads) and its share of the next block has landed (the previous item's
+      // stores are younger than the blocks that were loaded before them)
+      if (kb < kBehind && stores == 1)
+        dma::wait<(S - 2) * LOADS + kStores>();
+      else if (kb < kBehind && stores == 2)
+        dma::wait<(S - 2) * LOADS + 2 * kStores>();
+      else
+        dma::wait<(S - 2) * LOADS>();
       dma::barrier();
-      issue(q);
+      if (kOwnRows || kb + 1 < nkb) issue(q);
+      const int done = q;
       q = q + 1 == S ? 0 : q + 1;
-      if (kb + 1 < nkb) read(0, q, 0);
-      multiply(1);
+      // (after the item's last block this reads the next item's first fragments,
+      // which are read again behind the epilogue: one form of the loop's body)
+      multiply(1, q, 0);
+      last = done;
     }
 
     // ---- epilogue ----
+    // (the lane's indices made anew, opaque to the compiler: it would otherwise
+    // keep offsets made from them in registers through the K loop)
+    uint32_t lane_again = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane_again));
+    const int lane = (int)lane_again, l16 = lane & 15, lq = lane >> 4;
+    // (and its parameters read anew from the kernel's arguments, for the same reason)
+    typedef const __attribute__((address_space(4))) GemmParams* Args;
+    Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(args));
+    Epilogue ep;
+    __builtin_memcpy(&ep, (const Epilogue*)&args->epi, sizeof(ep));
+    // 16 rows at a time: the wave's sums go to LDS as the MFMA leaves them and
+    // come back as rows, 8 consecutive columns per lane
+    {
+      typedef __attribute__((address_space(3))) v4f* lp;
+      const uint32_t so = kOwnRows ? lds0 + S * STAGE + wave * 16 * RS : lds0 + last * STAGE + wave * (STAGE / NW);
+      const int m0w = wm * OpA::WTX, n = cur.n0 + wn * OpB::WTX + 8 * (lane % LPR);
+      const int rows = min(BM, p.m - cur.m0);
+      const bool lines = p.splits == 1 && ep.vec8;  // whole lines, 16 bytes per lane
+      const epi::Rows er = epi::rows_of(ep, cur.m0, rows, p.n);
+      float bias[8];
+      {
+        const v4f b0 = epi::bias4(ep, n, p.n), b1 = epi::bias4(ep, n + 4, p.n);
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      const int n = cur.n0 + wn * OpB::WTX + 16 * i + 4 * lq;
-      if (n >= p.n) continue;
-      const v4f bias = p.splits > 1 ? v4f{0.f, 0.f, 0.f, 0.f} : epi::bias4(p.epi, n, p.n);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        const int m = cur.m0 + wm * OpA::WTX + 16 * j + l16;
-        if (m >= p.m) continue;
-        if (p.splits > 1) {
-          float* w = p.ws + cur.split * p.ws_stride + (int64_t)m * p.n + n;
-          if (p.n % 4 == 0) {
-            *reinterpret_cast<v4f*>(w) = acc[i][j];
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (n + r < p.n) w[r] = acc[i][j][r];
-          }
-        } else {
-          epi::finish4(p.epi, m, n, p.n, acc[i][j] + bias);
+        for (int e = 0; e < 4; ++e) {
+          bias[e] = b0[e];
+          bias[4 + e] = b1[e];
         }
       }
+      // residual rows are loaded kAhead rows of fragments before their use: a
+      // load waits for the stores before it
+      constexpr int kAhead = FM < 4 ? FM : 4;
+      epi::v4i res[kAhead][ROUNDS];
+      auto load_res = [&](int j, epi::v4i* to) {
+#pragma unroll
+        for (int h = 0; h < ROUNDS; ++h) {
+          const int m = m0w + 16 * j + RPR * h + lane / LPR;
+          to[h] = epi::residual8(ep, er, m, n, j < FM && m < rows && n < p.n);
+        }
+      };
+      const bool ahead = lines && ep.res;
+      if (ahead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) load_res(j, res[j]);
+      }
+      // partial sums, and rows that do not start on 16-byte boundaries
+      auto finish_some = [&](int m, int n, const float* v, const float* bias) {
+#pragma unroll 1
+        for (int c = 0; c < 2 && n + 4 * c < p.n; ++c) {
+          v4f x, b;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = c ? v[4 + e] : v[e];
+            b[e] = c ? bias[4 + e] : bias[e];
+          }
+          if (p.splits == 1) {
+            epi::finish4(ep, cur.m0 + m, n + 4 * c, p.n, x + b);
+          } else {
+            float* w = p.ws + cur.split * p.ws_stride + (int64_t)(cur.m0 + m) * p.n + n + 4 * c;
+            if (p.n % 4 == 0) {
+              *reinterpret_cast<v4f*>(w) = x;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n + 4 * c + e < p.n) w[e] = x[e];
+            }
+          }
+        }
+      };
+      // (the outer loop is not unrolled: one copy of the epilogue's code per kAhead rows)
+#pragma unroll 1
+      for (int jo = 0; jo < FM; jo += kAhead) {
+#pragma unroll
+        for (int ji = 0; ji < kAhead; ++ji) {
+          const int j = jo + ji;
+#pragma unroll
+          for (int jc = ji; jc < FM; jc += kAhead)
+            if (jc == j) {
+#pragma unroll
+              for (int i = 0; i < FN; ++i)
+                *(lp)(uintptr_t)(so + l16 * RS + (((4 * i + lq) ^ (l16 & (RC - 1))) << 4)) = acc[i][jc];
+            }
+          dma::lds_done();
+          float v[ROUNDS][8];
+#pragma unroll
+          for (int h = 0; h < ROUNDS; ++h) {
+            const int r = RPR * h + lane / LPR;
+            const uint32_t a = so + r * RS, c = 2 * (lane % LPR), x = r & (RC - 1);
+            const v4f lo = *(lp)(uintptr_t)(a + ((c ^ x) << 4)), hi = *(lp)(uintptr_t)(a + (((c + 1) ^ x) << 4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[h][e] = lo[e];
+              v[h][4 + e] = hi[e];
+            }
+          }
+          dma::lds_done();  // before the next rows take their place
+          epi::v4i rs[ROUNDS];
+#pragma unroll
+          for (int h = 0; h < ROUNDS; ++h) rs[h] = res[ji][h];
+          if (ahead) load_res(j + kAhead, res[ji]);
+#pragma unroll
+          for (int h = 0; h < ROUNDS; ++h) {
+            const int m = m0w + 16 * j + RPR * h + lane / LPR;
+            if (lines) {
+              epi::finish8(ep, er, m, n, m < rows && n < p.n, v[h], bias, rs[h]);
+            } else if (m < rows) {
+              finish_some(m, n, v[h], bias);
+            }
+          }
+        }
+      }
+      if constexpr (!kOwnRows) {
+        dma::barrier();  // every wave is done with the slot
+        issue(last);
+      }
+      const int per = !lines ? 0 : (ep.out_f32 ? 2 : 1) + (ep.pre ? 1 : 0);
+      stores = per <= 2 ? per : 0;
     }
     cur = next(ct);
   }
@@ -292,25 +420,24 @@ template <int TILE>
 hipError_t launch_layout(int layout, const GemmParams& p, int grid, hipStream_t stream) {
   if (layout == kNT) return launch_tile<TILE, false, false>(p, grid, stream);
   if (layout == kNN) return launch_tile<TILE, false, true>(p, grid, stream);
-  if constexpr (gemm_has(kTN, TILE)) return launch_tile<TILE, true, true>(p, grid, stream);
-  return hipErrorInvalidValue;
+  return launch_tile<TILE, true, true>(p, grid, stream);
 }
 
 // ---- the activation's backward pass and the bias gradient ----
-// A workgroup takes 256 columns x kBiasRows rows: 32 lanes of 8 columns by 8
-// rows in flight; the column sums of its 8 row lanes meet in LDS.  Bound by
+// A workgroup takes 256 columns x p.rows rows: 32 lanes of 8 columns by 8 rows in
+// flight; the column sums of its 8 row lanes meet in LDS.  Bound by
 // HBM: dc and pre read, dpre written, once.
 __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
   __shared__ float sum[8][256];
   const int lx = threadIdx.x & 31, ly = threadIdx.x >> 5;
   const int c = blockIdx.x * 256 + lx * 8;
-  const int r0 = blockIdx.y * kBiasRows;
+  const int r0 = blockIdx.y * p.rows;
   float s[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) s[e] = 0.f;
   if (c < p.ldp) {
 #pragma unroll 2
-    for (int r = r0 + ly; r < min(p.m, r0 + kBiasRows); r += 8) {
+    for (int r = r0 + ly; r < min(p.m, r0 + p.rows); r += 8) {
       float d[8], x[8];
       const uint16_t* dc = p.dc + (int64_t)r * p.lddc + c;
       const uint16_t* pr = p.pre ? p.pre + (int64_t)r * p.ldpre + c : nullptr;
@@ -339,9 +466,9 @@ __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
         }
       }
       uint32_t o[4];
+      if (pr) act::times_grad<8>(d, x, p.act);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (pr) d[e] *= act::grad(x[e], p.act);
         if (c + e >= p.n) d[e] = 0.f;  // the padding columns
         s[e] += d[e];
       }
@@ -365,12 +492,19 @@ __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
   }
 }
 
+// 64 columns per workgroup; its four waves sum a quarter of the chunks each.
 __global__ __launch_bounds__(256) void bias_sum_kernel(const float* partial, float* dbias, int chunks, int n) {
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= n) return;
+  __shared__ float sum[4][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane, per = (chunks + 3) / 4;
   float v = 0.f;
-  for (int k = 0; k < chunks; ++k) v += partial[(int64_t)k * n + c];
-  dbias[c] = v;
+  if (c < n) {
+#pragma unroll 8
+    for (int k = wave * per; k < min(chunks, (wave + 1) * per); ++k) v += partial[(int64_t)k * n + c];
+  }
+  sum[wave][lane] = v;
+  __syncthreads();
+  if (wave == 0 && c < n) dbias[c] = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
 }
 
 }  // namespace
@@ -381,18 +515,19 @@ hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipS
     case 1: return launch_layout<1>(layout, p, grid, stream);
     case 2: return launch_layout<2>(layout, p, grid, stream);
     case 3: return launch_layout<3>(layout, p, grid, stream);
+    case 4: return launch_layout<4>(layout, p, grid, stream);
     default: return hipErrorInvalidValue;
   }
 }
 
 hipError_t launch_dact(const DactParams& p, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.ldp + 255) / 256), (unsigned)((p.m + kBiasRows - 1) / kBiasRows));
+  const dim3 grid((unsigned)((p.ldp + 255) / 256), (unsigned)((p.m + p.rows - 1) / p.rows));
   dact_kernel<<<grid, 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_bias_sum(const float* partial, float* dbias, int chunks, int n, hipStream_t stream) {
-  bias_sum_kernel<<<(n + 255) / 256, 256, 0, stream>>>(partial, dbias, chunks, n);
+  bias_sum_kernel<<<(n + 63) / 64, 256, 0, stream>>>(partial, dbias, chunks, n);
   return hipGetLastError();
 }
 

@@ -25,7 +25,7 @@ from tests.parity import say
 pytestmark = pytest.mark.gpu
 BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
 ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
-TILES = ["256x256x2x4", "256x128x4x2", "128x128x2x2", "64x128x2x2"]
+TILES = ["256x256x2x4", "256x128x4x2", "128x128x2x2", "64x128x2x2", "64x64x2x2"]
 
 
 @pytest.fixture(scope="module")
@@ -240,8 +240,7 @@ def test_backward_tiles(dg, force, tile, splits):
     force(tile, splits)
     say(f"linear backward tile {tile} splits={splits}")
     for m, n, k in ((300, 260, 392), (713, 333, 264)):
-        # (the 64-row tile has no form for db)
-        backward_case(dg, m, n, k, "silu", which=(True, not tile.startswith("64"), True))
+        backward_case(dg, m, n, k, "silu")
 
 
 @pytest.mark.parametrize("which", [(True, False, False), (False, True, False), (False, False, True)])
@@ -305,7 +304,7 @@ def test_graph_and_side_stream(dg):
     out, pre = torch.empty((m, n), dtype=BF16, device="cuda"), torch.empty((m, n), dtype=BF16, device="cuda")
     dout = torch.randn((m, n), generator=g, device="cuda").to(BF16)
     da, db, dbias = torch.empty_like(a), torch.empty_like(b), torch.empty(n, device="cuda")
-    ws = torch.empty(2 * m * n + 4 * 2 * n + 64, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(dg.gemm_bf16_nt_epilogue_backward_workspace(m, n), dtype=torch.uint8, device="cuda")
 
     def step():
         dg.gemm_bf16_nt_epilogue(a, b, out, None, "gelu", None, pre)
