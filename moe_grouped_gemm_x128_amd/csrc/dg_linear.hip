@@ -60,63 +60,106 @@ dg_status make_epilogue(void* c, int64_t ldc, int c_type, const dg_epilogue* in,
   return DG_SUCCESS;
 }
 
-// Tile and K splits of a tile GEMM: the least modelled time
-//   passes over the CUs x (K blocks x time per block + fixed time per item)
-//   + (split) the partials' write, their read and the second launch.
-// Times per block from the rate a tile reaches on full CUs.
+// The model behind the choice of tile and K splits, in microseconds:
+//   passes over the workgroups x (K blocks x time per block + fixed time per
+//   item) + (split) the partials' write and read and the second launch.
+// Rates (TFLOP/s of the whole card on full CUs), the share of a block's time
+// that a workgroup alone on a CU needs where two would share it, and the other
+// constants are fitted to a sweep of every tile and split over nine shapes
+// from 100 x 2112 x 7168 to 4096 x 7168 x 16384 (chosen within 10% of the best).
+constexpr double kTileRate[kNumGemmTiles] = {1350., 1050., 1080., 900., 600.};
+constexpr double kAlone = 0.75, kItemUs = 3.0, kSplitUs = 4.0, kPartialBytesPerUs = 8e6;
+
+double block_us(int tile, int cus, bool alone) {
+  const GemmTile g = kGemmTiles[tile];
+  const int res = gemm_residents(tile);
+  const double us = 2.0 * g.bm * g.bn * 64 * cus * res / (kTileRate[tile] * 1e6);
+  return alone && res > 1 ? us * kAlone : us;
+}
+
+bool forced_out(const GemmTile& g) {  // DG_FORCE_TILE names another tile
+  const char* force = std::getenv("DG_FORCE_TILE");
+  int bm, bn, wm, wn;
+  return force && *force && std::sscanf(force, "%dx%dx%dx%d", &bm, &bn, &wm, &wn) == 4 &&
+         !(bm == g.bm && bn == g.bn && wm == g.wm && wn == g.wn);
+}
+
 struct Plan {
   int tile, splits, kchunk;
+  double us;
 };
 
-Plan plan(int layout, int m, int n, int k, int cus, bool may_split) {
-  // TFLOP/s of the whole card when every CU works on this tile
-  static const double rate[kNumGemmTiles] = {1350., 1150., 1080., 850., 600.};
+Plan plan(int m, int n, int k, int cus, bool may_split) {
   const int blocks = ceil_div(k, 64);
-  const char* force = std::getenv("DG_FORCE_TILE");
   const char* fsplit = std::getenv("DG_FORCE_SPLITS");
-  Plan best{-1, 1, blocks};
-  double best_us = 1e300;
+  const bool force = fsplit && *fsplit && may_split;
+  Plan best{-1, 1, blocks, 1e300};
   for (int t = 0; t < kNumGemmTiles; ++t) {
     const GemmTile g = kGemmTiles[t];
-    if (force && *force) {
-      int bm, bn, wm, wn;
-      if (std::sscanf(force, "%dx%dx%dx%d", &bm, &bn, &wm, &wn) == 4 &&
-          !(bm == g.bm && bn == g.bn && wm == g.wm && wn == g.wn))
-        continue;
-    }
-    const double tiles = (double)ceil_div(m, g.bm) * ceil_div(n, g.bn);
-    const int res = gemm_residents(t);
-    const double block_us = 2.0 * g.bm * g.bn * 64 * cus * res / (rate[t] * 1e6);
+    if (forced_out(g)) continue;
+    const int64_t tiles = (int64_t)ceil_div(m, g.bm) * ceil_div(n, g.bn);
+    const int64_t slots = (int64_t)cus * gemm_residents(t);
     for (int s = 1; s <= 16; ++s) {
-      if (fsplit && *fsplit && may_split && s != std::atoi(fsplit)) continue;
+      if (force && s != std::atoi(fsplit)) continue;
       if (s > 1 && (!may_split || blocks < s)) break;
       const int chunk = ceil_div(blocks, s);
       if (ceil_div(blocks, chunk) != s) continue;  // a split would be empty
       const double bytes = 4.0 * s * m * n;
-      if (s > 1 && (bytes > 256e6 || (chunk < 4 && !(fsplit && *fsplit)))) break;
-      const double passes = (double)ceil_div((int64_t)(tiles * s), (int64_t)cus * res);
-      double us = passes * (chunk * block_us + 3.0 * res);
-      if (s > 1) us += 4.0 + 2.0 * bytes / 4e6;
-      if (us < best_us) {
-        best_us = us;
-        best = Plan{t, s, chunk};
-      }
+      if (s > 1 && (bytes > 256e6 || (chunk < 4 && !force))) break;
+      const double passes = (double)((tiles * s + slots - 1) / slots);
+      double us = passes * (chunk * block_us(t, cus, tiles * s <= cus) + kItemUs * gemm_residents(t));
+      if (s > 1) us += kSplitUs + 2.0 * bytes / kPartialBytesPerUs;
+      if (us < best.us) best = Plan{t, s, chunk, us};
     }
   }
   return best;
 }
 
+// da and db in one launch: the tile, and how many of its workgroups da gets.
+struct PairPlan {
+  int tile, first, grid;
+  double us;
+};
+
+PairPlan plan_pair(const GemmParams& nn, const GemmParams& tn, int cus) {
+  PairPlan best{-1, 0, 0, 1e300};
+  for (int t = 0; t < kNumGemmTiles; ++t) {
+    const GemmTile g = kGemmTiles[t];
+    if (forced_out(g)) continue;
+    const int64_t ta = (int64_t)ceil_div(nn.m, g.bm) * ceil_div(nn.n, g.bn);
+    const int64_t tb = (int64_t)ceil_div(tn.m, g.bm) * ceil_div(tn.n, g.bn);
+    if (ta > (1 << 24) || tb > (1 << 24)) continue;
+    const int64_t slots = (int64_t)(cus > 16 ? cus / 8 * 8 : 16) * gemm_residents(t);
+    const int ka = ceil_div(nn.k, 64), kb = ceil_div(tn.k, 64);
+    const double blk = block_us(t, cus, ta + tb <= cus), item = kItemUs * gemm_residents(t);
+    for (int passes = 1; passes <= 16; ++passes) {  // of da's workgroups
+      const int64_t first = (ceil_div(ta, passes) + 7) / 8 * 8;
+      if (first >= slots) continue;
+      int64_t rest = slots - first;
+      if (rest > tb) rest = (tb + 7) / 8 * 8;
+      const double a = (double)((ta + first - 1) / first) * (ka * blk + item);
+      const double b = (double)((tb + rest - 1) / rest) * (kb * blk + item);
+      const double us = a > b ? a : b;
+      if (us < best.us) best = PairPlan{t, (int)first, (int)(first + rest), us};
+    }
+  }
+  return best;
+}
+
+void set_tiles(GemmParams& p, const GemmTile& g, int splits, int kchunk) {
+  p.tiles_m = ceil_div(p.m, g.bm);
+  p.tiles_n = ceil_div(p.n, g.bn);
+  p.splits = splits;
+  p.kchunk = kchunk;
+}
+
 // One tile GEMM with its epilogue (arguments checked).
-dg_status gemm(int layout, GemmParams& p, int cus, hipStream_t stream) {
-  const bool may_split = !is_capturing(stream);
+dg_status gemm(int layout, GemmParams& p, int cus, bool may_split, hipStream_t stream) {
   for (int attempt = 0; attempt < 2; ++attempt) {
-    const Plan c = plan(layout, p.m, p.n, p.k, cus, may_split && attempt == 0);
+    const Plan c = plan(p.m, p.n, p.k, cus, may_split && attempt == 0);
     if (c.tile < 0) return DG_ERROR_UNSUPPORTED;
     const GemmTile g = kGemmTiles[c.tile];
-    p.tiles_m = ceil_div(p.m, g.bm);
-    p.tiles_n = ceil_div(p.n, g.bn);
-    p.splits = c.splits;
-    p.kchunk = c.kchunk;
+    set_tiles(p, g, c.splits, c.kchunk);
     const int64_t items = (int64_t)p.tiles_m * p.tiles_n * c.splits;
     if (items > (1 << 30)) return DG_ERROR_UNSUPPORTED;
     // a multiple of 8 workgroups: the ids of a workgroup stay on its XCD's run
@@ -193,7 +236,7 @@ dg_status dg_gemm_bf16_nt_epilogue(const void* a, int64_t lda, const void* b, in
   p.n = n;
   p.k = k;
   p.epi = e;
-  return gemm(kNT, p, cus, stream);
+  return gemm(kNT, p, cus, !is_capturing(stream), stream);
 }
 
 dg_status dg_gemm_fp8_nt_epilogue(const void* a, const float* sa, const void* b, const float* sb, void* c, int64_t ldc,
@@ -272,36 +315,52 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
       return DG_ERROR_LAUNCH;
   }
   const uint8_t* g = in_place ? static_cast<const uint8_t*>(dc) : reinterpret_cast<const uint8_t*>(dpre);
+  GemmParams nn{}, tn{};
   if (da) {
-    GemmParams p{};
-    p.a = g;
-    p.lda = 2 * ldp;
-    p.b = static_cast<const uint8_t*>(b);
-    p.ldb = 2 * ldb;
-    p.wb = k;
-    p.m = m;
-    p.n = k;
-    p.k = n;
-    const dg_status st = make_epilogue(da, ldda, DG_TYPE_BF16, nullptr, k, &p.epi);
+    nn.a = g;
+    nn.lda = 2 * ldp;
+    nn.b = static_cast<const uint8_t*>(b);
+    nn.ldb = 2 * ldb;
+    nn.wb = k;
+    nn.m = m;
+    nn.n = k;
+    nn.k = n;
+    const dg_status st = make_epilogue(da, ldda, DG_TYPE_BF16, nullptr, k, &nn.epi);
     if (st != DG_SUCCESS) return st;
-    const dg_status r = gemm(kNN, p, cus, stream);
-    if (r != DG_SUCCESS) return r;
   }
   if (db) {
-    GemmParams p{};
-    p.a = g;
-    p.lda = 2 * ldp;
-    p.wa = (int)round8(n);
-    p.b = static_cast<const uint8_t*>(a);
-    p.ldb = 2 * lda;
-    p.wb = k;
-    p.m = n;
-    p.n = k;
-    p.k = m;
-    const dg_status st = make_epilogue(db, lddb, DG_TYPE_BF16, nullptr, k, &p.epi);
+    tn.a = g;
+    tn.lda = 2 * ldp;
+    tn.wa = (int)round8(n);
+    tn.b = static_cast<const uint8_t*>(a);
+    tn.ldb = 2 * lda;
+    tn.wb = k;
+    tn.m = n;
+    tn.n = k;
+    tn.k = m;
+    const dg_status st = make_epilogue(db, lddb, DG_TYPE_BF16, nullptr, k, &tn.epi);
     if (st != DG_SUCCESS) return st;
-    return gemm(kTN, p, cus, stream);
   }
+  const bool may_split = !is_capturing(stream);
+  if (da && db) {
+    const PairPlan c = plan_pair(nn, tn, cus);
+    const Plan ca = plan(nn.m, nn.n, nn.k, cus, may_split), cb = plan(tn.m, tn.n, tn.k, cus, may_split);
+    // (two launches where splitting K gains more than sharing the card)
+    if (c.tile >= 0 && c.us <= ca.us + cb.us) {
+      const GemmTile tile = kGemmTiles[c.tile];
+      set_tiles(nn, tile, 1, ceil_div(nn.k, 64));
+      set_tiles(tn, tile, 1, ceil_div(tn.k, 64));
+      if (std::getenv("DG_LOG"))
+        std::fprintf(stderr, "[dg] linear backward m=%d n=%d k=%d -> tile %dx%d first=%d grid=%d\n", m, n, k, tile.bm,
+                     tile.bn, c.first, c.grid);
+      return launch_gemm_pair(c.tile, nn, tn, c.first, c.grid, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+    }
+  }
+  if (da) {
+    const dg_status r = gemm(kNN, nn, cus, may_split, stream);
+    if (r != DG_SUCCESS) return r;
+  }
+  if (db) return gemm(kTN, tn, cus, may_split, stream);
   return DG_SUCCESS;
 }
 

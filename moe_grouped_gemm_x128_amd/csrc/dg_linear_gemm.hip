@@ -22,7 +22,7 @@
 //
 // The MFMA takes B rows first and A rows second: a lane holds 4 consecutive
 // columns of one row of C.
-#include <type_traits>
+#include <cstddef>
 
 #include "dg_dma.h"
 #include "dg_linear.h"
@@ -132,8 +132,14 @@ struct Operand {
   }
 };
 
-template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB>
-__global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmParams p) {
+// LDS of a workgroup: the ring, and the epilogue's rows where they are its own.
+template <int BM, int BN, int WM, int WN, int S>
+constexpr int kLds = S * (BM + BN) * 128 + (S == 2 ? WM * WN * 16 * (BN / WN) * 4 : 0);
+
+// The items of one product that workgroup `wg` of `nwg` computes.  `p` is the
+// kernel's argument at byte ARG.
+template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int ARG>
+__device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, uint8_t* smem) {
   constexpr int NW = WM * WN;
   using OpA = Operand<BM, WM, NW, TA>;
   using OpB = Operand<BN, WN, NW, TB>;
@@ -149,7 +155,6 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmPar
   constexpr int kBehind = kOwnRows ? S - 1 : S - 2;  // blocks of the next item loaded before the stores
   static_assert(kOwnRows || 16 * RS <= STAGE / NW, "a wave's rows fit its share of the slot");
   static_assert((S - 2) * LOADS + 2 * kStores < 64, "vmcnt range");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + (kOwnRows ? NW * 16 * RS : 0)];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = (int)uniform(tid >> 6);
@@ -185,20 +190,20 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmPar
     return x;
   };
   // (an id that maps past the items is followed by live ones of other XCDs'
-  // runs: a workgroup's own ids t, t + grid, ... with grid a multiple of 8
+  // runs: a workgroup's own ids t, t + nwg, ... with nwg a multiple of 8
   // stay on one XCD's run and end together)
   auto next = [&](int& t) {
     Item x = decode(t);
     while (!x.live && t < per_xcd * 8) {
-      t += gridDim.x;
+      t += nwg;
       x = decode(t);
     }
-    t += gridDim.x;
+    t += nwg;
     return x;
   };
 
   // ---- the stream of K blocks over the workgroup's items ----
-  int lt = blockIdx.x;
+  int lt = wg;
   Item li{};
   const uint8_t *pa = nullptr, *pb = nullptr;
   int left = 0;
@@ -221,7 +226,7 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmPar
     }
   };
 
-  int ct = blockIdx.x;
+  int ct = wg;
   Item cur = next(ct);
   if (!cur.live) return;
   enter();
@@ -293,7 +298,7 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmPar
     const int lane = (int)lane_again, l16 = lane & 15, lq = lane >> 4;
     // (and its parameters read anew from the kernel's arguments, for the same reason)
     typedef const __attribute__((address_space(4))) GemmParams* Args;
-    Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+    Args args = (Args)((const __attribute__((address_space(4))) uint8_t*)__builtin_amdgcn_kernarg_segment_ptr() + ARG);
     asm volatile("" : "+s"(args));
     Epilogue ep;
     __builtin_memcpy(&ep, (const Epilogue*)&args->epi, sizeof(ep));
@@ -409,6 +414,30 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmPar
   dma::wait<0>();  // no load outlives the workgroup
 }
 
+template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB>
+__global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds<BM, BN, WM, WN, S>];
+  run_items<BM, BN, WM, WN, S, TA, TB, 0>(p, blockIdx.x, gridDim.x, smem);
+}
+
+// The two products of the backward pass in one launch: workgroups below
+// `first` compute da (NN), the others db (TN).  Neither fills the card by
+// itself as well as both do together (4096 x 7168 x 2048 on 256x256 tiles: 128
+// tiles of 112 blocks beside 224 of 64), and small ones overlap whole.
+struct PairParams {
+  GemmParams nn, tn;
+  int first;
+};
+template <int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(WM * WN * 64) void linear_gemm_pair_kernel(const PairParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds<BM, BN, WM, WN, S>];
+  if ((int)blockIdx.x < p.first)
+    run_items<BM, BN, WM, WN, S, false, true, offsetof(PairParams, nn)>(p.nn, blockIdx.x, p.first, smem);
+  else
+    run_items<BM, BN, WM, WN, S, true, true, offsetof(PairParams, tn)>(p.tn, blockIdx.x - p.first,
+                                                                       gridDim.x - p.first, smem);
+}
+
 template <int TILE, bool TA, bool TB>
 hipError_t launch_tile(const GemmParams& p, int grid, hipStream_t stream) {
   constexpr GemmTile t = kGemmTiles[TILE];
@@ -421,6 +450,13 @@ hipError_t launch_layout(int layout, const GemmParams& p, int grid, hipStream_t 
   if (layout == kNT) return launch_tile<TILE, false, false>(p, grid, stream);
   if (layout == kNN) return launch_tile<TILE, false, true>(p, grid, stream);
   return launch_tile<TILE, true, true>(p, grid, stream);
+}
+
+template <int TILE>
+hipError_t launch_both(const PairParams& p, int grid, hipStream_t stream) {
+  constexpr GemmTile t = kGemmTiles[TILE];
+  linear_gemm_pair_kernel<t.bm, t.bn, t.wm, t.wn, t.stages><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
+  return hipGetLastError();
 }
 
 // ---- the activation's backward pass and the bias gradient ----
@@ -516,6 +552,19 @@ hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipS
     case 2: return launch_layout<2>(layout, p, grid, stream);
     case 3: return launch_layout<3>(layout, p, grid, stream);
     case 4: return launch_layout<4>(layout, p, grid, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_gemm_pair(int tile, const GemmParams& nn, const GemmParams& tn, int first, int grid,
+                            hipStream_t stream) {
+  const PairParams p{nn, tn, first};
+  switch (tile) {
+    case 0: return launch_both<0>(p, grid, stream);
+    case 1: return launch_both<1>(p, grid, stream);
+    case 2: return launch_both<2>(p, grid, stream);
+    case 3: return launch_both<3>(p, grid, stream);
+    case 4: return launch_both<4>(p, grid, stream);
     default: return hipErrorInvalidValue;
   }
 }
