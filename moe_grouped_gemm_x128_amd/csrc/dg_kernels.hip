@@ -294,7 +294,7 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
   // bf16 epilogue staging: a wave's 16-row fragment row goes through LDS so
   // that each store covers whole (64 columns) or half (32 columns) 128-byte
   // lines; rows padded by 16 bytes against bank conflicts
-  constexpr bool kStage = !kFp32Out && !kSwiGLU && !kLinear && (WTN == 64 || WTN == 32);
+  constexpr bool kStage = !kFp32Out && !kSwiGLU && (WTN == 64 || WTN == 32);
   constexpr int kStageRow = WTN * 2 + 16;
   __shared__ __attribute__((aligned(16))) uint8_t sOut[kStage ? NW : 1][kStage ? 16 * kStageRow : 16];
   // fused SwiGLU: each wave's |h| maximum over its columns, per tile row
@@ -539,9 +539,11 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
   // (not for the fp32 D kinds: their row-scale registers leave no room for
   // it; staged layouts: bf16 with N % 8 == 0 only, split-K partials take the
   // per-fragment path with the conservative wait)
-  const bool staged = kStage && !(kCanSplit && splits > 1) && p.vec_out && (p.n % 8 == 0);
+  // (the linear layer's epilogue: whole lines of a bf16 C, no stored pre)
+  const bool staged = kStage && !(kCanSplit && splits > 1) && p.vec_out && (p.n % 8 == 0) &&
+                      (!kLinear || (p.epi.vec8 && !p.epi.out_f32 && !p.epi.pre));
   // (nor for the linear layer, whose epilogue loads and stores what it is asked to)
-  const bool exact_stores = kExactFits && !(kLinear && splits == 1) && (kStage ? staged : (!kFp32Out || (kCanSplit && splits > 1))) &&
+  const bool exact_stores = kExactFits && (!kLinear || splits > 1 || staged) && (kStage ? staged : (!kFp32Out || (kCanSplit && splits > 1))) &&
                             p.vec_out && (int64_t)BM * p.n * 4 < 0x7fffffffLL;
   bool stores_pending = false;  // the previous tile's epilogue stores may be in flight
 
@@ -1043,8 +1045,45 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
       constexpr int kRounds = 16 / kRowsPerRound;   // 2 or 1
       uint8_t* so = sOut[kStage ? wave : 0];
       const uint32_t sbase = lds_addr(so);
+      const uint32_t ldo = kLinear ? (uint32_t)p.epi.ldc : (uint32_t)p.n;  // elements between output rows
       const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(static_cast<uint16_t*>(p.out) + out_row0 * p.n), (short)0, (int)((uint32_t)BM * p.n * 2), 0x00020000);
+          (void*)(static_cast<uint16_t*>(p.out) + out_row0 * (int64_t)ldo), (short)0,
+          (int)(kLinear ? ((uint32_t)(rows - 1) * ldo + p.n) * 2 : (uint32_t)BM * p.n * 2), 0x00020000);
+      if constexpr (kLinear) {
+        // bias, activation and residual where the MFMA leaves the sums, before
+        // the first store (a load behind a store waits for it); the residual in
+        // 8-byte loads, 4 columns of a row, a few fragment rows at a time
+        constexpr int kBatch = FM % 4 == 0 ? 4 : FM % 3 == 0 ? 3 : FM % 2 == 0 ? 2 : 1;
+        v4f bias[FN];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) bias[i] = epi::bias4(p.epi, n0 + wn * WTN + 16 * i + 4 * lq, p.n);
+#pragma unroll
+        for (int j0 = 0; j0 < FM; j0 += kBatch) {
+          uint2 rv[kBatch][FN];
+          if (p.epi.res) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const int ml = wm * WTM + 16 * (j0 + j) + l16;
+              const uint16_t* rp = p.epi.res + (out_row0 + (ml < rows ? ml : 0)) * p.epi.ldr;
+#pragma unroll
+              for (int i = 0; i < FN; ++i) {
+                const int n = n0 + wn * WTN + 16 * i + 4 * lq;
+                rv[j][i] = *reinterpret_cast<const uint2*>(rp + (n < p.n ? n : 0));
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+              v4f& v = acc[i][j0 + j];
+              v += bias[i];
+              act::apply<4>(v, p.epi.act);
+              if (p.epi.res) v += epi::unpack4(rv[j][i]);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
       const int rl = lane / kLanesPerRow, cb = (lane % kLanesPerRow) * 16;  // read-back row and byte
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
@@ -1065,7 +1104,7 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
           else
             row_ok = ml < rows;
           const int n = n0 + wn * WTN + cb / 2;  // 8 columns, all valid or none (N % 8 == 0)
-          const uint32_t off = (row_ok && n < p.n) ? ((uint32_t)ml * p.n + n) * 2u : 0x80000000u;
+          const uint32_t off = (row_ok && n < p.n) ? ((uint32_t)ml * ldo + n) * 2u : 0x80000000u;
           __builtin_amdgcn_raw_buffer_store_b128(v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w}, ro, off, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);  // one fragment row at a time (registers)

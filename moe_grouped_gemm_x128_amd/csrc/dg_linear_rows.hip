@@ -1,10 +1,12 @@
 // dg_linear_rows.hip -- the linear layer for few rows (M <= 64: decode steps,
 // router logits): C = act(A.B^T + bias) + residual, bound by reading B once.
 //
-// A workgroup owns 32 columns of C (the stream's groups A and B are 16 rows of
-// B each) and all rows of A; its waves take units of 256 bytes of K round robin
-// (dg_stream.h) and meet once in LDS.  No second kernel and no workspace: the
-// split over K is inside the workgroup.
+// A workgroup owns 32 columns of C (the stream's groups are 16 rows of B each)
+// and all rows of A; its waves take units of 256 bytes of K round robin
+// (dg_stream.h) and meet once in LDS.  Where 32 columns each would leave half of
+// the CUs idle it owns 16 (the groups are two lines of K of the same rows): more
+// CUs load, though each loads A once more.  No second kernel and no
+// workspace: the split over K is inside the workgroup.
 #include "dg_linear.h"
 #include "dg_stream.h"
 
@@ -32,7 +34,7 @@ struct RowsCursor {
       // (the unit's second line of 128 may lie past the row's last block: its
       // operand bytes and its scales then read zero)
       u.s = p->sb + 2 * kb;
-      u.srange = u.so[1] + (u.kbytes > 128 ? 8u : 4u);
+      u.srange = u.kbytes > 128 ? 8 : 4;
       u.xs = p->sa + 2 * kb;
       u.xsrange = (uint32_t)((p->m - 1) * (p->k >> 7)) * 4u + (u.kbytes > 128 ? 8u : 4u);
     }
@@ -51,15 +53,16 @@ struct RowsCursor {
   }
 };
 
-template <int MODE, int NT, int W, int D>
+template <int MODE, int NT, bool SAME, int W, int D>
 __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(MODE, W, D)];
   // the waves' sums meet where the ring was
-  static_assert(ring_bytes(MODE, W, D) >= W * 2 * NT * 1024, "the sums fit the ring");
-  v4f(*red)[2 * NT][64] = reinterpret_cast<v4f(*)[2 * NT][64]>(ring);
+  constexpr int G = SAME ? 1 : 2;  // groups of 16 columns
+  static_assert(ring_bytes(MODE, W, D) >= W * G * NT * 1024, "the sums fit the ring");
+  v4f(*red)[G * NT][64] = reinterpret_cast<v4f(*)[G * NT][64]>(ring);
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
-  const int n0 = blockIdx.x * 32;
+  const int n0 = blockIdx.x * 16 * G;
 
   RowsCursor c{};
   c.p = &p;
@@ -71,15 +74,21 @@ __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p)
   c.u.tiles = NT;
   c.u.ra = min(16, p.n - n0);
   c.u.rb = min(16, p.n - n0 - 16);
+  c.u.so[1] = SAME ? 4 : 0;
   c.u.wrow = (uint32_t)p.ldb;
   RowsParams q = p;
   if constexpr (MODE == kFp8) {
-    q.sb = p.sb + (int64_t)(n0 >> 7) * (p.k >> 7);  // 32 columns lie in one block of 128
+    q.sb = p.sb + (int64_t)(n0 >> 7) * (p.k >> 7);  // the workgroup's columns lie in one block of 128
     c.p = &q;
   }
   c.place();
   const int mine = c.nb > wave ? (c.nb - wave + W - 1) / W : 0;
-  Pipe<MODE, D, true, RowsCursor> pipe;
+  // what the epilogue reads, asked for before the stream: its latency is hidden
+  const int em = 16 * (wave / G) + l16, en = n0 + 16 * (wave % G) + 4 * lq;  // wave's first group of sums
+  const bool mine_out = wave < G * NT && em < p.m && en < p.n;
+  v4f bias = v4f{0.f, 0.f, 0.f, 0.f};
+  if (mine_out) bias = epi::bias4(p.epi, en, p.n);
+  Pipe<MODE, D, true, SAME, RowsCursor> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
   v4f a[NT], b[NT];
 #pragma unroll
@@ -89,39 +98,45 @@ __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p)
   dma::barrier();   // on any wave
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    red[wave][2 * t][lane] = a[t];
-    red[wave][2 * t + 1][lane] = b[t];
+    if constexpr (SAME) {
+      red[wave][t][lane] = a[t] + b[t];
+    } else {
+      red[wave][2 * t][lane] = a[t];
+      red[wave][2 * t + 1][lane] = b[t];
+    }
   }
   __syncthreads();
-  for (int s = wave; s < 2 * NT; s += W) {
-    v4f v = red[0][s][lane];
+  static_assert(G * NT <= W, "one group of sums per wave");
+  if (mine_out) {
+    v4f v = red[0][wave][lane];
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += red[w][s][lane];
-    const int m = 16 * (s >> 1) + l16, n = n0 + 16 * (s & 1) + 4 * lq;
-    if (m < p.m && n < p.n) {
-      v += epi::bias4(p.epi, n, p.n);
-      epi::finish4(p.epi, m, n, p.n, v);
-    }
+    for (int w = 1; w < W; ++w) v += red[w][wave][lane];
+    epi::finish4(p.epi, em, en, p.n, v + bias);
   }
 }
 
-template <int MODE, int NT, int W, int D>
-hipError_t launch(const RowsParams& p, hipStream_t stream) {
-  linear_rows_kernel<MODE, NT, W, D><<<(p.n + 31) / 32, W * 64, 0, stream>>>(p);
+template <int MODE, int NT>
+hipError_t launch(const RowsParams& p, int cus, hipStream_t stream) {
+  constexpr int W = 8, D = 4;
+  // 16 columns per workgroup where 32 would occupy at most half of the CUs
+  if (p.n <= 16 * cus)
+    linear_rows_kernel<MODE, NT, true, W, D><<<(p.n + 15) / 16, W * 64, 0, stream>>>(p);
+  else
+    linear_rows_kernel<MODE, NT, false, W, D><<<(p.n + 31) / 32, W * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <int MODE>
-hipError_t launch_mode(const RowsParams& p, hipStream_t stream) {
-  if (p.m <= 16) return launch<MODE, 1, 8, 4>(p, stream);
-  if (p.m <= 32) return launch<MODE, 2, 8, 4>(p, stream);
-  return launch<MODE, 4, 8, 4>(p, stream);
+hipError_t launch_mode(const RowsParams& p, int cus, hipStream_t stream) {
+  if (p.m <= 16) return launch<MODE, 1>(p, cus, stream);
+  if (p.m <= 32) return launch<MODE, 2>(p, cus, stream);
+  return launch<MODE, 4>(p, cus, stream);
 }
 
 }  // namespace
 
-hipError_t launch_linear_rows(bool fp8, const RowsParams& p, int, hipStream_t stream) {
-  return fp8 ? launch_mode<kFp8>(p, stream) : launch_mode<kBf16>(p, stream);
+hipError_t launch_linear_rows(bool fp8, const RowsParams& p, int num_cus, hipStream_t stream) {
+  return fp8 ? launch_mode<kFp8>(p, num_cus, stream) : launch_mode<kBf16>(p, num_cus, stream);
 }
 
 }  // namespace dg

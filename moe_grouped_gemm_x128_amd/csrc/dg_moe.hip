@@ -371,7 +371,7 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(const MoeParams p) {
   c.u.srange = c.u.so[1] + 4u;
   c.seek();
   const int mine = c.nb > wave ? (c.nb - wave + W - 1) / W : 0;  // units of an item on this wave
-  Pipe<MODE, D, false, UpCursor> pipe;
+  Pipe<MODE, D, false, false, UpCursor> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
 
   for (int item = blockIdx.x; item < c.items; item += c.grid) {
@@ -412,10 +412,12 @@ __global__ __launch_bounds__(W * 64) void moe_up_kernel(const MoeParams p) {
 
 // ---- second kernel ---------------------------------------------------------
 // A workgroup owns 32 rows of every chosen expert's w2 (32 output columns; the
-// unit's groups are 16 rows each) and walks (segment, K block) units, the
-// waves round robin.  A wave's sums of a segment go to its own LDS rows
-// [token][32] when it leaves the segment, and the waves' rows meet at the end.
-template <int TMAX>
+// unit's groups are 16 rows each), or 16 where 32 each would leave half of the
+// CUs idle (the groups are two lines of K), and walks (segment, K block) units,
+// the waves round robin.  A wave's sums of a segment go to its own LDS rows
+// [token][columns] when it leaves the segment, and the waves' rows meet at the
+// end.
+template <int TMAX, bool SAME>
 struct DownCursor {
   Unit u;
   const MoeParams* p;
@@ -429,12 +431,19 @@ struct DownCursor {
     q0 = (int)uniform(tb->seg[seg]);
     q1 = (int)uniform(tb->seg[seg + 1]);
     const int e = (int)uniform(tb->sid[seg]);
-    const int wb = p->s2 ? 128 : 256;
+    const int wb = p->s2 && !SAME ? 128 : 256;      // bytes of K per unit
+    const int xb = p->s2 && SAME ? 512 : 256;       // of the activations
     u.tiles = (q1 - q0 + 15) >> 4;
     u.wa = p->w2 + ((int64_t)e * p->hid + h0) * u.wrow + kb * wb;
     u.wb = u.wa + 16 * (int64_t)u.wrow;
-    if (p->s2) u.s = p->s2 + ((int64_t)e * (p->hid >> 7) + (h0 >> 7)) * nb + kb;
-    u.x = reinterpret_cast<const uint8_t*>(p->h + kb * 128);
+    u.kbytes = (int)u.wrow - kb * wb;
+    u.xbytes = 2 * p->inter - kb * xb;
+    u.xrange = (uint32_t)(p->t * p->top_k - 1) * (uint32_t)p->inter * 2u + min(u.xbytes, xb);
+    if (p->s2) {
+      u.s = p->s2 + ((int64_t)e * (p->hid >> 7) + (h0 >> 7)) * (p->inter >> 7) + kb * (SAME ? 2 : 1);
+      u.srange = SAME && u.kbytes > 128 ? 8 : 4;
+    }
+    u.x = reinterpret_cast<const uint8_t*>(p->h) + kb * xb;
   }
   __device__ __forceinline__ void next() {
     kb += waves;
@@ -451,13 +460,12 @@ struct DownCursor {
   __device__ __forceinline__ uint32_t scale(int) const { return kOut; }
 };
 
-constexpr int kYStride = 36;  // floats per token in LDS: 32 and a pad against bank conflicts
-
 // TMAX: the most tokens of the call (LDS rows).
-template <int MODE, int TMAX, int W, int D>
+template <int MODE, int TMAX, bool SAME, int W, int D>
 __global__ __launch_bounds__(W * 64) void moe_down_kernel(const MoeParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(MODE, W, D)];
   __shared__ __attribute__((aligned(16))) Tables<TMAX> tb;
+  constexpr int R = SAME ? 16 : 32, kYStride = R + 4;  // columns; floats per token in LDS (padded against bank conflicts)
   __shared__ __attribute__((aligned(16))) float yacc[W][TMAX][kYStride];
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
@@ -465,25 +473,22 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(const MoeParams p) {
     reinterpret_cast<v4f*>(&yacc[0][0][0])[i] = v4f{0.f, 0.f, 0.f, 0.f};
   build_tables<false, TMAX>(p, tb);
 
-  using Cursor = DownCursor<TMAX>;
+  using Cursor = DownCursor<TMAX, SAME>;
   Cursor c{};
   c.p = &p;
   c.tb = &tb;
   c.nseg = (int)uniform(tb.nseg);
-  c.nb = p.inter >> 7;
+  c.nb = MODE == kW8A16 && SAME ? (p.inter + 255) >> 8 : p.inter >> 7;
   c.waves = W;
-  c.h0 = blockIdx.x * 32;
+  c.h0 = blockIdx.x * R;
   c.seg = wave / c.nb;
   c.kb = wave - c.seg * c.nb;
   c.u.ra = c.u.rb = 16;
   c.u.wrow = (uint32_t)p.inter * (MODE == kBf16 ? 2 : 1);
-  c.u.kbytes = MODE == kBf16 ? 256 : 128;
-  c.u.xbytes = 256;
-  c.u.xrange = (uint32_t)(p.t * p.top_k - 1) * (uint32_t)p.inter * 2u + 256u;
   c.u.s = p.s2;
-  c.u.srange = 4;
+  c.u.so[1] = SAME ? 4 : 0;
   c.seek();
-  Pipe<MODE, D, false, Cursor> pipe;
+  Pipe<MODE, D, false, SAME, Cursor> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
 
   v4f a[kMaxTiles], b[kMaxTiles];
@@ -500,8 +505,12 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(const MoeParams p) {
       const int pr = column_pair(tb, c.q0, c.q1, 16 * t + l16);
       if (pr >= 0) {
         v4f* y = reinterpret_cast<v4f*>(&yacc[wave][pr / p.top_k][4 * lq]);
-        y[0] += a[t];
-        y[4] += b[t];
+        if constexpr (SAME) {
+          y[0] += a[t] + b[t];
+        } else {
+          y[0] += a[t];
+          y[4] += b[t];
+        }
       }
     }
   };
@@ -516,8 +525,8 @@ __global__ __launch_bounds__(W * 64) void moe_down_kernel(const MoeParams p) {
   }
   dma::wait<0>();  // no load outlives the workgroup
   __syncthreads();
-  for (int i = tid; i < p.t * 8; i += W * 64) {
-    const int t = i >> 3, h = 4 * (i & 7);
+  for (int i = tid; i < p.t * (R / 4); i += W * 64) {
+    const int t = i / (R / 4), h = 4 * (i % (R / 4));
     v4f s = *reinterpret_cast<const v4f*>(&yacc[0][t][h]);
 #pragma unroll
     for (int w = 1; w < W; ++w) s += *reinterpret_cast<const v4f*>(&yacc[w][t][h]);
@@ -546,10 +555,18 @@ hipError_t launch_moe(const MoeParams& p, int cus, hipStream_t stream) {
     moe_up_kernel<MODE, false, W, D><<<grid, W * 64, 0, stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (p.t <= 16)
-    moe_down_kernel<MODE, 16, 8, 4><<<p.hid / 32, 8 * 64, 0, stream>>>(p);
-  else
-    moe_down_kernel<MODE, kMaxTokens, 4, 6><<<p.hid / 32, 4 * 64, 0, stream>>>(p);
+  // 16 columns per workgroup where 32 would occupy at most half of the CUs
+  const bool narrow = p.hid <= 16 * cus;
+  if (p.t <= 16) {
+    if (narrow)
+      moe_down_kernel<MODE, 16, true, 8, 4><<<p.hid / 16, 8 * 64, 0, stream>>>(p);
+    else
+      moe_down_kernel<MODE, 16, false, 8, 4><<<p.hid / 32, 8 * 64, 0, stream>>>(p);
+  } else if (narrow) {
+    moe_down_kernel<MODE, kMaxTokens, true, 4, 7><<<p.hid / 16, 4 * 64, 0, stream>>>(p);
+  } else {
+    moe_down_kernel<MODE, kMaxTokens, false, 4, 6><<<p.hid / 32, 4 * 64, 0, stream>>>(p);
+  }
   return hipGetLastError();
 }
 

@@ -2,10 +2,10 @@
 // few rows by large weights (the linear layer for few rows, the few-token MoE
 // layer), all bound by reading the weights once.
 //
-// A wave works alone on a stream of units.  A unit is 256 bytes of K (bf16
-// operands: 128 values; fp8 by fp8: 256) or, with fp8 weights and bf16
-// activations, 128 values of 32 weight rows -- two groups A and B of 16 rows --
-// and up to 4 tiles of 16 activation rows.  The wave has a private ring of D
+// A wave works alone on a stream of units: two groups A and B of 16 weight rows,
+// or the same 16 rows at consecutive lines of K (SAME), and up to 4 tiles of 16
+// activation rows.  A unit is 256 bytes of K of the weights; with fp8 weights,
+// bf16 activations and groups of different rows 128.  The wave has a private ring of D
 // entries in LDS, filled by loads straight to LDS and drained in order, so no
 // barrier separates loads from use: an entry is complete when at most the loads
 // of the D - 1 younger entries are in flight.  Every entry has the same number
@@ -100,11 +100,12 @@ struct Unit {
 
 // PARTIAL: rows and lines may be cut (the linear layer); otherwise every unit
 // has 16 rows in both groups and whole lines.
-template <int MODE, int D, bool PARTIAL, class Cursor>
+template <int MODE, int D, bool PARTIAL, bool SAME, class Cursor>
 struct Pipe {
   static constexpr int kEntry = entry_bytes(MODE);
   static constexpr int kLoads = MODE == kBf16 ? 4 : 5;
-  static constexpr int WE = MODE == kW8A16 ? 1 : 2;  // weight entries (lines of K) per unit
+  static constexpr int WE = SAME || MODE == kW8A16 ? 1 : 2;  // weight entries per unit
+  static constexpr int XE = SAME && MODE == kW8A16 ? 2 : 1;  // activation entries per tile
   static_assert((D - 1) * kLoads < 64, "vmcnt range");
 
   uint32_t ring;       // LDS address
@@ -140,34 +141,37 @@ struct Pipe {
     islot = islot + 1 == D ? 0 : islot + 1;
     const Unit& u = ic.u;
     if (phase < WE || !u.live) {
-      // one line of K of 16 rows of A and 16 of B
-      const int koff = u.live ? 128 * phase : 0;
-      const int left = u.live ? (PARTIAL ? u.kbytes - koff : 128) : 0;
+      // one line of K of 16 rows of A and 16 of B, or two lines of A's
+      const int koff = !SAME && u.live ? 128 * phase : 0;
+      const int left = u.live ? (PARTIAL || SAME ? u.kbytes - koff : 128) : 0;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int rows = PARTIAL ? (g ? u.rb : u.ra) : 16;
-        const dma::v4i r = dma::resource((g ? u.wb : u.wa) + koff,
-                                         left > 0 && rows > 0 ? (uint32_t)(rows - 1) * u.wrow + min(left, 128) : 0u);
+        const int rows = PARTIAL ? (g && !SAME ? u.rb : u.ra) : 16;
+        const int lg = SAME ? left - 128 * g : left;
+        const dma::v4i r = dma::resource(SAME ? u.wa + 128 * g : (g ? u.wb : u.wa) + koff,
+                                         lg > 0 && rows > 0 ? (uint32_t)(rows - 1) * u.wrow + min(lg, 128) : 0u);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          dma::load16_nt(lds + (2 * g + j) * 1024, r, !PARTIAL || (int)xc[j] < left ? wv[j] : kOut);
+          dma::load16_nt(lds + (2 * g + j) * 1024, r, !PARTIAL || (int)xc[j] < lg ? wv[j] : kOut);
       }
       if constexpr (MODE != kBf16) {
-        // lane 0: A's scale of this line, lane 1: B's
-        const uint32_t so = (lane ? u.so[1] : u.so[0]) + (MODE == kFp8 ? 4u * phase : 0u);
+        // lane 0: A's scale, lane 1: B's
+        const uint32_t so = (lane ? u.so[1] : u.so[0]) + (MODE == kFp8 && !SAME ? 4u * phase : 0u);
         const dma::v4i r = dma::resource(u.s, left > 0 ? u.srange : 0u);
         if (lane < 2) dma::load4(lds + 4096, r, so);
       }
     } else {
-      const int t = phase - WE;
+      const int t = (phase - WE) / XE;
+      const int kx = 256 * ((phase - WE) % XE);
       const uint32_t off[2] = {ic.row(t, lrow), ic.row(t, 8 + lrow)};
 #pragma unroll
       for (int l = 0; l < 2; ++l) {
-        const dma::v4i r = dma::resource(u.x + 128 * l, !PARTIAL || u.xrange > 128u * l ? u.xrange - 128u * l : 0u);
+        const int at = kx + 128 * l;  // byte of the unit's K
+        const bool part = PARTIAL || SAME;
+        const dma::v4i r = dma::resource(u.x + at, !part || (int)u.xrange > at ? u.xrange - at : 0u);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          dma::load16(lds + (2 * l + j) * 1024, r,
-                      !PARTIAL || 128 * l + (int)xc[j] < u.xbytes ? off[j] + xc[j] : kOut);
+          dma::load16(lds + (2 * l + j) * 1024, r, !part || at + (int)xc[j] < u.xbytes ? off[j] + xc[j] : kOut);
       }
       if constexpr (MODE != kBf16) {
         if constexpr (MODE == kFp8) {
@@ -180,7 +184,7 @@ struct Pipe {
         }
       }
     }
-    if (u.live && ++phase == WE + u.tiles) {
+    if (u.live && ++phase == WE + XE * u.tiles) {
       phase = 0;
       ic.next();
     }
@@ -207,11 +211,12 @@ struct Pipe {
   }
 
   // One unit of `tiles` tiles into the sums of A and B (tile t's lanes: column
-  // l16, rows 4 lq .. 4 lq + 3 of the group).  The last weight entry and the
-  // first tile are read together: one LDS latency for both.
+  // l16, rows 4 lq .. 4 lq + 3 of the group; SAME: two parts of one sum).  The
+  // last weight entry and the first activation entry are read together: one
+  // LDS latency for both.
   template <int NT>
   __device__ __forceinline__ void unit(int tiles, v4f* a, v4f* b) {
-    v4i w[2][WE][2];  // [group][line][chunk lq, lq + 4]
+    v4i w[2][WE][2];  // [group][entry][chunk lq, lq + 4]
     float s[2][WE];
 #pragma unroll
     for (int e = 0; e < WE; ++e) {
@@ -227,40 +232,49 @@ struct Pipe {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (t > 0 && t >= tiles) break;
-      const uint32_t lds = t == 0 ? arrive<1>() : arrive<0>();
-      v4i x[2][2];
-      float xs[2];
 #pragma unroll
-      for (int l = 0; l < 2; ++l) {
+      for (int xe = 0; xe < XE; ++xe) {
+        const bool held = t == 0 && xe == 0;  // with the weights
+        const uint32_t lds = held ? arrive<1>() : arrive<0>();
+        v4i x[2][2];
+        float xs[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) x[l][j] = *(lv)(uintptr_t)(lds + 2048 * l + o[(MODE == kW8A16 ? 2 : 0) + j]);
-        xs[l] = MODE == kFp8 ? *(lf)(uintptr_t)(lds + 4096 + 4 * (16 * l + (lane & 15))) : 1.f;
-      }
-      if (t == 0) release<2>(); else release<1>();
+        for (int l = 0; l < 2; ++l) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        v4f& acc = g ? b[t] : a[t];
-        if constexpr (MODE == kBf16) {
+          for (int j = 0; j < 2; ++j) x[l][j] = *(lv)(uintptr_t)(lds + 2048 * l + o[(MODE == kW8A16 ? 2 : 0) + j]);
+          xs[l] = MODE == kFp8 ? *(lf)(uintptr_t)(lds + 4096 + 4 * (16 * l + (lane & 15))) : 1.f;
+        }
+        if (held) release<2>(); else release<1>();
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+        for (int g = 0; g < 2; ++g) {
+          v4f& acc = g ? b[t] : a[t];
+          if constexpr (MODE == kBf16) {
+            // group g by every line of the unit, or (SAME) its own
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc = mfma_bf16(w[g][e][j], x[e][j], acc);
-        } else if constexpr (MODE == kW8A16) {
-          v4f p = v4f{0.f, 0.f, 0.f, 0.f};
+            for (int l = 0; l < 2; ++l)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            p = mfma_bf16(__builtin_bit_cast(v4i, fp8_to_bf16(w[g][0][j][0], w[g][0][j][1])), x[j][0], p);
-            p = mfma_bf16(__builtin_bit_cast(v4i, fp8_to_bf16(w[g][0][j][2], w[g][0][j][3])), x[j][1], p);
-          }
+              for (int j = 0; j < 2; ++j)
+                if (!SAME || l == g) acc = mfma_bf16(w[g][SAME ? 0 : l][j], x[l][j], acc);
+          } else if constexpr (MODE == kW8A16) {
+            if (SAME && xe != g) continue;
+            v4f p = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s[g][0], p[r], acc[r]);
-        } else {
+            for (int j = 0; j < 2; ++j) {
+              p = mfma_bf16(__builtin_bit_cast(v4i, fp8_to_bf16(w[g][0][j][0], w[g][0][j][1])), x[j][0], p);
+              p = mfma_bf16(__builtin_bit_cast(v4i, fp8_to_bf16(w[g][0][j][2], w[g][0][j][3])), x[j][1], p);
+            }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const v4f p = mfma_fp8(w[g][e][0], w[g][e][1], x[e][0], x[e][1]);
-            const float f = s[g][e] * xs[e];
+            for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(s[g][0], p[r], acc[r]);
+          } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(f, p[r], acc[r]);
+            for (int l = 0; l < 2; ++l) {
+              if (SAME && l != g) continue;
+              const int e = SAME ? 0 : l;
+              const v4f p = mfma_fp8(w[g][e][0], w[g][e][1], x[l][0], x[l][1]);
+              const float f = s[g][e] * xs[l];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(f, p[r], acc[r]);
+            }
           }
         }
       }
