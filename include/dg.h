@@ -329,8 +329,8 @@ typedef struct {
 } dg_epilogue;
 
 /* BF16: a [M,K], b [N,K]; c [M,N] of c_type.  K % 8 == 0, K <= 2^22; a, b 16-byte
- * aligned with lda, ldb multiples of 8; lda, ldb <= 2^23; c, bias, residual and
- * pre aligned to their element.  Few rows (M <= 64) run in one kernel that
+ * aligned with lda, ldb multiples of 8; lda, ldb <= 2^22; c, bias, residual and
+ * pre aligned to their element, their rows at most 2^20 elements apart.  Few rows (M <= 64) run in one kernel that
  * streams b; more run on tiles, with K split over workgroups (fp32 partials in the
  * stream's split-K workspace, see above; not while capturing) where there are few.
  * epi null: the plain product. */

@@ -135,6 +135,12 @@ __device__ __forceinline__ v4i residual8(const Epilogue& e, const Rows& r, int m
   return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r.res, off, 0, 0));
 }
 
+// The sums alone, as bf16.
+__device__ __forceinline__ void store8(const Epilogue& e, const Rows& r, int m, int n, bool in, const float* v) {
+  const uint32_t off = in ? ((uint32_t)m * (uint32_t)e.ldc + (uint32_t)n) * 2u : 0x80000000u;
+  __builtin_amdgcn_raw_buffer_store_b128(pack8(v), r.out, off, 0, 0);
+}
+
 __device__ __forceinline__ void finish8(const Epilogue& e, const Rows& r, int m, int n, bool in, float* v,
                                         const float* bias, const v4i& res) {
 #pragma unroll

@@ -49,10 +49,11 @@ constexpr int kNumGemmTiles = 5;
 constexpr int gemm_residents(int tile) { return tile >= 2 ? 2 : 1; }
 hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipStream_t stream);
 
-// An NN and a TN product in one launch: `first` workgroups (a multiple of 8) on
-// the first, the rest on the second.
+// An NN and a TN product (neither split, both with Epilogue::vec8) in one launch: `first` workgroups (a multiple of 8) on
+// the first, the rest on the second; and the bias sum of launch_bias_sum (dbias
+// null: none).
 hipError_t launch_gemm_pair(int tile, const GemmParams& nn, const GemmParams& tn, int first, int grid,
-                            hipStream_t stream);
+                            const float* partial, float* dbias, int chunks, hipStream_t stream);
 
 // dpre = dc * act'(pre) as bf16 [m, ldp] (columns n .. ldp - 1 zero), unless
 // dpre is null, and the column sums of the unrounded dpre in chunks of `rows`

@@ -14,13 +14,15 @@ int64_t round8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 constexpr int kMaxK = 1 << 22;
-constexpr int64_t kMaxLd = 1 << 23;  // a tile's 256 operand rows within 32-bit byte offsets
+constexpr int64_t kMaxLd = 1 << 22;  // a tile's 256 operand rows within 32-bit byte offsets
+constexpr int64_t kMaxOutLd = 1 << 20;  // and 256 rows of up to 4 bytes an element within 31 bits
 
 // Checks c and the epilogue's arguments and fills `e`.
 dg_status make_epilogue(void* c, int64_t ldc, int c_type, const dg_epilogue* in, int n, Epilogue* e) {
   *e = Epilogue{};
   if (c_type != DG_TYPE_BF16 && c_type != DG_TYPE_F32) return DG_ERROR_INVALID_VALUE;
   if (ldc < n) return DG_ERROR_INVALID_VALUE;
+  if (ldc > kMaxOutLd) return DG_ERROR_UNSUPPORTED;
   const int es = c_type == DG_TYPE_F32 ? 4 : 2;
   if (!aligned(c, es)) return DG_ERROR_UNSUPPORTED;
   e->out = c;
@@ -39,7 +41,7 @@ dg_status make_epilogue(void* c, int64_t ldc, int c_type, const dg_epilogue* in,
     }
     if (in->residual) {
       if (in->ld_residual < n) return DG_ERROR_INVALID_VALUE;
-      if (!aligned(in->residual, 2)) return DG_ERROR_UNSUPPORTED;
+      if (!aligned(in->residual, 2) || in->ld_residual > kMaxOutLd) return DG_ERROR_UNSUPPORTED;
       e->res = static_cast<const uint16_t*>(in->residual);
       e->ldr = in->ld_residual;
       vec = vec && aligned(e->res, 8) && e->ldr % 4 == 0;
@@ -47,7 +49,7 @@ dg_status make_epilogue(void* c, int64_t ldc, int c_type, const dg_epilogue* in,
     }
     if (in->pre) {
       if (in->ld_pre < n) return DG_ERROR_INVALID_VALUE;
-      if (!aligned(in->pre, 2)) return DG_ERROR_UNSUPPORTED;
+      if (!aligned(in->pre, 2) || in->ld_pre > kMaxOutLd) return DG_ERROR_UNSUPPORTED;
       e->pre = static_cast<uint16_t*>(in->pre);
       e->ldp = in->ld_pre;
       vec = vec && aligned(e->pre, 8) && e->ldp % 4 == 0;
@@ -55,8 +57,7 @@ dg_status make_epilogue(void* c, int64_t ldc, int c_type, const dg_epilogue* in,
     }
   }
   e->vec = vec;
-  // 32-bit byte offsets over a tile's 256 rows
-  e->vec8 = vec8 && ldc <= kMaxLd / 4 && e->ldr <= kMaxLd / 4 && e->ldp <= kMaxLd / 4;
+  e->vec8 = vec8;
   return DG_SUCCESS;
 }
 
@@ -311,9 +312,8 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
     d.act = activation;
     d.vec = aligned(dc, 16) && lddc % 8 == 0 && (!act || (aligned(pre, 16) && ld_pre % 8 == 0));
     if (launch_dact(d, stream) != hipSuccess) return DG_ERROR_LAUNCH;
-    if (dbias && launch_bias_sum(partial, dbias, ceil_div(m, d.rows), n, stream) != hipSuccess)
-      return DG_ERROR_LAUNCH;
   }
+  const int chunks = ceil_div(m, dact_rows(m, n));  // of the bias partials
   const uint8_t* g = in_place ? static_cast<const uint8_t*>(dc) : reinterpret_cast<const uint8_t*>(dpre);
   GemmParams nn{}, tn{};
   if (da) {
@@ -342,7 +342,7 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
     if (st != DG_SUCCESS) return st;
   }
   const bool may_split = !is_capturing(stream);
-  if (da && db) {
+  if (da && db && nn.epi.vec8 && tn.epi.vec8) {
     const PairPlan c = plan_pair(nn, tn, cus);
     const Plan ca = plan(nn.m, nn.n, nn.k, cus, may_split), cb = plan(tn.m, tn.n, tn.k, cus, may_split);
     // (two launches where splitting K gains more than sharing the card)
@@ -353,9 +353,10 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
       if (std::getenv("DG_LOG"))
         std::fprintf(stderr, "[dg] linear backward m=%d n=%d k=%d -> tile %dx%d first=%d grid=%d\n", m, n, k, tile.bm,
                      tile.bn, c.first, c.grid);
-      return launch_gemm_pair(c.tile, nn, tn, c.first, c.grid, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+      return launch_gemm_pair(c.tile, nn, tn, c.first, c.grid, partial, dbias, chunks, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
     }
   }
+  if (dbias && launch_bias_sum(partial, dbias, chunks, n, stream) != hipSuccess) return DG_ERROR_LAUNCH;
   if (da) {
     const dg_status r = gemm(kNN, nn, cus, may_split, stream);
     if (r != DG_SUCCESS) return r;

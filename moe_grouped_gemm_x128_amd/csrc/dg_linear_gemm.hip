@@ -137,8 +137,10 @@ template <int BM, int BN, int WM, int WN, int S>
 constexpr int kLds = S * (BM + BN) * 128 + (S == 2 ? WM * WN * 16 * (BN / WN) * 4 : 0);
 
 // The items of one product that workgroup `wg` of `nwg` computes.  `p` is the
-// kernel's argument at byte ARG.
-template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, int ARG>
+// kernel's argument at byte ARG.  LINES: K is not split and every row of the
+// output, pre and residual is whole 16-byte pieces (a form of its own: the two
+// epilogues in one kernel cost the K loop some 45 registers).
+template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, bool LINES, int ARG>
 __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, uint8_t* smem) {
   constexpr int NW = WM * WN;
   using OpA = Operand<BM, WM, NW, TA>;
@@ -309,96 +311,147 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
       const uint32_t so = kOwnRows ? lds0 + S * STAGE + wave * 16 * RS : lds0 + last * STAGE + wave * (STAGE / NW);
       const int m0w = wm * OpA::WTX, n = cur.n0 + wn * OpB::WTX + 8 * (lane % LPR);
       const int rows = min(BM, p.m - cur.m0);
-      const bool lines = p.splits == 1 && ep.vec8;  // whole lines, 16 bytes per lane
       const epi::Rows er = epi::rows_of(ep, cur.m0, rows, p.n);
-      float bias[8];
-      {
+      // residual rows are loaded kAhead rows of fragments before their use: a
+      // load waits for the stores before it
+      constexpr int kAhead = FM < 4 ? FM : 4;
+      // fragment row j = STEP x + FIRST of the sums, into LDS (the loops over x
+      // below are not unrolled: one copy of the epilogue's code per STEP rows; the
+      // row is picked by an opaque bit, since the compiler makes "jc == j" an
+      // access by index, which would put the sums in scratch memory)
+      auto put = [&](int j, int first, int step) {
+        uint32_t bit = 1u << j;
+        asm("" : "+s"(bit));
+#pragma unroll
+        for (int jc = first; jc < FM; jc += step)
+          if (bit >> jc & 1) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+              *(lp)(uintptr_t)(so + l16 * RS + (((4 * i + lq) ^ (l16 & (RC - 1))) << 4)) = acc[i][jc];
+          }
+        dma::lds_done();
+      };
+      if constexpr (LINES) {
+        float bias[8];
         const v4f b0 = epi::bias4(ep, n, p.n), b1 = epi::bias4(ep, n + 4, p.n);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           bias[e] = b0[e];
           bias[4 + e] = b1[e];
         }
-      }
-      // residual rows are loaded kAhead rows of fragments before their use: a
-      // load waits for the stores before it
-      constexpr int kAhead = FM < 4 ? FM : 4;
-      epi::v4i res[kAhead][ROUNDS];
-      auto load_res = [&](int j, epi::v4i* to) {
-#pragma unroll
-        for (int h = 0; h < ROUNDS; ++h) {
-          const int m = m0w + 16 * j + RPR * h + lane / LPR;
-          to[h] = epi::residual8(ep, er, m, n, j < FM && m < rows && n < p.n);
-        }
-      };
-      const bool ahead = lines && ep.res;
-      if (ahead) {
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) load_res(j, res[j]);
-      }
-      // partial sums, and rows that do not start on 16-byte boundaries
-      auto finish_some = [&](int m, int n, const float* v, const float* bias) {
-#pragma unroll 1
-        for (int c = 0; c < 2 && n + 4 * c < p.n; ++c) {
-          v4f x, b;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = c ? v[4 + e] : v[e];
-            b[e] = c ? bias[4 + e] : bias[e];
-          }
-          if (p.splits == 1) {
-            epi::finish4(ep, cur.m0 + m, n + 4 * c, p.n, x + b);
-          } else {
-            float* w = p.ws + cur.split * p.ws_stride + (int64_t)(cur.m0 + m) * p.n + n + 4 * c;
-            if (p.n % 4 == 0) {
-              *reinterpret_cast<v4f*>(w) = x;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (n + 4 * c + e < p.n) w[e] = x[e];
-            }
-          }
-        }
-      };
-      // (the outer loop is not unrolled: one copy of the epilogue's code per kAhead rows)
-#pragma unroll 1
-      for (int jo = 0; jo < FM; jo += kAhead) {
-#pragma unroll
-        for (int ji = 0; ji < kAhead; ++ji) {
-          const int j = jo + ji;
-#pragma unroll
-          for (int jc = ji; jc < FM; jc += kAhead)
-            if (jc == j) {
-#pragma unroll
-              for (int i = 0; i < FN; ++i)
-                *(lp)(uintptr_t)(so + l16 * RS + (((4 * i + lq) ^ (l16 & (RC - 1))) << 4)) = acc[i][jc];
-            }
-          dma::lds_done();
-          float v[ROUNDS][8];
-#pragma unroll
-          for (int h = 0; h < ROUNDS; ++h) {
-            const int r = RPR * h + lane / LPR;
-            const uint32_t a = so + r * RS, c = 2 * (lane % LPR), x = r & (RC - 1);
-            const v4f lo = *(lp)(uintptr_t)(a + ((c ^ x) << 4)), hi = *(lp)(uintptr_t)(a + (((c + 1) ^ x) << 4));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[h][e] = lo[e];
-              v[h][4 + e] = hi[e];
-            }
-          }
-          dma::lds_done();  // before the next rows take their place
-          epi::v4i rs[ROUNDS];
-#pragma unroll
-          for (int h = 0; h < ROUNDS; ++h) rs[h] = res[ji][h];
-          if (ahead) load_res(j + kAhead, res[ji]);
+        epi::v4i res[kAhead][ROUNDS];
+        auto load_res = [&](int j, epi::v4i* to) {
 #pragma unroll
           for (int h = 0; h < ROUNDS; ++h) {
             const int m = m0w + 16 * j + RPR * h + lane / LPR;
-            if (lines) {
-              epi::finish8(ep, er, m, n, m < rows && n < p.n, v[h], bias, rs[h]);
-            } else if (m < rows) {
-              finish_some(m, n, v[h], bias);
+            to[h] = epi::residual8(ep, er, m, n, j < FM && m < rows && n < p.n);
+          }
+        };
+        constexpr bool kPlain = TB;  // the backward pass's products: nothing but the sums, in bf16
+        if (!kPlain && ep.res) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) load_res(j, res[j]);
+        }
+#pragma unroll 1
+        for (int jo = 0; jo < FM; jo += kAhead) {
+#pragma unroll
+          for (int ji = 0; ji < kAhead; ++ji) {
+            const int j = jo + ji;
+            put(j, ji, kAhead);
+            float v[ROUNDS][8];
+#pragma unroll
+            for (int h = 0; h < ROUNDS; ++h) {
+              const int r = RPR * h + lane / LPR;
+              const uint32_t a = so + r * RS, c = 2 * (lane % LPR), x = r & (RC - 1);
+              const v4f lo = *(lp)(uintptr_t)(a + ((c ^ x) << 4)), hi = *(lp)(uintptr_t)(a + (((c + 1) ^ x) << 4));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                v[h][e] = lo[e];
+                v[h][4 + e] = hi[e];
+              }
             }
+            dma::lds_done();  // before the next rows take their place
+            epi::v4i rs[ROUNDS];
+#pragma unroll
+            for (int h = 0; h < ROUNDS; ++h) rs[h] = res[ji][h];
+            if (!kPlain && ep.res) load_res(j + kAhead, res[ji]);
+#pragma unroll
+            for (int h = 0; h < ROUNDS; ++h) {
+              const int m = m0w + 16 * j + RPR * h + lane / LPR;
+              if constexpr (kPlain)
+                epi::store8(ep, er, m, n, m < rows && n < p.n, v[h]);
+              else
+                epi::finish8(ep, er, m, n, m < rows && n < p.n, v[h], bias, rs[h]);
+            }
+          }
+        }
+      } else {
+        // Rows that do not start on 16-byte boundaries, and partial sums: one
+        // column per lane, so that an instruction still covers whole rows' runs
+        // (8 columns per lane in 2-byte pieces would touch every line 8 times)
+        constexpr int NV = 16 * OpB::WTX / 64, RPV = 64 / OpB::WTX;  // values per lane and 16 rows; rows per value
+        const int col = lane % OpB::WTX, nc = cur.n0 + wn * OpB::WTX + col;
+        const bool whole = p.splits == 1, with_res = whole && ep.res;
+        const float bias = whole && ep.bias && nc < p.n
+                               ? (ep.bias_f32 ? static_cast<const float*>(ep.bias)[nc]
+                                              : epi::from_bf16(static_cast<const uint16_t*>(ep.bias)[nc]))
+                               : 0.f;
+        const __amdgpu_buffer_rsrc_t part = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(p.ws + cur.split * p.ws_stride + (int64_t)cur.m0 * p.n), (short)0, whole ? 0 : rows * p.n * 4,
+            0x00020000);
+        // byte offset of value e of fragment row j in rows of ld elements of es
+        // bytes (from an opaque copy of the lane's place: the compiler would
+        // otherwise keep every value's offset in every tensor across the rows)
+        auto at = [&](int j, int e, int64_t ld, int es) -> uint32_t {
+          uint32_t place = (uint32_t)lane;
+          asm("" : "+v"(place));
+          const int m = m0w + 16 * j + RPV * e + (int)(place / OpB::WTX);
+          const int c = cur.n0 + wn * OpB::WTX + (int)(place % OpB::WTX);
+          return m < rows && c < p.n ? ((uint32_t)m * (uint32_t)ld + (uint32_t)c) * es : kOut;
+        };
+        uint16_t res[NV];
+        auto load_col = [&](int j) {
+#pragma unroll
+          for (int e = 0; e < NV; ++e)
+            res[e] = __builtin_amdgcn_raw_buffer_load_b16(er.res, j < FM ? at(j, e, ep.ldr, 2) : kOut, 0, 0);
+        };
+        if (with_res) load_col(0);
+#pragma unroll 1
+        for (int j = 0; j < FM; ++j) {
+          put(j, 0, 1);
+          float v[NV];
+#pragma unroll
+          for (int e = 0; e < NV; ++e) {
+            typedef __attribute__((address_space(3))) const float* lf;
+            const int row = e * RPV + lane / OpB::WTX;
+            v[e] = *(lf)(uintptr_t)(so + row * RS + (((col >> 2) ^ (row & (RC - 1))) << 4) + ((col & 3) << 2)) + bias;
+          }
+          dma::lds_done();
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), part, at(j, e, p.n, 4), 0, 0);
+            continue;
+          }
+          if (ep.pre) {
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+              __builtin_amdgcn_raw_buffer_store_b16(epi::to_bf16(v[e]), er.pre, at(j, e, ep.ldp, 2), 0, 0);
+          }
+          act::apply<NV>(v, ep.act);
+          if (with_res) {
+#pragma unroll
+            for (int e = 0; e < NV; ++e) v[e] += epi::from_bf16(res[e]);
+            load_col(j + 1);
+          }
+          if (ep.out_f32) {
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), er.out, at(j, e, ep.ldc, 4), 0, 0);
+          } else {
+#pragma unroll
+            for (int e = 0; e < NV; ++e)
+              __builtin_amdgcn_raw_buffer_store_b16(epi::to_bf16(v[e]), er.out, at(j, e, ep.ldc, 2), 0, 0);
           }
         }
       }
@@ -406,7 +459,7 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
         dma::barrier();  // every wave is done with the slot
         issue(last);
       }
-      const int per = !lines ? 0 : (ep.out_f32 ? 2 : 1) + (ep.pre ? 1 : 0);
+      const int per = !LINES ? 0 : (ep.out_f32 ? 2 : 1) + (ep.pre ? 1 : 0);
       stores = per <= 2 ? per : 0;
     }
     cur = next(ct);
@@ -414,34 +467,59 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
   dma::wait<0>();  // no load outlives the workgroup
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB>
+// dbias of columns 64 b .. 64 b + 63: a workgroup's first four waves sum a
+// quarter of the chunks each.
+__device__ __forceinline__ void bias_sum(const float* partial, float* dbias, int chunks, int n, int b,
+                                         float (*sum)[64]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = b * 64 + lane, per = (chunks + 3) / 4;
+  float v = 0.f;
+  if (wave < 4 && c < n) {
+#pragma unroll 8
+    for (int k = wave * per; k < min(chunks, (wave + 1) * per); ++k) v += partial[(int64_t)k * n + c];
+  }
+  if (wave < 4) sum[wave][lane] = v;
+  __syncthreads();
+  if (wave == 0 && c < n) dbias[c] = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
+}
+
+template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, bool LINES>
 __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds<BM, BN, WM, WN, S>];
-  run_items<BM, BN, WM, WN, S, TA, TB, 0>(p, blockIdx.x, gridDim.x, smem);
+  run_items<BM, BN, WM, WN, S, TA, TB, LINES, 0>(p, blockIdx.x, gridDim.x, smem);
 }
 
 // The two products of the backward pass in one launch: workgroups below
-// `first` compute da (NN), the others db (TN).  Neither fills the card by
-// itself as well as both do together (4096 x 7168 x 2048 on 256x256 tiles: 128
-// tiles of 112 blocks beside 224 of 64), and small ones overlap whole.
+// `first` compute da (NN), the others db (TN).  Small ones overlap whole
+// (517 x 1161 x 1096: 27 us against 33 in two launches), large ones fill the
+// card's last pass together.
+// The workgroups past the products' sum the bias partials (bias_sum).
 struct PairParams {
   GemmParams nn, tn;
-  int first;
+  int first, grid;
+  const float* partial;
+  float* dbias;
+  int chunks;
 };
 template <int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(WM * WN * 64) void linear_gemm_pair_kernel(const PairParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds<BM, BN, WM, WN, S>];
   if ((int)blockIdx.x < p.first)
-    run_items<BM, BN, WM, WN, S, false, true, offsetof(PairParams, nn)>(p.nn, blockIdx.x, p.first, smem);
+    run_items<BM, BN, WM, WN, S, false, true, true, offsetof(PairParams, nn)>(p.nn, blockIdx.x, p.first, smem);
+  else if ((int)blockIdx.x < p.grid)
+    run_items<BM, BN, WM, WN, S, true, true, true, offsetof(PairParams, tn)>(p.tn, blockIdx.x - p.first,
+                                                                             p.grid - p.first, smem);
   else
-    run_items<BM, BN, WM, WN, S, true, true, offsetof(PairParams, tn)>(p.tn, blockIdx.x - p.first,
-                                                                       gridDim.x - p.first, smem);
+    bias_sum(p.partial, p.dbias, p.chunks, p.tn.m, blockIdx.x - p.grid, reinterpret_cast<float(*)[64]>(smem));
 }
 
 template <int TILE, bool TA, bool TB>
 hipError_t launch_tile(const GemmParams& p, int grid, hipStream_t stream) {
   constexpr GemmTile t = kGemmTiles[TILE];
-  linear_gemm_kernel<t.bm, t.bn, t.wm, t.wn, t.stages, TA, TB><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
+  if (p.splits == 1 && p.epi.vec8)
+    linear_gemm_kernel<t.bm, t.bn, t.wm, t.wn, t.stages, TA, TB, true><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
+  else
+    linear_gemm_kernel<t.bm, t.bn, t.wm, t.wn, t.stages, TA, TB, false><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -453,8 +531,9 @@ hipError_t launch_layout(int layout, const GemmParams& p, int grid, hipStream_t 
 }
 
 template <int TILE>
-hipError_t launch_both(const PairParams& p, int grid, hipStream_t stream) {
+hipError_t launch_both(const PairParams& p, hipStream_t stream) {
   constexpr GemmTile t = kGemmTiles[TILE];
+  const int grid = p.grid + (p.dbias ? (p.tn.m + 63) / 64 : 0);
   linear_gemm_pair_kernel<t.bm, t.bn, t.wm, t.wn, t.stages><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
@@ -466,7 +545,9 @@ hipError_t launch_both(const PairParams& p, int grid, hipStream_t stream) {
 __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
   __shared__ float sum[8][256];
   const int lx = threadIdx.x & 31, ly = threadIdx.x >> 5;
-  const int c = blockIdx.x * 256 + lx * 8;
+  // 8 consecutive columns per lane where rows start on 16-byte boundaries, else
+  // every 32nd (2-byte accesses that cover whole runs)
+  const int c = blockIdx.x * 256 + (p.vec ? lx * 8 : lx), step = p.vec ? 1 : 32;
   const int r0 = blockIdx.y * p.rows;
   float s[8];
 #pragma unroll
@@ -497,26 +578,35 @@ __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          d[e] = c + e < p.n ? epi::from_bf16(dc[e]) : 0.f;
-          x[e] = pr && c + e < p.n ? epi::from_bf16(pr[e]) : 0.f;
+          d[e] = c + e * step < p.n ? epi::from_bf16(dc[e * step]) : 0.f;
+          x[e] = pr && c + e * step < p.n ? epi::from_bf16(pr[e * step]) : 0.f;
         }
       }
       uint32_t o[4];
       if (pr) act::times_grad<8>(d, x, p.act);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (c + e >= p.n) d[e] = 0.f;  // the padding columns
+        if (c + e * step >= p.n) d[e] = 0.f;  // the padding columns
         s[e] += d[e];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         o[e] = (uint32_t)epi::to_bf16(d[2 * e]) | ((uint32_t)epi::to_bf16(d[2 * e + 1]) << 16);
-      if (p.dpre) *reinterpret_cast<uint4*>(p.dpre + (int64_t)r * p.ldp + c) = uint4{o[0], o[1], o[2], o[3]};
+      if (p.dpre) {
+        uint16_t* to = p.dpre + (int64_t)r * p.ldp + c;
+        if (p.vec) {
+          *reinterpret_cast<uint4*>(to) = uint4{o[0], o[1], o[2], o[3]};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e * 32 < p.ldp) to[e * 32] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+        }
+      }
     }
   }
   if (p.partial) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[ly][lx * 8 + e] = s[e];
+    for (int e = 0; e < 8; ++e) sum[ly][p.vec ? lx * 8 + e : lx + e * 32] = s[e];
     __syncthreads();
     const int col = blockIdx.x * 256 + threadIdx.x;
     if (col < p.n) {
@@ -528,19 +618,9 @@ __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
   }
 }
 
-// 64 columns per workgroup; its four waves sum a quarter of the chunks each.
 __global__ __launch_bounds__(256) void bias_sum_kernel(const float* partial, float* dbias, int chunks, int n) {
   __shared__ float sum[4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane, per = (chunks + 3) / 4;
-  float v = 0.f;
-  if (c < n) {
-#pragma unroll 8
-    for (int k = wave * per; k < min(chunks, (wave + 1) * per); ++k) v += partial[(int64_t)k * n + c];
-  }
-  sum[wave][lane] = v;
-  __syncthreads();
-  if (wave == 0 && c < n) dbias[c] = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
+  bias_sum(partial, dbias, chunks, n, blockIdx.x, sum);
 }
 
 }  // namespace
@@ -557,14 +637,14 @@ hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipS
 }
 
 hipError_t launch_gemm_pair(int tile, const GemmParams& nn, const GemmParams& tn, int first, int grid,
-                            hipStream_t stream) {
-  const PairParams p{nn, tn, first};
+                            const float* partial, float* dbias, int chunks, hipStream_t stream) {
+  const PairParams p{nn, tn, first, grid, partial, dbias, chunks};
   switch (tile) {
-    case 0: return launch_both<0>(p, grid, stream);
-    case 1: return launch_both<1>(p, grid, stream);
-    case 2: return launch_both<2>(p, grid, stream);
-    case 3: return launch_both<3>(p, grid, stream);
-    case 4: return launch_both<4>(p, grid, stream);
+    case 0: return launch_both<0>(p, stream);
+    case 1: return launch_both<1>(p, stream);
+    case 2: return launch_both<2>(p, stream);
+    case 3: return launch_both<3>(p, stream);
+    case 4: return launch_both<4>(p, stream);
     default: return hipErrorInvalidValue;
   }
 }
