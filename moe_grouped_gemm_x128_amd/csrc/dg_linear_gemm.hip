@@ -539,16 +539,15 @@ hipError_t launch_both(const PairParams& p, hipStream_t stream) {
 }
 
 // ---- the activation's backward pass and the bias gradient ----
-// A workgroup takes 256 columns x p.rows rows: 32 lanes of 8 columns by 8 rows in
-// flight; the column sums of its 8 row lanes meet in LDS.  Bound by
-// HBM: dc and pre read, dpre written, once.
+// A workgroup takes 256 columns x p.rows rows.  Bound by HBM: dc and pre read,
+// dpre written, once (4096 x 7168: 36 us, 4.9 TB/s).
+//
+// Rows on 16-byte boundaries: 32 lanes of 8 columns by 8 rows in flight; the
+// column sums of the 8 row lanes meet in LDS.
 __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
   __shared__ float sum[8][256];
   const int lx = threadIdx.x & 31, ly = threadIdx.x >> 5;
-  // 8 consecutive columns per lane where rows start on 16-byte boundaries, else
-  // every 32nd (2-byte accesses that cover whole runs)
-  const int c = blockIdx.x * 256 + (p.vec ? lx * 8 : lx), step = p.vec ? 1 : 32;
-  const int r0 = blockIdx.y * p.rows;
+  const int c = blockIdx.x * 256 + lx * 8, r0 = blockIdx.y * p.rows;
   float s[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) s[e] = 0.f;
@@ -558,7 +557,7 @@ __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
       float d[8], x[8];
       const uint16_t* dc = p.dc + (int64_t)r * p.lddc + c;
       const uint16_t* pr = p.pre ? p.pre + (int64_t)r * p.ldpre + c : nullptr;
-      if (p.vec && c + 7 < p.n) {
+      if (c + 7 < p.n) {
         const uint4 v = *reinterpret_cast<const uint4*>(dc);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -578,35 +577,24 @@ __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          d[e] = c + e * step < p.n ? epi::from_bf16(dc[e * step]) : 0.f;
-          x[e] = pr && c + e * step < p.n ? epi::from_bf16(pr[e * step]) : 0.f;
+          d[e] = c + e < p.n ? epi::from_bf16(dc[e]) : 0.f;
+          x[e] = pr && c + e < p.n ? epi::from_bf16(pr[e]) : 0.f;
         }
       }
-      uint32_t o[4];
       if (pr) act::times_grad<8>(d, x, p.act);
+      uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (c + e * step >= p.n) d[e] = 0.f;  // the padding columns
-        s[e] += d[e];
-      }
+      for (int e = 0; e < 8; ++e) s[e] += d[e];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         o[e] = (uint32_t)epi::to_bf16(d[2 * e]) | ((uint32_t)epi::to_bf16(d[2 * e + 1]) << 16);
-      if (p.dpre) {
-        uint16_t* to = p.dpre + (int64_t)r * p.ldp + c;
-        if (p.vec) {
-          *reinterpret_cast<uint4*>(to) = uint4{o[0], o[1], o[2], o[3]};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e * 32 < p.ldp) to[e * 32] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
-        }
-      }
+      if (p.dpre)  // (the padding columns are zeros: 0 times a finite derivative)
+        *reinterpret_cast<uint4*>(p.dpre + (int64_t)r * p.ldp + c) = uint4{o[0], o[1], o[2], o[3]};
     }
   }
   if (p.partial) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[ly][p.vec ? lx * 8 + e : lx + e * 32] = s[e];
+    for (int e = 0; e < 8; ++e) sum[ly][lx * 8 + e] = s[e];
     __syncthreads();
     const int col = blockIdx.x * 256 + threadIdx.x;
     if (col < p.n) {
@@ -616,6 +604,39 @@ __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
       p.partial[(int64_t)blockIdx.y * p.n + col] = v;
     }
   }
+}
+
+// Other rows: one column per lane (2-byte accesses that cover whole runs), 16
+// rows in flight (517 x 1161: 5 us; columns 32 apart by one lane, each behind its
+// own branch, 13).
+__global__ __launch_bounds__(256) void dact_columns_kernel(const DactParams p) {
+  const int c = blockIdx.x * 256 + threadIdx.x, r0 = blockIdx.y * p.rows;
+  const int rows = min(p.rows, p.m - r0);
+  const bool in = c < p.n;
+  auto rows_from = [&](const uint16_t* at, int64_t ld) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(at + (int64_t)r0 * ld), (short)0,
+                                             at ? (int)(2 * ((rows - 1) * ld + p.n)) : 0, 0x00020000);
+  };
+  const __amdgpu_buffer_rsrc_t dc = rows_from(p.dc, p.lddc), pre = rows_from(p.pre, p.ldpre);
+  float s = 0.f;
+  for (int r = 0; r < rows; r += 16) {
+    float d[16], x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const bool live = in && r + e < rows;
+      const uint32_t at_dc = 2 * ((uint32_t)(r + e) * (uint32_t)p.lddc + c);
+      const uint32_t at_pre = 2 * ((uint32_t)(r + e) * (uint32_t)p.ldpre + c);
+      d[e] = epi::from_bf16(__builtin_amdgcn_raw_buffer_load_b16(dc, live ? at_dc : kOut, 0, 0));
+      x[e] = epi::from_bf16(__builtin_amdgcn_raw_buffer_load_b16(pre, live ? at_pre : kOut, 0, 0));
+    }
+    if (p.pre) act::times_grad<16>(d, x, p.act);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      s += d[e];
+      if (p.dpre && c < p.ldp && r + e < rows) p.dpre[(int64_t)(r0 + r + e) * p.ldp + c] = epi::to_bf16(d[e]);
+    }
+  }
+  if (p.partial && in) p.partial[(int64_t)blockIdx.y * p.n + c] = s;
 }
 
 __global__ __launch_bounds__(256) void bias_sum_kernel(const float* partial, float* dbias, int chunks, int n) {
@@ -651,7 +672,10 @@ hipError_t launch_gemm_pair(int tile, const GemmParams& nn, const GemmParams& tn
 
 hipError_t launch_dact(const DactParams& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.ldp + 255) / 256), (unsigned)((p.m + p.rows - 1) / p.rows));
-  dact_kernel<<<grid, 256, 0, stream>>>(p);
+  if (p.vec)
+    dact_kernel<<<grid, 256, 0, stream>>>(p);
+  else
+    dact_columns_kernel<<<grid, 256, 0, stream>>>(p);
   return hipGetLastError();
 }
 
