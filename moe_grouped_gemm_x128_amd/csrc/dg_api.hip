@@ -56,7 +56,7 @@ int occupancy(int kind, const dg::TileShape& s) {
 // power-of-two scales, and BF16.
 bool dense_like(int kind) {
   return kind == DG_KIND_DENSE || kind == DG_KIND_DENSE_POW2 || kind == DG_KIND_BF16 ||
-         kind == dg::KIND_DENSE_LINEAR;
+         dg::linear_kind(kind);
 }
 
 bool parse_forced(dg::TileShape* s) {
@@ -450,7 +450,7 @@ dg_status linear_fp8(const void* a, const float* sa, const void* b, const float*
   p.kbs = k / 128;
   p.groups = 1;
   p.vec_out = n % 4 == 0;  // the split-K partials' rows; out goes by p.epi
-  return run(KIND_DENSE_LINEAR, p, m, n, k, 1, stream);
+  return run(e.out_f32 ? KIND_DENSE_LINEAR_F32 : KIND_DENSE_LINEAR, p, m, n, k, 1, stream);
 }
 
 int compute_units() {

@@ -28,13 +28,15 @@ enum Kind : int {
   KIND_CONTIG_BF16 = 10,   // KIND_CONTIGUOUS with bf16 operands and no scales (as KIND_BF16)
   KIND_MASKED_BF16 = 11,   // KIND_MASKED with bf16 operands and no scales (as KIND_BF16)
   KIND_DENSE_LINEAR = 12,  // KIND_DENSE with the linear layer's epilogue (Params::epi) on its outputs
+  KIND_DENSE_LINEAR_F32 = 13,  // the same with fp32 outputs: codes multiplied as bf16 (exact products and sums)
 };
 
 // The operand layout and scheduling of a kind (the power-of-two and the
 // grouped bf16 kinds share their fp32-scale kind's; the dense bf16 kind
 // keeps its own).
+constexpr bool linear_kind(int kind) { return kind == KIND_DENSE_LINEAR || kind == KIND_DENSE_LINEAR_F32; }
 constexpr int layout_of(int kind) {
-  return kind == KIND_DENSE_POW2 || kind == KIND_DENSE_LINEAR   ? KIND_DENSE
+  return kind == KIND_DENSE_POW2 || linear_kind(kind)           ? KIND_DENSE
          : kind == KIND_CONTIG_POW2 || kind == KIND_CONTIG_BF16 ? KIND_CONTIGUOUS
          : kind == KIND_MASKED_POW2 || kind == KIND_MASKED_BF16 ? KIND_MASKED
                                                                  : kind;
@@ -76,7 +78,7 @@ struct Params {
   int kchunk;            // K blocks per split
   float* ws;             // fp32 partials [splits][rows of all groups][n]
   int64_t ws_stride;     // floats per split
-  Epilogue epi;          // KIND_DENSE_LINEAR (its `out` is p.out)
+  Epilogue epi;          // the linear kinds (its `out` is p.out)
   int kg_min_blocks;     // K-grouped: fewest K blocks of any non-empty group
   int kb_begin[kMaxKGroups + 1];  // K-grouped: first 128-block of each group
 };

@@ -196,7 +196,29 @@ __device__ __forceinline__ v4f mfma_block_bf16(const v8i& b_rows, const v8i& a_r
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1, a1, d, 0, 0, 0);
 }
 
+// 8 FP8 codes as bf16 (exact).
+__device__ __forceinline__ v8bf bf16_of_codes(int lo, int hi) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.f, false);
+  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.f, true);
+  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, false);
+  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, true);
+  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// EXACT (the linear layer's fp32 outputs): the FP8 matrix instructions keep 16
+// bits or so of a block's sum (1.5e-5 of its size off, measured: far below a
+// bf16 output's rounding, not below an fp32 one's); bf16's are 1e-8 off.
+template <bool EXACT>
 __device__ __forceinline__ v4f mfma_block(const v8i& b_rows, const v8i& a_rows) {
+  if constexpr (EXACT) {
+    v4f d = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < 8; h += 2)
+      d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of_codes(b_rows[h], b_rows[h + 1]),
+                                                  bf16_of_codes(a_rows[h], a_rows[h + 1]), d, 0, 0, 0);
+    return d;
+  }
   // D[n][m] = sum over the 128 k of the block; both operands use the same
   // (lane, byte) -> k assignment, so the sum covers exactly the block.
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b_rows, a_rows, v4f{0.f, 0.f, 0.f, 0.f},
@@ -232,7 +254,8 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
   // in the DMA loop cost the 256x256 instances registers (spills in the loop).
   constexpr bool kStreamB =
       ((LAYOUT == KIND_DENSE || KIND == KIND_BF16) && BM <= 128) || LAYOUT == KIND_MASKED;
-  constexpr bool kLinear = (KIND == KIND_DENSE_LINEAR);  // bias, activation, residual in the epilogue
+  constexpr bool kLinear = linear_kind(KIND);  // bias, activation, residual in the epilogue
+  constexpr bool kExact = KIND == KIND_DENSE_LINEAR_F32;
   constexpr bool kDirectAcc = kPow2 || kBf16;         // MFMAs accumulate into acc: no promotion
   constexpr bool kFp32Out = kRowScaleB;
   // the columns of one wave tile sit inside one 128-block: one sb per wave
@@ -294,7 +317,7 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
   // bf16 epilogue staging: a wave's 16-row fragment row goes through LDS so
   // that each store covers whole (64 columns) or half (32 columns) 128-byte
   // lines; rows padded by 16 bytes against bank conflicts
-  constexpr bool kStage = !kFp32Out && !kSwiGLU && (WTN == 64 || WTN == 32);
+  constexpr bool kStage = !kFp32Out && !kSwiGLU && KIND != KIND_DENSE_LINEAR_F32 && (WTN == 64 || WTN == 32);
   constexpr int kStageRow = WTN * 2 + 16;
   __shared__ __attribute__((aligned(16))) uint8_t sOut[kStage ? NW : 1][kStage ? 16 * kStageRow : 16];
   // fused SwiGLU: each wave's |h| maximum over its columns, per tile row
@@ -541,7 +564,7 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
   // per-fragment path with the conservative wait)
   // (the linear layer's epilogue: whole lines of a bf16 C, no stored pre)
   const bool staged = kStage && !(kCanSplit && splits > 1) && p.vec_out && (p.n % 8 == 0) &&
-                      (!kLinear || (p.epi.vec8 && !p.epi.out_f32 && !p.epi.pre));
+                      (!kLinear || (p.epi.vec8 && !p.epi.pre));
   // (nor for the linear layer, whose epilogue loads and stores what it is asked to)
   const bool exact_stores = kExactFits && (!kLinear || splits > 1 || staged) && (kStage ? staged : (!kFp32Out || (kCanSplit && splits > 1))) &&
                             p.vec_out && (int64_t)BM * p.n * 4 < 0x7fffffffLL;
@@ -902,7 +925,7 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
                                       : mfma_block_scaled(cur, res[r], acc_at(o, r), ue8m0_of(sbv[i], esh),
                                                           ue8m0_of(sa, esh));
             } else {
-              part[r] = kStreamM ? mfma_block(res[r], cur) : mfma_block(cur, res[r]);
+              part[r] = kStreamM ? mfma_block<kExact>(res[r], cur) : mfma_block<kExact>(cur, res[r]);
               if (r + 1 < NR) {
                 if (o > 0)
                   promote(o - 1, r + 1, true);
@@ -1270,6 +1293,9 @@ hipError_t launch_shape(int kind, const Params& p, int grid, hipStream_t stream)
     case KIND_DENSE_LINEAR:
       launch_kind<BM, BN, WM, WN, S, KIND_DENSE_LINEAR>(g, b, stream, p);
       break;
+    case KIND_DENSE_LINEAR_F32:
+      launch_kind<BM, BN, WM, WN, S, KIND_DENSE_LINEAR_F32>(g, b, stream, p);
+      break;
     default:
       return hipErrorInvalidValue;
   }
@@ -1348,7 +1374,7 @@ hipError_t launch_splitk_linear(const Epilogue& e, const float* ws, int64_t ws_s
 }
 
 hipError_t launch_splitk_reduce(int kind, const Params& p, hipStream_t stream) {
-  if (kind == KIND_DENSE_LINEAR) return launch_splitk_linear(p.epi, p.ws, p.ws_stride, p.splits, p.m, p.n, stream);
+  if (linear_kind(kind)) return launch_splitk_linear(p.epi, p.ws, p.ws_stride, p.splits, p.m, p.n, stream);
   const int layout = layout_of(kind);
   if (layout != KIND_DENSE && layout != KIND_MASKED && kind != KIND_BF16) return hipErrorInvalidValue;
   const int64_t items = (int64_t)p.groups * p.m * ((p.n + 3) / 4);

@@ -53,7 +53,7 @@ struct RowsCursor {
   }
 };
 
-template <int MODE, int NT, bool SAME, int W, int D>
+template <int MODE, int NT, bool SAME, bool EXACT, int W, int D>
 __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(MODE, W, D)];
   // the waves' sums meet where the ring was
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p)
   const bool mine_out = wave < G * NT && em < p.m && en < p.n;
   v4f bias = v4f{0.f, 0.f, 0.f, 0.f};
   if (mine_out) bias = epi::bias4(p.epi, en, p.n);
-  Pipe<MODE, D, true, SAME, RowsCursor> pipe;
+  Pipe<MODE, D, true, SAME, RowsCursor, EXACT> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
   v4f a[NT], b[NT];
 #pragma unroll
@@ -115,28 +115,29 @@ __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p)
   }
 }
 
-template <int MODE, int NT>
+template <int MODE, int NT, bool EXACT>
 hipError_t launch(const RowsParams& p, int cus, hipStream_t stream) {
   constexpr int W = 8, D = 4;
   // 16 columns per workgroup where 32 would occupy at most half of the CUs
   if (p.n <= 16 * cus)
-    linear_rows_kernel<MODE, NT, true, W, D><<<(p.n + 15) / 16, W * 64, 0, stream>>>(p);
+    linear_rows_kernel<MODE, NT, true, EXACT, W, D><<<(p.n + 15) / 16, W * 64, 0, stream>>>(p);
   else
-    linear_rows_kernel<MODE, NT, false, W, D><<<(p.n + 31) / 32, W * 64, 0, stream>>>(p);
+    linear_rows_kernel<MODE, NT, false, EXACT, W, D><<<(p.n + 31) / 32, W * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
-template <int MODE>
+template <int MODE, bool EXACT>
 hipError_t launch_mode(const RowsParams& p, int cus, hipStream_t stream) {
-  if (p.m <= 16) return launch<MODE, 1>(p, cus, stream);
-  if (p.m <= 32) return launch<MODE, 2>(p, cus, stream);
-  return launch<MODE, 4>(p, cus, stream);
+  if (p.m <= 16) return launch<MODE, 1, EXACT>(p, cus, stream);
+  if (p.m <= 32) return launch<MODE, 2, EXACT>(p, cus, stream);
+  return launch<MODE, 4, EXACT>(p, cus, stream);
 }
 
 }  // namespace
 
 hipError_t launch_linear_rows(bool fp8, const RowsParams& p, int num_cus, hipStream_t stream) {
-  return fp8 ? launch_mode<kFp8>(p, num_cus, stream) : launch_mode<kBf16>(p, num_cus, stream);
+  if (!fp8) return launch_mode<kBf16, false>(p, num_cus, stream);
+  return p.epi.out_f32 ? launch_mode<kFp8, true>(p, num_cus, stream) : launch_mode<kFp8, false>(p, num_cus, stream);
 }
 
 }  // namespace dg

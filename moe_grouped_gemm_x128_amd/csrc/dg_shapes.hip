@@ -6,7 +6,7 @@
 namespace dg {
 
 bool has_instance(int kind, const TileShape& s) {
-  if (kind < KIND_DENSE || kind > KIND_DENSE_LINEAR) return false;
+  if (kind < KIND_DENSE || kind > KIND_DENSE_LINEAR_F32) return false;
 #define X(BM, BN, WM, WN, S) \
   if (s.bm == BM && s.bn == BN && s.wm == WM && s.wn == WN) return !excluded(BM, BN, WM, kind);
   DG_SHAPES(X)
@@ -29,7 +29,7 @@ int lds_bytes_of(int kind, const TileShape& s) {
   const int sb_n = row_sb ? ((s.bn + 63) / 64) * 64 : 64;
   const int stage = (s.bm + s.bn) * kBlockK + 4 * (sa_n + sb_n);
   const int wtn = s.bn / s.wn;
-  const bool staged = !row_sb && !swiglu && (wtn == 64 || wtn == 32);
+  const bool staged = !row_sb && !swiglu && kind != KIND_DENSE_LINEAR_F32 && (wtn == 64 || wtn == 32);
   const int out = swiglu ? s.bm * s.wn * 4 : staged ? s.wm * s.wn * 16 * (wtn * 2 + 16) : 16;
   const int groups = 2 * ((s.bm + 15) / 16) * 16 * 16;
 #define X(BM, BN, WM, WN, S)                                                                    \

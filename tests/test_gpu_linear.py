@@ -156,6 +156,25 @@ def test_many_tiles_per_workgroup(dg, force):
         forward_case(dg, 2048 + 40, 8192 + 24, 72, "silu", bias=F32)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 64, 128), (19, 283, 2816), (64, 4500, 256), (65, 70, 3840), (300, 256, 1024),
+                                   (700, 1030, 512)])
+def test_fp8_with_fp32_result_is_that_exact(dg, m, n, k):
+    """An fp32 result of FP8 operands is off by fp32 rounding alone: K additions,
+    each rounding a partial sum no larger than the result by 2^-24 at most, in
+    independent directions -- sqrt(K) 2^-24 of the whole.  (The FP8 matrix
+    instructions by themselves are 1.5e-5 off.)"""
+    say(f"linear fp8 fp32 {m}x{n}x{k}")
+    g = torch.Generator(device="cuda").manual_seed(8)
+    a = (100 * torch.randn((m, k), generator=g, device="cuda")).clamp(-448, 448).to(torch.float8_e4m3fn)
+    b = (100 * torch.randn((n, k), generator=g, device="cuda")).clamp(-448, 448).to(torch.float8_e4m3fn)
+    sa, sb = torch.ones((m, k // 128), device="cuda"), torch.ones(((n + 127) // 128, k // 128), device="cuda")
+    o = torch.empty((m, n), device="cuda")
+    dg.gemm_fp8_nt_epilogue((a, sa), (b, sb), o)
+    ref = a.float().to(F64) @ b.float().to(F64).t()
+    off = ((o.to(F64) - ref).norm() / ref.norm()).item()
+    assert off <= k ** 0.5 * 2.0 ** -24, off
+
+
 @pytest.mark.parametrize("m", [4, 200])
 def test_residual_in_place_and_plain(dg, m):
     say(f"linear in place m={m}")
