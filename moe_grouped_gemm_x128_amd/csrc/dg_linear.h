@@ -40,13 +40,15 @@ struct GemmParams {
 enum GemmLayout : int { kNT = 0, kNN = 1, kTN = 2 };  // A, B stored: [m,k] [n,k]; [m,k] [k,n]; [k,m] [k,n]
 
 struct GemmTile {
-  int bm, bn, wm, wn, stages;
+  int bm, bn, wm, wn, wk, stages;  // wk groups of wm x wn waves, each every wk-th block of K
 };
+constexpr int gemm_threads(const GemmTile& t) { return t.wm * t.wn * t.wk * 64; }
 constexpr GemmTile kGemmTiles[] = {
-    {256, 256, 2, 4, 2}, {256, 128, 4, 2, 3}, {128, 128, 2, 2, 2}, {64, 128, 2, 2, 3}, {64, 64, 2, 2, 4}};
-constexpr int kNumGemmTiles = 5;
+    {256, 256, 2, 4, 1, 2}, {256, 128, 4, 2, 1, 3}, {128, 128, 2, 2, 1, 2}, {64, 128, 2, 2, 1, 3},
+    {64, 64, 2, 2, 1, 4},   {128, 128, 2, 2, 2, 2}, {64, 128, 2, 2, 2, 3},  {64, 64, 2, 2, 2, 3}};
+constexpr int kNumGemmTiles = 8, kNumPairTiles = 5;  // the first kNumPairTiles in launch_gemm_pair too
 // workgroups of a tile that share a CU (LDS)
-constexpr int gemm_residents(int tile) { return tile >= 2 ? 2 : 1; }
+constexpr int gemm_residents(int tile) { return tile >= 2 && tile <= 4 ? 2 : 1; }
 hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipStream_t stream);
 
 // An NN and a TN product (neither split, both with Epilogue::vec8) in one launch: `first` workgroups (a multiple of 8) on

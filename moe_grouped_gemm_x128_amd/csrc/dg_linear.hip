@@ -66,23 +66,33 @@ dg_status make_epilogue(void* c, int64_t ldc, int c_type, const dg_epilogue* in,
 //   item) + (split) the partials' write and read and the second launch.
 // Rates (TFLOP/s of the whole card on full CUs), the share of a block's time
 // that a workgroup alone on a CU needs where two would share it, and the other
-// constants are fitted to a sweep of every tile and split over nine shapes
-// from 100 x 2112 x 7168 to 4096 x 7168 x 16384 (chosen within 10% of the best).
-constexpr double kTileRate[kNumGemmTiles] = {1350., 1050., 1080., 900., 600.};
-constexpr double kAlone = 0.75, kItemUs = 3.0, kSplitUs = 4.0, kPartialBytesPerUs = 8e6;
+// constants are fitted to timings of every tile and split at 150 sizes drawn
+// from 65..5000 x 64..9000, K 256..8192: the choice is 1.5% behind the best in
+// the mean.  A workgroup alone on a CU is bound by the chain of a block (wait,
+// barrier, loads issued, fragments read, MFMAs), not by bandwidth: hence the
+// tiles of two groups, which halve the number of such steps (333 x 2111 x 1536:
+// 11.6 us on 64x64 with two groups, 14.6 with one; 1024 x 4096 x 4096: 54.6 us
+// on 128x128 against 66.6), while one group is better where two workgroups
+// share a CU (517 x 1161 x 1096 backward: 18.4 us against 22.4).
+constexpr double kTileRate[kNumGemmTiles] = {1370., 700., 1220., 740., 660., 880., 650., 560.};
+constexpr double kAlone = 0.82, kItemUs = 2.4, kSplitUs = 4.5, kPartialBytesPerUs = 5.7e6;
 
-double block_us(int tile, int cus, bool alone) {
+// time per K block and per item
+struct TileTime {
+  double block, item;
+};
+TileTime tile_time(int tile, int cus, bool alone) {
   const GemmTile g = kGemmTiles[tile];
   const int res = gemm_residents(tile);
   const double us = 2.0 * g.bm * g.bn * 64 * cus * res / (kTileRate[tile] * 1e6);
-  return alone && res > 1 ? us * kAlone : us;
+  return alone && res > 1 ? TileTime{us * kAlone, kItemUs} : TileTime{us, kItemUs * res};
 }
 
 bool forced_out(const GemmTile& g) {  // DG_FORCE_TILE names another tile
   const char* force = std::getenv("DG_FORCE_TILE");
-  int bm, bn, wm, wn;
-  return force && *force && std::sscanf(force, "%dx%dx%dx%d", &bm, &bn, &wm, &wn) == 4 &&
-         !(bm == g.bm && bn == g.bn && wm == g.wm && wn == g.wn);
+  int bm, bn, wm, wn, wk;
+  const int got = force && *force ? std::sscanf(force, "%dx%dx%dx%dx%d", &bm, &bn, &wm, &wn, &wk) : 0;
+  return got >= 4 && !(bm == g.bm && bn == g.bn && wm == g.wm && wn == g.wn && (got == 4 || wk == g.wk));
 }
 
 struct Plan {
@@ -108,7 +118,8 @@ Plan plan(int m, int n, int k, int cus, bool may_split) {
       const double bytes = 4.0 * s * m * n;
       if (s > 1 && (bytes > 256e6 || (chunk < 4 && !force))) break;
       const double passes = (double)((tiles * s + slots - 1) / slots);
-      double us = passes * (chunk * block_us(t, cus, tiles * s <= cus) + kItemUs * gemm_residents(t));
+      const TileTime w = tile_time(t, cus, tiles * s <= cus);
+      double us = passes * (chunk * w.block + w.item);
       if (s > 1) us += kSplitUs + 2.0 * bytes / kPartialBytesPerUs;
       if (us < best.us) best = Plan{t, s, chunk, us};
     }
@@ -124,7 +135,7 @@ struct PairPlan {
 
 PairPlan plan_pair(const GemmParams& nn, const GemmParams& tn, int cus) {
   PairPlan best{-1, 0, 0, 1e300};
-  for (int t = 0; t < kNumGemmTiles; ++t) {
+  for (int t = 0; t < kNumPairTiles; ++t) {
     const GemmTile g = kGemmTiles[t];
     if (forced_out(g)) continue;
     const int64_t ta = (int64_t)ceil_div(nn.m, g.bm) * ceil_div(nn.n, g.bn);
@@ -132,14 +143,14 @@ PairPlan plan_pair(const GemmParams& nn, const GemmParams& tn, int cus) {
     if (ta > (1 << 24) || tb > (1 << 24)) continue;
     const int64_t slots = (int64_t)(cus > 16 ? cus / 8 * 8 : 16) * gemm_residents(t);
     const int ka = ceil_div(nn.k, 64), kb = ceil_div(tn.k, 64);
-    const double blk = block_us(t, cus, ta + tb <= cus), item = kItemUs * gemm_residents(t);
+    const TileTime w = tile_time(t, cus, ta + tb <= cus);
     for (int passes = 1; passes <= 16; ++passes) {  // of da's workgroups
       const int64_t first = (ceil_div(ta, passes) + 7) / 8 * 8;
       if (first >= slots) continue;
       int64_t rest = slots - first;
       if (rest > tb) rest = (tb + 7) / 8 * 8;
-      const double a = (double)((ta + first - 1) / first) * (ka * blk + item);
-      const double b = (double)((tb + rest - 1) / rest) * (kb * blk + item);
+      const double a = (double)((ta + first - 1) / first) * (ka * w.block + w.item);
+      const double b = (double)((tb + rest - 1) / rest) * (kb * w.block + w.item);
       const double us = a > b ? a : b;
       if (us < best.us) best = PairPlan{t, (int)first, (int)(first + rest), us};
     }
@@ -167,8 +178,8 @@ dg_status gemm(int layout, GemmParams& p, int cus, bool may_split, hipStream_t s
     const int64_t slots = (int64_t)(cus > 8 ? cus / 8 * 8 : 8) * gemm_residents(c.tile);
     const int grid = (int)(items < slots ? (items + 7) / 8 * 8 : slots);
     if (std::getenv("DG_LOG"))
-      std::fprintf(stderr, "[dg] linear layout=%d m=%d n=%d k=%d -> tile %dx%d splits=%d grid=%d\n", layout, p.m, p.n,
-                   p.k, g.bm, g.bn, c.splits, grid);
+      std::fprintf(stderr, "[dg] linear layout=%d m=%d n=%d k=%d -> tile %dx%d wk=%d splits=%d grid=%d\n", layout, p.m, p.n,
+                   p.k, g.bm, g.bn, g.wk, c.splits, grid);
     if (c.splits == 1) return launch_gemm(layout, c.tile, p, grid, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
     p.ws_stride = (int64_t)p.m * p.n;
     bool owned = false;

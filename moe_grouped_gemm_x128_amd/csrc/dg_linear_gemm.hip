@@ -3,8 +3,10 @@
 // which read an operand with K as its row index (NN, TN) where it lies -- no
 // transposed copy is made.
 //
-// A workgroup of WM x WN waves owns a BM x BN tile; K goes in blocks of 64
-// values through a ring of S LDS stages filled by loads straight to LDS.
+// A workgroup owns a BM x BN tile; K goes in blocks of 64 values through a ring
+// of S LDS stages filled by loads straight to LDS.  It has WK groups of WM x WN
+// waves, each with every WK-th block of K and a share of a stage; their sums meet
+// in LDS, where each group takes FM / WK fragment rows of every wave's tile.
 // Stored layouts of a block in LDS:
 //   K contiguous: [row][64 k], 128-byte rows, 16-byte chunk c of row r at
 //     position c ^ swz(r); a fragment is one 16-byte read per lane;
@@ -133,35 +135,40 @@ struct Operand {
 };
 
 // LDS of a workgroup: the ring, and the epilogue's rows where they are its own.
-template <int BM, int BN, int WM, int WN, int S>
-constexpr int kLds = S * (BM + BN) * 128 + (S == 2 ? WM * WN * 16 * (BN / WN) * 4 : 0);
+template <int BM, int BN, int WM, int WN, int WK, int S>
+constexpr int kLds = WK * (S * (BM + BN) * 128 + (S == 2 && WK == 1 ? WM * WN * 16 * (BN / WN) * 4 : 0));
 
 // The items of one product that workgroup `wg` of `nwg` computes.  `p` is the
 // kernel's argument at byte ARG.  LINES: K is not split and every row of the
 // output, pre and residual is whole 16-byte pieces (a form of its own: the two
 // epilogues in one kernel cost the K loop some 45 registers).
-template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, bool LINES, int ARG>
+template <int BM, int BN, int WM, int WN, int WK, int S, bool TA, bool TB, bool LINES, int ARG>
 __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, uint8_t* smem) {
-  constexpr int NW = WM * WN;
+  constexpr int NW = WM * WN;  // waves of a group
   using OpA = Operand<BM, WM, NW, TA>;
   using OpB = Operand<BN, WN, NW, TB>;
   constexpr int FM = OpA::F, FN = OpB::F;
-  constexpr int STAGE = OpA::kBytes + OpB::kBytes;
+  constexpr int PART = OpA::kBytes + OpB::kBytes;  // a group's share of a stage
+  constexpr int STAGE = WK * PART;
+  constexpr int FR = FM / WK;  // fragment rows of C that a group finishes
+  static_assert(FM % WK == 0, "whole fragment rows per group");
   constexpr int LOADS = OpA::kQ + OpB::kQ;  // per wave and block
   // whole-line epilogue: 16 rows of a wave at a time, fp32, the 16-byte chunk c
   // of row r at c ^ r
   constexpr int RS = OpB::WTX * 4, RC = RS / 16;                        // bytes and chunks per row
   constexpr int LPR = OpB::WTX / 8, RPR = 64 / LPR, ROUNDS = 16 / RPR;  // lanes per row, rows per round
-  constexpr int kStores = FM * ROUNDS;                                   // 16-byte bf16 stores of a wave
-  constexpr bool kOwnRows = S == 2;
+  constexpr int kStores = FR * ROUNDS;                                   // 16-byte bf16 stores of a wave
+  constexpr bool kOwnRows = S == 2 && WK == 1;
   constexpr int kBehind = kOwnRows ? S - 1 : S - 2;  // blocks of the next item loaded before the stores
-  static_assert(kOwnRows || 16 * RS <= STAGE / NW, "a wave's rows fit its share of the slot");
+  // LDS that a wave's sums pass through, and (WK > 1) its rows that others finish
+  constexpr int kRows = 16 * RS, kGiven = (FM - FR) * FN * 1024;
+  static_assert(kOwnRows || (kRows <= PART / NW && kGiven <= PART / NW), "a wave's rows fit its share of the slot");
   static_assert((S - 2) * LOADS + 2 * kStores < 64, "vmcnt range");
 
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = (int)uniform(tid >> 6);
+  const int wave = (int)uniform((tid >> 6) % NW), wk = WK == 1 ? 0 : (int)uniform((tid >> 6) / NW);
   const int wm = wave / WN, wn = wave % WN;
-  const uint32_t lds0 = dma::lds_addr(smem);
+  const uint32_t lds0 = dma::lds_addr(smem) + wk * PART;
   OpA oa;
   OpB ob;
   oa.init(p.lda, wave, lane, wm);
@@ -212,19 +219,20 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
   auto enter = [&]() {
     li = next(lt);
     left = li.live ? li.k1 - li.k0 : 0;
-    pa = p.a + (TA ? (int64_t)li.k0 * p.lda + 2 * li.m0 : (int64_t)li.m0 * p.lda + 2 * (int64_t)li.k0);
-    pb = p.b + (TB ? (int64_t)li.k0 * p.ldb + 2 * li.n0 : (int64_t)li.n0 * p.ldb + 2 * (int64_t)li.k0);
+    const int64_t k0 = li.k0 + 64 * wk;  // (past the item's end: read by no load)
+    pa = p.a + (TA ? k0 * p.lda + 2 * li.m0 : (int64_t)li.m0 * p.lda + 2 * k0);
+    pb = p.b + (TB ? k0 * p.ldb + 2 * li.n0 : (int64_t)li.n0 * p.ldb + 2 * k0);
   };
   auto issue = [&](int slot) {
     const uint32_t st = uniform(lds0 + slot * STAGE);
-    oa.issue(pa, p.lda, (TA ? p.wa : p.m) - li.m0, left, st, wave);
-    ob.issue(pb, p.ldb, (TB ? p.wb : p.n) - li.n0, left, st + OpA::kBytes, wave);
-    left -= 64;
+    oa.issue(pa, p.lda, (TA ? p.wa : p.m) - li.m0, left - 64 * wk, st, wave);
+    ob.issue(pb, p.ldb, (TB ? p.wb : p.n) - li.n0, left - 64 * wk, st + OpA::kBytes, wave);
+    left -= 64 * WK;
     if (left <= 0) {
       if (li.live) enter();
     } else {
-      pa += TA ? 64 * p.lda : 128;
-      pb += TB ? 64 * p.ldb : 128;
+      pa += WK * (TA ? 64 * p.lda : 128);
+      pb += WK * (TB ? 64 * p.ldb : 128);
     }
   };
 
@@ -240,7 +248,7 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
   int q = 0;       // ring slot of the current block
   int stores = 0;  // the previous item's stores per kStores, 0: not counted
   while (cur.live) {
-    const int nkb = (cur.k1 - cur.k0 + 63) >> 6;
+    const int nkb = (cur.k1 - cur.k0 + 64 * WK - 1) / (64 * WK);
     v4f acc[FN][FM];
 #pragma unroll
     for (int i = 0; i < FN; ++i)
@@ -308,13 +316,47 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
     // come back as rows, 8 consecutive columns per lane
     {
       typedef __attribute__((address_space(3))) v4f* lp;
-      const uint32_t so = kOwnRows ? lds0 + S * STAGE + wave * 16 * RS : lds0 + last * STAGE + wave * (STAGE / NW);
+      const uint32_t so = kOwnRows ? lds0 + S * STAGE + wave * kRows : lds0 + last * STAGE + wave * (PART / NW);
+      const int j_first = wk * FR;  // the group's own fragment rows
+      if constexpr (WK > 1) {
+        // the groups' sums of one half of K each meet: a wave hands out the rows
+        // that others finish, in order, and adds what it gets in the groups' order
+        const uint32_t given = so;
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+          if (j / FR != wk) {
+            const int x = j - (j / FR > wk ? FR : 0);
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+              *(lp)(uintptr_t)(given + (x * FN + i) * 1024 + lane * 16) = acc[i][j];
+          }
+        dma::lds_done();
+        dma::barrier();
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+          if (j / FR == wk) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+              v4f sum = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int h = 0; h < WK; ++h) {
+                const uint32_t from = given + (h - wk) * PART + ((j - (j / FR > h ? FR : 0)) * FN + i) * 1024 + lane * 16;
+                if (h == wk)
+                  sum += acc[i][j];
+                else
+                  sum += *(lp)(uintptr_t)from;
+              }
+              acc[i][j] = sum;
+            }
+          }
+        dma::barrier();  // before the rows below take their place
+      }
       const int m0w = wm * OpA::WTX, n = cur.n0 + wn * OpB::WTX + 8 * (lane % LPR);
       const int rows = min(BM, p.m - cur.m0);
       const epi::Rows er = epi::rows_of(ep, cur.m0, rows, p.n);
       // residual rows are loaded kAhead rows of fragments before their use: a
       // load waits for the stores before it
-      constexpr int kAhead = FM < 4 ? FM : 4;
+      constexpr int kAhead = FR < 4 ? FR : 4;
       // fragment row j = STEP x + FIRST of the sums, into LDS (the loops over x
       // below are not unrolled: one copy of the epilogue's code per STEP rows; the
       // row is picked by an opaque bit, since the compiler makes "jc == j" an
@@ -344,16 +386,16 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
 #pragma unroll
           for (int h = 0; h < ROUNDS; ++h) {
             const int m = m0w + 16 * j + RPR * h + lane / LPR;
-            to[h] = epi::residual8(ep, er, m, n, j < FM && m < rows && n < p.n);
+            to[h] = epi::residual8(ep, er, m, n, j < j_first + FR && m < rows && n < p.n);
           }
         };
         constexpr bool kPlain = TB;  // the backward pass's products: nothing but the sums, in bf16
         if (!kPlain && ep.res) {
 #pragma unroll
-          for (int j = 0; j < kAhead; ++j) load_res(j, res[j]);
+          for (int j = 0; j < kAhead; ++j) load_res(j_first + j, res[j]);
         }
 #pragma unroll 1
-        for (int jo = 0; jo < FM; jo += kAhead) {
+        for (int jo = j_first; jo < j_first + FR; jo += kAhead) {
 #pragma unroll
           for (int ji = 0; ji < kAhead; ++ji) {
             const int j = jo + ji;
@@ -413,11 +455,11 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
         auto load_col = [&](int j) {
 #pragma unroll
           for (int e = 0; e < NV; ++e)
-            res[e] = __builtin_amdgcn_raw_buffer_load_b16(er.res, j < FM ? at(j, e, ep.ldr, 2) : kOut, 0, 0);
+            res[e] = __builtin_amdgcn_raw_buffer_load_b16(er.res, j < j_first + FR ? at(j, e, ep.ldr, 2) : kOut, 0, 0);
         };
-        if (with_res) load_col(0);
+        if (with_res) load_col(j_first);
 #pragma unroll 1
-        for (int j = 0; j < FM; ++j) {
+        for (int j = j_first; j < j_first + FR; ++j) {
           put(j, 0, 1);
           float v[NV];
 #pragma unroll
@@ -483,10 +525,10 @@ __device__ __forceinline__ void bias_sum(const float* partial, float* dbias, int
   if (wave == 0 && c < n) dbias[c] = (sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]);
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool TA, bool TB, bool LINES>
-__global__ __launch_bounds__(WM * WN * 64) void linear_gemm_kernel(const GemmParams p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds<BM, BN, WM, WN, S>];
-  run_items<BM, BN, WM, WN, S, TA, TB, LINES, 0>(p, blockIdx.x, gridDim.x, smem);
+template <int BM, int BN, int WM, int WN, int WK, int S, bool TA, bool TB, bool LINES>
+__global__ __launch_bounds__(WM * WN * WK * 64) void linear_gemm_kernel(const GemmParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds<BM, BN, WM, WN, WK, S>];
+  run_items<BM, BN, WM, WN, WK, S, TA, TB, LINES, 0>(p, blockIdx.x, gridDim.x, smem);
 }
 
 // The two products of the backward pass in one launch: workgroups below
@@ -501,13 +543,13 @@ struct PairParams {
   float* dbias;
   int chunks;
 };
-template <int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__(WM * WN * 64) void linear_gemm_pair_kernel(const PairParams p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds<BM, BN, WM, WN, S>];
+template <int BM, int BN, int WM, int WN, int WK, int S>
+__global__ __launch_bounds__(WM * WN * WK * 64) void linear_gemm_pair_kernel(const PairParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds<BM, BN, WM, WN, WK, S>];
   if ((int)blockIdx.x < p.first)
-    run_items<BM, BN, WM, WN, S, false, true, true, offsetof(PairParams, nn)>(p.nn, blockIdx.x, p.first, smem);
+    run_items<BM, BN, WM, WN, WK, S, false, true, true, offsetof(PairParams, nn)>(p.nn, blockIdx.x, p.first, smem);
   else if ((int)blockIdx.x < p.grid)
-    run_items<BM, BN, WM, WN, S, true, true, true, offsetof(PairParams, tn)>(p.tn, blockIdx.x - p.first,
+    run_items<BM, BN, WM, WN, WK, S, true, true, true, offsetof(PairParams, tn)>(p.tn, blockIdx.x - p.first,
                                                                              p.grid - p.first, smem);
   else
     bias_sum(p.partial, p.dbias, p.chunks, p.tn.m, blockIdx.x - p.grid, reinterpret_cast<float(*)[64]>(smem));
@@ -517,9 +559,9 @@ template <int TILE, bool TA, bool TB>
 hipError_t launch_tile(const GemmParams& p, int grid, hipStream_t stream) {
   constexpr GemmTile t = kGemmTiles[TILE];
   if (p.splits == 1 && p.epi.vec8)
-    linear_gemm_kernel<t.bm, t.bn, t.wm, t.wn, t.stages, TA, TB, true><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
+    linear_gemm_kernel<t.bm, t.bn, t.wm, t.wn, t.wk, t.stages, TA, TB, true><<<grid, gemm_threads(t), 0, stream>>>(p);
   else
-    linear_gemm_kernel<t.bm, t.bn, t.wm, t.wn, t.stages, TA, TB, false><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
+    linear_gemm_kernel<t.bm, t.bn, t.wm, t.wn, t.wk, t.stages, TA, TB, false><<<grid, gemm_threads(t), 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -534,7 +576,7 @@ template <int TILE>
 hipError_t launch_both(const PairParams& p, hipStream_t stream) {
   constexpr GemmTile t = kGemmTiles[TILE];
   const int grid = p.grid + (p.dbias ? (p.tn.m + 63) / 64 : 0);
-  linear_gemm_pair_kernel<t.bm, t.bn, t.wm, t.wn, t.stages><<<grid, t.wm * t.wn * 64, 0, stream>>>(p);
+  linear_gemm_pair_kernel<t.bm, t.bn, t.wm, t.wn, t.wk, t.stages><<<grid, gemm_threads(t), 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -653,6 +695,9 @@ hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipS
     case 2: return launch_layout<2>(layout, p, grid, stream);
     case 3: return launch_layout<3>(layout, p, grid, stream);
     case 4: return launch_layout<4>(layout, p, grid, stream);
+    case 5: return launch_layout<5>(layout, p, grid, stream);
+    case 6: return launch_layout<6>(layout, p, grid, stream);
+    case 7: return launch_layout<7>(layout, p, grid, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -156,6 +156,31 @@ def test_many_tiles_per_workgroup(dg, force):
         forward_case(dg, 2048 + 40, 8192 + 24, 72, "silu", bias=F32)
 
 
+# tiles by one or two groups of waves that share K
+TILES_K = [f"{t}x{w}" for t in ("128x128x2x2", "64x128x2x2", "64x64x2x2") for w in (1, 2)]
+
+
+@pytest.mark.parametrize("tile", TILES_K)
+@pytest.mark.parametrize("m,n,k,splits,fits", [(5, 9, 64, None, 0), (70, 200, 72, None, 0), (300, 390, 200, None, 0),
+                                               (257, 264, 1032, None, 0), (130, 129, 712, 4, 0), (65, 128, 8, None, 0),
+                                               (1100, 2056, 136, None, 8)])
+def test_forward_tiles_by_groups(dg, force, tile, m, n, k, splits, fits):
+    force(tile, splits)
+    say(f"linear tile {tile} {m}x{n}x{k} splits={splits}")
+    o = forward_case(dg, m, n, k, "gelu", bias=F32, residual=True, pre=True, pad=fits)
+    again = forward_case(dg, m, n, k, "gelu", bias=F32, residual=True, pre=True, pad=fits)
+    assert torch.equal(o, again), "not deterministic"
+
+
+@pytest.mark.parametrize("tile", TILES_K)
+def test_backward_parts_by_groups(dg, force, tile):
+    force(tile)
+    say(f"linear backward tile {tile}")
+    for which in ((True, False, True), (False, True, False)):
+        for m, n, k in ((300, 260, 392), (713, 333, 264), (65, 8, 200)):
+            backward_case(dg, m, n, k, "silu", which=which)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 64, 128), (19, 283, 2816), (64, 4500, 256), (65, 70, 3840), (300, 256, 1024),
                                    (700, 1030, 512)])
 def test_fp8_with_fp32_result_is_that_exact(dg, m, n, k):
