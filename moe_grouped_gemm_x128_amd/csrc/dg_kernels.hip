@@ -1351,12 +1351,27 @@ __global__ __launch_bounds__(256) void splitk_linear_kernel(const Epilogue e, co
     const float* w = ws + row * n + c;
     v4f v = epi::bias4(e, c, n);
     if (vec_ws && c + 3 < n) {
-      for (int sp = 0; sp < splits; ++sp) v += *reinterpret_cast<const v4f*>(w + sp * ws_stride);
-    } else {
+      // (the splits' loads in flight together, the sums in order)
+      for (int s0 = 0; s0 < splits; s0 += 8) {
+        v4f u[8];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (c + r < n)
-          for (int sp = 0; sp < splits; ++sp) v[r] += w[sp * ws_stride + r];
+        for (int x = 0; x < 8; ++x)
+          u[x] = s0 + x < splits ? *reinterpret_cast<const v4f*>(w + (s0 + x) * ws_stride) : v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v += u[x];
+      }
+    } else {
+      for (int s0 = 0; s0 < splits; s0 += 4) {
+        float u[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) u[x][r] = s0 + x < splits && c + r < n ? w[(s0 + x) * ws_stride + r] : 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] += u[x][r];
+      }
     }
     epi::finish4(e, row, c, n, v);
   }

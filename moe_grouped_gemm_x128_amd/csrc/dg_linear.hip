@@ -62,30 +62,37 @@ dg_status make_epilogue(void* c, int64_t ldc, int c_type, const dg_epilogue* in,
 }
 
 // The model behind the choice of tile and K splits, in microseconds:
-//   passes over the workgroups x (K blocks x time per block + fixed time per
-//   item) + (split) the partials' write and read and the second launch.
+//   passes over the workgroups x (K blocks x time per block + a fixed time and
+//   one by the tile's area per item) + (split) the partials' write and read and
+//   the second launch.
 // Rates (TFLOP/s of the whole card on full CUs), the share of a block's time
 // that a workgroup alone on a CU needs where two would share it, and the other
-// constants are fitted to timings of every tile and split at 150 sizes drawn
-// from 65..5000 x 64..9000, K 256..8192: the choice is 1.5% behind the best in
+// constants are fitted to timings of every tile and split at 140 sizes drawn
+// from 65..5000 x 64..9000, K 256..8192: the choice is 1% behind the best in
 // the mean.  A workgroup alone on a CU is bound by the chain of a block (wait,
 // barrier, loads issued, fragments read, MFMAs), not by bandwidth: hence the
 // tiles of two groups, which halve the number of such steps (333 x 2111 x 1536:
 // 11.6 us on 64x64 with two groups, 14.6 with one; 1024 x 4096 x 4096: 54.6 us
 // on 128x128 against 66.6), while one group is better where two workgroups
 // share a CU (517 x 1161 x 1096 backward: 18.4 us against 22.4).
-constexpr double kTileRate[kNumGemmTiles] = {1370., 700., 1220., 740., 660., 880., 650., 560.};
-constexpr double kAlone = 0.82, kItemUs = 2.4, kSplitUs = 4.5, kPartialBytesPerUs = 5.7e6;
+constexpr double kTileRate[kNumGemmTiles] = {1280., 660., 1210., 720., 620., 880., 690., 540.};
+// the same of the two products of the backward pass in one launch (42 sizes:
+// 0.3% behind the best)
+constexpr double kPairRate[kNumPairTiles] = {1390., 1060., 1190., 820., 600.};
+constexpr double kTwoUs = 6.0;
+constexpr double kAlone = 0.91, kItemUs = 2.4, kAreaUs = 2.2 / 65536;
+constexpr double kSplitUs = 2.1, kPartialUs = 0.4, kPartialBytesPerUs = 5.9e6;
 
 // time per K block and per item
 struct TileTime {
   double block, item;
 };
-TileTime tile_time(int tile, int cus, bool alone) {
+TileTime tile_time(int tile, double rate, int cus, bool alone) {
   const GemmTile g = kGemmTiles[tile];
   const int res = gemm_residents(tile);
-  const double us = 2.0 * g.bm * g.bn * 64 * cus * res / (kTileRate[tile] * 1e6);
-  return alone && res > 1 ? TileTime{us * kAlone, kItemUs} : TileTime{us, kItemUs * res};
+  const double us = 2.0 * g.bm * g.bn * 64 * cus * res / (rate * 1e6);
+  const double item = kItemUs + kAreaUs * g.bm * g.bn;
+  return alone && res > 1 ? TileTime{us * kAlone, item} : TileTime{us, item * res};
 }
 
 bool forced_out(const GemmTile& g) {  // DG_FORCE_TILE names another tile
@@ -118,9 +125,9 @@ Plan plan(int m, int n, int k, int cus, bool may_split) {
       const double bytes = 4.0 * s * m * n;
       if (s > 1 && (bytes > 256e6 || (chunk < 4 && !force))) break;
       const double passes = (double)((tiles * s + slots - 1) / slots);
-      const TileTime w = tile_time(t, cus, tiles * s <= cus);
+      const TileTime w = tile_time(t, kTileRate[t], cus, tiles * s <= cus);
       double us = passes * (chunk * w.block + w.item);
-      if (s > 1) us += kSplitUs + 2.0 * bytes / kPartialBytesPerUs;
+      if (s > 1) us += kSplitUs + kPartialUs * s + 2.0 * bytes / kPartialBytesPerUs;
       if (us < best.us) best = Plan{t, s, chunk, us};
     }
   }
@@ -143,7 +150,7 @@ PairPlan plan_pair(const GemmParams& nn, const GemmParams& tn, int cus) {
     if (ta > (1 << 24) || tb > (1 << 24)) continue;
     const int64_t slots = (int64_t)(cus > 16 ? cus / 8 * 8 : 16) * gemm_residents(t);
     const int ka = ceil_div(nn.k, 64), kb = ceil_div(tn.k, 64);
-    const TileTime w = tile_time(t, cus, ta + tb <= cus);
+    const TileTime w = tile_time(t, kPairRate[t], cus, ta + tb <= cus);
     for (int passes = 1; passes <= 16; ++passes) {  // of da's workgroups
       const int64_t first = (ceil_div(ta, passes) + 7) / 8 * 8;
       if (first >= slots) continue;
@@ -356,8 +363,11 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
   if (da && db && nn.epi.vec8 && tn.epi.vec8) {
     const PairPlan c = plan_pair(nn, tn, cus);
     const Plan ca = plan(nn.m, nn.n, nn.k, cus, may_split), cb = plan(tn.m, tn.n, tn.k, cus, may_split);
-    // (two launches where splitting K gains more than sharing the card)
-    if (c.tile >= 0 && c.us <= ca.us + cb.us) {
+    // Two launches where splitting K gains more than sharing the card does:
+    // 45 x 6920 x 2520 37 us against 47.  (kTwoUs: what the second launch and the
+    // transposed operands cost beyond the model; 517 x 1161 x 1096 is 18 us in
+    // one launch and 27 in two, where the model sees 17 and 17.)
+    if (c.tile >= 0 && c.us <= ca.us + cb.us + kTwoUs) {
       const GemmTile tile = kGemmTiles[c.tile];
       set_tiles(nn, tile, 1, ceil_div(nn.k, 64));
       set_tiles(tn, tile, 1, ceil_div(tn.k, 64));
