@@ -328,18 +328,21 @@ typedef struct {
   int64_t ld_pre;
 } dg_epilogue;
 
-/* BF16: a [M,K], b [N,K]; c [M,N] of c_type.  K % 8 == 0, K <= 2^22; a, b 16-byte
- * aligned with lda, ldb multiples of 8; lda, ldb <= 2^22; c, bias, residual and
- * pre aligned to their element, their rows at most 2^20 elements apart.  Few rows (M <= 64) run in one kernel that
- * streams b; more run on tiles, with K split over workgroups (fp32 partials in the
- * stream's split-K workspace, see above; not while capturing) where there are few.
- * epi null: the plain product. */
+/* BF16: a [M,K], b [N,K]; c [M,N] of c_type.  K % 8 == 0, K <= 2^22; a, b
+ * 16-byte aligned with lda, ldb multiples of 8 up to 2^22; c, bias, residual and
+ * pre aligned to their element, their rows at most 2^20 elements apart.  Few rows
+ * (M <= 64) run in one kernel that streams b; more (and, from 17 rows, long K) run
+ * on tiles, with K split over workgroups where tiles are few (fp32 partials in
+ * the stream's split-K workspace, see above; not while capturing, so a captured
+ * call may add up in another order).  epi null: the plain product. */
 dg_status dg_gemm_bf16_nt_epilogue(const void* a, int64_t lda, const void* b, int64_t ldb, void* c,
                                    int64_t ldc, int c_type, const dg_epilogue* epi, int m, int n,
                                    int k, hipStream_t stream);
 
 /* FP8: operands and scales as dg_gemm_fp8_nt (contiguous rows, K % 128 == 0,
- * K <= 2^22). */
+ * K <= 2^22).  An fp32 C is computed from exact products (the codes multiplied
+ * as bf16); for a bf16 C the FP8 matrix instructions' sums are 1.5e-5 off, far
+ * below its own rounding. */
 dg_status dg_gemm_fp8_nt_epilogue(const void* a, const float* sa, const void* b, const float* sb,
                                   void* c, int64_t ldc, int c_type, const dg_epilogue* epi, int m,
                                   int n, int k, hipStream_t stream);

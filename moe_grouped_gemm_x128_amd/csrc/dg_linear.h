@@ -21,6 +21,8 @@ struct RowsParams {
   int m, n, k;       // k in values
   Epilogue epi;
 };
+// Columns of C per workgroup: 16 where 32 would occupy at most half of the CUs
+constexpr int few_rows_columns(int n, int num_cus) { return n <= 16 * num_cus ? 16 : 32; }
 hipError_t launch_linear_rows(bool fp8, const RowsParams& p, int num_cus, hipStream_t stream);
 
 // Tiles, BF16: C[m, n] = sum_k A(m, k) B(n, k).  An operand is stored with K

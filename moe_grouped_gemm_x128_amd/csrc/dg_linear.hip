@@ -134,6 +134,23 @@ Plan plan(int m, int n, int k, int cus, bool may_split) {
   return best;
 }
 
+// Whether M <= 64 rows of BF16 go to the kernel that streams B.  Each of its
+// workgroups reads all of A beside its 16 or 32 rows of B, at some 65 KB per
+// microsecond: up to 16 rows B is most of it, with more rows and a long K the
+// tiles with K split are faster (64 x 4096 x 7168: 18.1 us against 23.0, 48 x 2112 x
+// 7168 15.0 against 19.5), with a short K slower (64 x 8192 x 1024: 9.5 against
+// 8.6).  (kBesideUs: launches, which the tiles' model leaves out.)  FP8 halves
+// A too: there it is the faster one for all M <= 64 (64 x 4096 x 7168 15.5 us
+// against 16.0, 17 x 4096 x 7168 10.2 against 12.8).
+constexpr double kRowsUs = 4.3, kRowsBytesPerUs = 65e3, kBesideUs = 2.5;
+
+bool few_rows(int m, int n, int k, int cus, bool may_split) {
+  if (m > kMaxFewRows) return false;
+  if (m <= 16) return true;
+  const double us = kRowsUs + 2.0 * k * (m + few_rows_columns(n, cus)) / kRowsBytesPerUs;
+  return us <= plan(m, n, k, cus, may_split).us + kBesideUs;
+}
+
 // da and db in one launch: the tile, and how many of its workgroups da gets.
 struct PairPlan {
   int tile, first, grid;
@@ -234,7 +251,8 @@ dg_status dg_gemm_bf16_nt_epilogue(const void* a, int64_t lda, const void* b, in
   if (cus <= 0) return DG_ERROR_LAUNCH;
   (void)hipGetLastError();  // clear a stale error from unrelated work
   const char* force = std::getenv("DG_FORCE_TILE");
-  if (m <= kMaxFewRows && !(force && *force)) {
+  const bool may_split = !is_capturing(stream);
+  if (!(force && *force) && few_rows(m, n, k, cus, may_split)) {
     RowsParams p{};
     p.a = static_cast<const uint8_t*>(a);
     p.b = static_cast<const uint8_t*>(b);
@@ -255,7 +273,7 @@ dg_status dg_gemm_bf16_nt_epilogue(const void* a, int64_t lda, const void* b, in
   p.n = n;
   p.k = k;
   p.epi = e;
-  return gemm(kNT, p, cus, !is_capturing(stream), stream);
+  return gemm(kNT, p, cus, may_split, stream);
 }
 
 dg_status dg_gemm_fp8_nt_epilogue(const void* a, const float* sa, const void* b, const float* sb, void* c, int64_t ldc,

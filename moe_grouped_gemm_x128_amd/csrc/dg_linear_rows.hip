@@ -118,8 +118,7 @@ __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p)
 template <int MODE, int NT, bool EXACT>
 hipError_t launch(const RowsParams& p, int cus, hipStream_t stream) {
   constexpr int W = 8, D = 4;
-  // 16 columns per workgroup where 32 would occupy at most half of the CUs
-  if (p.n <= 16 * cus)
+  if (few_rows_columns(p.n, cus) == 16)
     linear_rows_kernel<MODE, NT, true, EXACT, W, D><<<(p.n + 15) / 16, W * 64, 0, stream>>>(p);
   else
     linear_rows_kernel<MODE, NT, false, EXACT, W, D><<<(p.n + 31) / 32, W * 64, 0, stream>>>(p);
