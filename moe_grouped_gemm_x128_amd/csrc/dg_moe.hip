@@ -7,19 +7,24 @@
 //
 // Bound: the chosen experts' weights, each read once (a few tokens give each
 // weight a handful of operations).  So both kernels stream weights from HBM
-// straight into registers with 16-byte nontemporal loads, several units
-// (dg_stream.h: 16 rows x 128 K) ahead, and everything else is arranged around
-// that: the activations (bf16, a few KB) are re-read through the L2 by every
-// workgroup, fp8 weights are widened to bf16 in registers (exact), and the
-// products run on the bf16 MFMA with the tokens of one expert as its 16
-// columns -- the matrix unit has an order of magnitude to spare.
+// through a ring of LDS per wave, filled by loads of whole 128-byte lines several
+// units (dg_stream.h) ahead, and everything else is arranged around that: the
+// activations (bf16, a few KB) are re-read through the L2 by every workgroup,
+// fp8 weights are widened to bf16 in registers (exact), and the products run on
+// the bf16 MFMA with the tokens of one expert as its 16 columns -- the matrix unit
+// has an order of magnitude to spare.
 //
 // The routing weight is folded into h, so the second kernel only sums; a
-// workgroup of it owns 16 R output columns for all experts and tokens, which
+// workgroup of it owns 16 or 32 output columns for all experts and tokens, which
 // makes the combination over experts a private sum: no atomics, a fixed order.
 //
-// h is rounded to bf16 once (the MFMA's operand type; relative error 2^-9 per
-// value, the size of the output's own rounding); every sum is fp32.
+// h is rounded to bf16 once (the MFMA's operand type; up to 2^-8 of each value,
+// the size of the output's own rounding); every sum is fp32.
+//
+// Measured: one token, 8 of 16 experts of 7168 x 2048 in fp8 (352 MB) 70.6 us,
+// 5.0 TB/s; 13 tokens, 4 of 16 of 4096 x 1536 in bf16 (604 MB) 94 us, 6.3 TB/s; 64
+// tokens, 8 of 64 of 7168 x 2048 in fp8 (2.8 GB) 569 us, 5.0 TB/s (a device copy:
+// 5.2 TB/s).
 #include <climits>
 #include <cstdint>
 
