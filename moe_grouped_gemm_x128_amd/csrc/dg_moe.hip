@@ -21,9 +21,9 @@
 // h is rounded to bf16 once (the MFMA's operand type; up to 2^-8 of each value,
 // the size of the output's own rounding); every sum is fp32.
 //
-// Measured: one token, 8 of 16 experts of 7168 x 2048 in fp8 (352 MB) 70.6 us,
-// 5.0 TB/s; 13 tokens, 4 of 16 of 4096 x 1536 in bf16 (604 MB) 94 us, 6.3 TB/s; 64
-// tokens, 8 of 64 of 7168 x 2048 in fp8 (2.8 GB) 569 us, 5.0 TB/s (a device copy:
+// Measured: one token, 8 of 16 experts of 7168 x 2048 in fp8 (352 MB) 67.3 us,
+// 5.2 TB/s; 13 tokens, 4 of 16 of 4096 x 1536 in bf16 (604 MB) 94 us, 6.3 TB/s; 64
+// tokens, 8 of 64 of 7168 x 2048 in fp8 (2.8 GB) 489 us, 5.8 TB/s (a device copy:
 // 5.2 TB/s).
 #include <climits>
 #include <cstdint>
@@ -553,7 +553,11 @@ hipError_t launch_moe(const MoeParams& p, int cus, hipStream_t stream) {
   const long pairs = (long)p.t * p.top_k;
   const long items = (pairs < p.experts ? pairs : p.experts) * (p.inter / 16);
   const int grid = (int)(items < cus ? items : cus);
-  constexpr int W = 8, D = 4;
+  // Waves and ring entries per wave that fit the LDS.  fp8 weights take more work
+  // per byte (widening), so more waves beat deeper rings: one token on 8 experts of
+  // 7168 x 2048 67.2 us with 12 waves of 2 entries, 69.9 with 8 of 4; bf16 weights
+  // the other way round: 13 tokens on 4096 x 1536 94 against 97.
+  constexpr int W = MODE == kW8A16 ? 12 : 8, D = MODE == kW8A16 ? 2 : 4;
   if (p.logits)
     moe_up_kernel<MODE, true, W, D><<<grid, W * 64, 0, stream>>>(p);
   else
@@ -564,13 +568,18 @@ hipError_t launch_moe(const MoeParams& p, int cus, hipStream_t stream) {
   const bool narrow = p.hid <= 16 * cus;
   if (p.t <= 16) {
     if (narrow)
-      moe_down_kernel<MODE, 16, true, 8, 4><<<p.hid / 16, 8 * 64, 0, stream>>>(p);
+      moe_down_kernel<MODE, 16, true, W, D><<<p.hid / 16, W * 64, 0, stream>>>(p);
     else
-      moe_down_kernel<MODE, 16, false, 8, 4><<<p.hid / 32, 8 * 64, 0, stream>>>(p);
-  } else if (narrow) {
-    moe_down_kernel<MODE, kMaxTokens, true, 4, 7><<<p.hid / 16, 4 * 64, 0, stream>>>(p);
+      moe_down_kernel<MODE, 16, false, W, D><<<p.hid / 32, W * 64, 0, stream>>>(p);
+    return hipGetLastError();
+  }
+  // (the waves' sums of 64 tokens take half of the LDS: 64 tokens on 64 experts of
+  // 7168 x 2048 490 us with 8 waves of 2 entries, 522 with 6 of 3, 565 with 4 of 6)
+  if (narrow) {
+    constexpr int WN = MODE == kW8A16 ? 10 : 8, DN = MODE == kW8A16 ? 2 : 3;
+    moe_down_kernel<MODE, kMaxTokens, true, WN, DN><<<p.hid / 16, WN * 64, 0, stream>>>(p);
   } else {
-    moe_down_kernel<MODE, kMaxTokens, false, 4, 6><<<p.hid / 32, 4 * 64, 0, stream>>>(p);
+    moe_down_kernel<MODE, kMaxTokens, false, 8, 2><<<p.hid / 32, 8 * 64, 0, stream>>>(p);
   }
   return hipGetLastError();
 }
