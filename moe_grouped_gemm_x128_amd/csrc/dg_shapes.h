@@ -36,10 +36,10 @@ constexpr int kBlockK = 128;  // K block = scale granularity
 // columns of its rows.
 constexpr bool excluded(int bm, int bn, int wm, int kind) {
   if (kind == KIND_CONTIG_SWIGLU) return !(bm == 256 && bn == 256 && (wm == 1 || wm == 2));
-  // the linear layer: the tiles that the heuristic gives the dense layout
-  // (fp32 outputs: 128x128 at most, since a converted fragment takes twice the registers)
+  // the linear layer: the tiles that its planner knows (linear_tile in dg_api.hip;
+  // fp32 outputs: 128x128 at most, since a converted fragment takes twice the registers)
   if (kind == KIND_DENSE_LINEAR_F32 && bm > 128) return true;
-  if (kind == KIND_DENSE_LINEAR && bn != 256 && !(bm == 256 && bn == 128 && wm == 2) && bm > 128) return true;
+  if (kind == KIND_DENSE_LINEAR && bm > 128 && (bn < 128 || wm != 2)) return true;
   // the power-of-two kinds have their fp32-scale kind's instances
   kind = layout_of(kind);
   // 192-row tiles: dense layouts only (a grouped layout's 128-row blocks would
