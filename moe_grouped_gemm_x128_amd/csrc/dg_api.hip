@@ -5,10 +5,10 @@
 
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
-#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -201,7 +201,8 @@ dg::TileShape heuristic(int kind, int rows, int n, int k, int groups, int num_cu
 // choice is 6% behind the best in the mean, where the heuristic above, made for
 // the plain GEMM's sizes, is 40% behind (294 x 1548 x 3200: 14 us against 27; 809
 // x 68 x 1664: 8.5 against 17).
-dg::TileShape linear_tile(int kind, int rows, int n, int k, int num_cus, bool allow_split, int* splits) {
+dg::TileShape linear_tile(int kind, int rows, int n, int k, int num_cus, bool allow_split, bool residual,
+                          int* splits) {
   struct Tile {
     dg::TileShape s;
     double rate;
@@ -210,7 +211,10 @@ dg::TileShape linear_tile(int kind, int rows, int n, int k, int num_cus, bool al
                                {{128, 128, 2, 2}, 930.},  {{128, 64, 2, 2}, 450.},   {{64, 128, 1, 4}, 480.},
                                {{64, 64, 1, 4}, 890.},    {{64, 32, 2, 2}, 520.}};
   constexpr double kAlone = 0.79;                              // time per block of a workgroup without a neighbour
-  constexpr double kItemUs = 2.5, kAreaUs = 2.9, kOddUs = 11.5;  // per 65536 outputs; rows not in 16-byte pieces
+  constexpr double kItemUs = 2.5, kAreaUs = 2.9;               // per 65536 outputs
+  // the same of rows not in 16-byte pieces, on 8 waves (2-byte accesses from where
+  // the MFMA leaves the sums, the residual's too) and on 4
+  const double kOddUs = residual ? 35.0 : 12.0, kOddUs4 = 8.0;
   constexpr double kSplitUs = 2.0, kPartialUs = 0.34, kPartialBytesPerUs = 3.8e6;
   const int kbs = k / 128;
   dg::TileShape best{128, 128, 2, 2};
@@ -229,7 +233,7 @@ dg::TileShape linear_tile(int kind, int rows, int n, int k, int num_cus, bool al
       const double bytes = 4.0 * sp * rows * n;
       if (sp > 1 && bytes > (double)kMaxWorkspaceBytes) break;
       const bool alone = occ > 1 && count * sp <= num_cus;
-      const double item = kItemUs + (sp == 1 && n % 8 != 0 ? kOddUs : kAreaUs) * area;
+      const double item = kItemUs + (sp > 1 || n % 8 == 0 ? kAreaUs : t.s.wm * t.s.wn == 8 ? kOddUs : kOddUs4) * area;
       double us = std::ceil(count * sp / slots) * (alone ? chunk * block * kAlone + item : chunk * block + occ * item);
       if (sp > 1) us += kSplitUs + kPartialUs * sp + 2 * bytes / kPartialBytesPerUs;
       if (us < least) {
@@ -256,7 +260,7 @@ dg_status plan(int kind, int rows, int n, int k, int groups, int num_cus, bool a
   const bool linear = !forced && dg::linear_kind(kind);
   int linear_splits = 1;
   if (linear)
-    s = linear_tile(kind, rows, n, k, num_cus, allow_split, &linear_splits);
+    s = linear_tile(kind, rows, n, k, num_cus, allow_split, p.epi.res != nullptr, &linear_splits);
   else if (!forced)
     s = heuristic(kind, rows, n, k, groups, num_cus, allow_split);
   if (!dg::has_instance(kind, s)) return DG_ERROR_UNSUPPORTED;

@@ -256,6 +256,9 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
       ((LAYOUT == KIND_DENSE || KIND == KIND_BF16) && BM <= 128) || LAYOUT == KIND_MASKED;
   constexpr bool kLinear = linear_kind(KIND);  // bias, activation, residual in the epilogue
   constexpr bool kExact = KIND == KIND_DENSE_LINEAR_F32;
+  // the linear layer's rows in 2-byte pieces by way of LDS: not on 8 waves, whose
+  // registers are full (the 256x256 tile would spill: 4096 x 4096 x 7168 161 us for 128)
+  constexpr bool kOddRows = KIND == KIND_DENSE_LINEAR && NW == 4 && (WTN == 64 || WTN == 32);
   constexpr bool kDirectAcc = kPow2 || kBf16;         // MFMAs accumulate into acc: no promotion
   constexpr bool kFp32Out = kRowScaleB;
   // the columns of one wave tile sit inside one 128-block: one sb per wave
@@ -1133,6 +1136,73 @@ __global__ __launch_bounds__(WM * WN * 64) void fp8_gemm_kernel(const Params p) 
         __builtin_amdgcn_sched_barrier(0);  // one fragment row at a time (registers)
       }
       (void)sbase;
+    } else if (kOddRows && splits == 1 && !p.epi.pre) {
+      // the linear layer's rows that do not start on 16-byte boundaries: the same
+      // way through LDS, but one column per lane on the way out, so that a store
+      // covers whole runs of a row (1342 x 3091 x 256 with a residual: 31 us; 2-byte
+      // accesses from where the MFMA leaves the sums 50)
+      uint8_t* so = sOut[kStage ? wave : 0];
+      const uint32_t ldo = (uint32_t)p.epi.ldc;
+      const __amdgpu_buffer_rsrc_t ro =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(static_cast<uint16_t*>(p.out) + out_row0 * (int64_t)ldo), (short)0,
+                                            (int)(((uint32_t)(rows - 1) * ldo + p.n) * 2), 0x00020000);
+      constexpr int RPV = 64 / WTN > 0 ? 64 / WTN : 1, NV = 16 * WTN / 64;  // rows per store, stores per 16 rows
+      const int rl = lane / WTN, col = lane % WTN, nc = n0 + wn * WTN + col;
+      // byte offset of value e of fragment row j in rows of ld elements (from an
+      // opaque copy of the lane's row, so that the offsets are not kept)
+      auto at = [&](int j, int e, uint32_t ld) -> uint32_t {
+        int r = e * RPV + rl;
+        asm("" : "+v"(r));
+        const int ml = wm * WTM + 16 * j + r;
+        return ml < rows && nc < p.n ? ((uint32_t)ml * ld + nc) * 2u : 0x80000000u;
+      };
+      v4f bias[FN];
+#pragma unroll
+      for (int i = 0; i < FN; ++i) bias[i] = epi::bias4(p.epi, n0 + wn * WTN + 16 * i + 4 * lq, p.n);
+      // (the residual comes in the same way, before the first store)
+      const bool with_res = p.epi.res != nullptr;
+      const __amdgpu_buffer_rsrc_t rr = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(p.epi.res + out_row0 * p.epi.ldr), (short)0,
+          with_res ? (int)(((uint32_t)(rows - 1) * (uint32_t)p.epi.ldr + p.n) * 2) : 0, 0x00020000);
+      uint16_t rv[NV];
+      auto load_res = [&](int j) {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) rv[e] = __builtin_amdgcn_raw_buffer_load_b16(rr, at(j, e, (uint32_t)p.epi.ldr), 0, 0);
+      };
+      if (with_res) load_res(0);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        if (with_res) {
+#pragma unroll
+          for (int e = 0; e < NV; ++e)
+            *reinterpret_cast<uint16_t*>(so + (e * RPV + rl) * kStageRow + col * 2) = rv[e];
+          if (j + 1 < FM) load_res(j + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+          v4f& v = acc[i][j];
+          v += bias[i];
+          act::apply<4>(v, p.epi.act);
+          if (with_res)
+            v += epi::unpack4(*reinterpret_cast<const uint2*>(so + l16 * kStageRow + (16 * i + 4 * lq) * 2));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+          const uint32_t lo = (uint32_t)f32_to_bf16(acc[i][j][0]) | ((uint32_t)f32_to_bf16(acc[i][j][1]) << 16);
+          const uint32_t hi = (uint32_t)f32_to_bf16(acc[i][j][2]) | ((uint32_t)f32_to_bf16(acc[i][j][3]) << 16);
+          *reinterpret_cast<uint2*>(so + l16 * kStageRow + (16 * i + 4 * lq) * 2) = uint2{lo, hi};
+        }
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+          const uint16_t v = *reinterpret_cast<const uint16_t*>(so + (e * RPV + rl) * kStageRow + col * 2);
+          __builtin_amdgcn_raw_buffer_store_b16(v, ro, at(j, e, ldo), 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     } else if (exact_stores) {
       // One buffer store per fragment pair, issued whether or not its lanes
       // are valid: a lane whose row or columns fall outside the output gets
