@@ -198,7 +198,7 @@ dg::TileShape heuristic(int kind, int rows, int n, int k, int groups, int num_cu
 //   the tile's area per item) + (split) the partials and the second launch.
 // Rates (TFLOP/s of the whole card), and the rest, are fitted to timings of every
 // tile and split at 190 sizes drawn from 65..5000 x 64..9000, K 256..8192: the
-// choice is 6% behind the best in the mean, where the heuristic above, made for
+// choice is 4% behind the best in the mean, where the heuristic above, made for
 // the plain GEMM's sizes, is 40% behind (294 x 1548 x 3200: 14 us against 27; 809
 // x 68 x 1664: 8.5 against 17).
 dg::TileShape linear_tile(int kind, int rows, int n, int k, int num_cus, bool allow_split, bool residual,
