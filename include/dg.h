@@ -43,7 +43,8 @@
  *     in [0, G) is left untouched, masked_m[g] is clamped to [0, M_max].
  *   - environment overrides for tests and tuning, read at each call:
  *     DG_FORCE_TILE=BMxBNxWMxWN forces a tile instance (UNSUPPORTED if the kind
- *     has none), DG_FORCE_SPLITS=s forces s K splits where splitting is
+ *     has none; the linear layer's BF16 tiles take a fifth number, xWK, the
+ *     groups of waves that share K), DG_FORCE_SPLITS=s forces s K splits where splitting is
  *     allowed, DG_LOG=1 prints each plan to stderr.  Results stay within the
  *     same accuracy bound either way.
  */
