@@ -650,30 +650,31 @@ __global__ __launch_bounds__(256) void dact_kernel(const DactParams p) {
 
 // Other rows: one column per lane (2-byte accesses that cover whole runs), 16
 // rows in flight (517 x 1161: 5 us; columns 32 apart by one lane, each behind its
-// own branch, 13).
+// own branch, 13).  Rows may lie any distance apart: their starts are 64-bit and
+// uniform, a lane's column is 32-bit.  Lanes and rows past the end read the last
+// column and row again, so that no load has a branch, and drop what they get.
 __global__ __launch_bounds__(256) void dact_columns_kernel(const DactParams p) {
   const int c = blockIdx.x * 256 + threadIdx.x, r0 = blockIdx.y * p.rows;
   const int rows = min(p.rows, p.m - r0);
   const bool in = c < p.n;
-  auto rows_from = [&](const uint16_t* at, int64_t ld) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)(at + (int64_t)r0 * ld), (short)0,
-                                             at ? (int)(2 * ((rows - 1) * ld + p.n)) : 0, 0x00020000);
+  const uint32_t at = 2u * (uint32_t)min(c, p.n - 1);  // bytes into a row
+  auto value = [&](const uint16_t* base, int64_t ld, int r) {
+    const uint8_t* row = reinterpret_cast<const uint8_t*>(base + (int64_t)(r0 + min(r, rows - 1)) * ld);
+    return epi::from_bf16(*reinterpret_cast<const uint16_t*>(row + at));
   };
-  const __amdgpu_buffer_rsrc_t dc = rows_from(p.dc, p.lddc), pre = rows_from(p.pre, p.ldpre);
   float s = 0.f;
   for (int r = 0; r < rows; r += 16) {
     float d[16], x[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const bool live = in && r + e < rows;
-      const uint32_t at_dc = 2 * ((uint32_t)(r + e) * (uint32_t)p.lddc + c);
-      const uint32_t at_pre = 2 * ((uint32_t)(r + e) * (uint32_t)p.ldpre + c);
-      d[e] = epi::from_bf16(__builtin_amdgcn_raw_buffer_load_b16(dc, live ? at_dc : kOut, 0, 0));
-      x[e] = epi::from_bf16(__builtin_amdgcn_raw_buffer_load_b16(pre, live ? at_pre : kOut, 0, 0));
+    for (int e = 0; e < 16; ++e) d[e] = value(p.dc, p.lddc, r + e);
+    if (p.pre) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = value(p.pre, p.ldpre, r + e);
+      act::times_grad<16>(d, x, p.act);
     }
-    if (p.pre) act::times_grad<16>(d, x, p.act);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
+      if (!in || r + e >= rows) d[e] = 0.f;
       s += d[e];
       if (p.dpre && c < p.ldp && r + e < rows) p.dpre[(int64_t)(r0 + r + e) * p.ldp + c] = epi::to_bf16(d[e]);
     }
