@@ -84,6 +84,9 @@ __device__ __forceinline__ float grad_one(float x) {
     return __builtin_fmaf(x * 0.39894228040143268f, e, p);
   }
   if constexpr (A == DG_ACT_GELU_TANH) {
+    // (beyond |x| = 11 s is 0 or 1 in fp32 and so is the slope; |x| <= 16 keeps x du2,
+    // which would overflow from 1e13, finite beside the 0 of s (1 - s); NaN stays)
+    x = fabsf(x) > 16.f ? __builtin_copysignf(16.f, x) : x;
     const float s = sigmoid(tanh_arg2(x));
     const float du2 = 1.59576912160573071f * __builtin_fmaf(0.134145f * x, x, 1.f);
     return __builtin_fmaf(x * du2, s * (1.f - s), s);

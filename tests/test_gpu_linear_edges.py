@@ -1,16 +1,19 @@
-"""The linear layer and its backward pass where values or addresses are large.
+"""The linear layer and its backward pass where values or addresses are large:
+pre-activations up to bf16's largest value, rows any distance apart.
 
 Tolerances as in tests/test_gpu_linear.py, whose bounds hold for every finite
-value of the pre-activation."""
+value of the pre-activation: an activation's slope is 0 or 1 (or between) there
+too."""
 from __future__ import annotations
 
 import pytest
 import torch
 
 from tests.parity import say
-from tests.test_gpu_linear import BF16, F64, slope64, worst
+from tests.test_gpu_linear import ACTS, BF16, F64, act64, slope64, worst
 
 pytestmark = pytest.mark.gpu
+LARGE = [1e2, 1e4, 1e9, 1e12, 1.3e13, 1e16, 1e19, 2e19, 1e25, 1e30, 3e38, 3.38e38]
 
 
 @pytest.fixture(scope="module")
@@ -35,6 +38,40 @@ def check_backward(dg, dc, a, b, pre, act, what):
     ref = d.t() @ a64
     worst(db, ref, q * (d.t().abs() @ a64.abs()) + 2.0 ** -18 * (dc64.t().abs() @ a64.abs()) + r * ref.abs(), what + " db")
     worst(dbias, d.sum(0), 2.0 ** -16 * d.abs().sum(0) + 2.0 ** -18 * dc64.abs().sum(0), what + " dbias")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("n", [40, 41])  # rows on 16-byte boundaries, and not
+def test_backward_of_large_pre_activations(dg, act, n):
+    say(f"linear backward large pre {act} n={n}")
+    m, k = 50, 64
+    g = torch.Generator(device="cuda").manual_seed(21)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    large = torch.tensor([s * v for v in LARGE for s in (1.0, -1.0)], device="cuda")
+    pre = 2 * rn(m, n)
+    pick = torch.rand((m, n), generator=g, device="cuda") < 0.5
+    pre = torch.where(pick, large[torch.randint(0, len(large), (m, n), generator=g, device="cuda")], pre).to(BF16)
+    assert torch.isfinite(pre.float()).all()
+    check_backward(dg, rn(m, n).to(BF16), rn(m, k).to(BF16), (rn(n, k) / 8).to(BF16), pre, act, f"large pre {act} {n}")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m,n", [(5, 48), (5, 49), (80, 48), (80, 49)])
+def test_forward_of_large_pre_activations(dg, act, m, n):
+    """The bias brings the pre-activation up to 3.38e38; the products are of size 1."""
+    say(f"linear forward large pre {act} {m}x{n}")
+    k = 64
+    g = torch.Generator(device="cuda").manual_seed(22)
+    a, b = torch.randn((m, k), generator=g, device="cuda").to(BF16), (torch.randn((n, k), generator=g, device="cuda") / 8).to(BF16)
+    bias = torch.zeros(n, device="cuda")
+    bias[:2 * len(LARGE)] = torch.tensor([s * v for v in LARGE for s in (1.0, -1.0)], device="cuda")
+    out, pre = torch.empty((m, n), device="cuda"), torch.empty((m, n), dtype=BF16, device="cuda")
+    dg.gemm_bf16_nt_epilogue(a, b, out, bias, act, None, pre)
+    z = a.to(F64) @ b.to(F64).t() + bias.to(F64)
+    c = a.to(F64).abs() @ b.to(F64).abs().t() + bias.to(F64).abs()
+    ref = act64(z, act)
+    worst(out, ref, 1.2 * 2.0 ** -16 * c + 2.0 ** -20 * z.abs() + 2.0 ** -22 * ref.abs(), f"{act} {m}x{n}")
+    worst(pre, z, 2.0 ** -16 * c + 2.0 ** -8 * z.abs(), f"{act} {m}x{n} pre")
 
 
 # Rows whose distance passes what 32-bit byte offsets reach: in chunks of 16 rows (few of them) or 64 (64 x 131072),
