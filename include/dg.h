@@ -390,7 +390,8 @@ dg_status dg_gemm_bf16_nt_epilogue_backward_workspace(int m, int n, int64_t* byt
  *       the lowest expert, -inf never chosen; weights e^l / sum (softmax) or
  *       1 / (1 + e^-l) (sigmoid), the sum taken over the chosen experts
  *       (renormalize != 0) or over all (softmax; sigmoid: no division), times
- *       `scale`.  ids [T,k] int32 and weights [T,k] fp32 are written, in order
+ *       `scale`; renormalised sigmoids whose logits are all below -745 (masks)
+ *       have weight 0.  ids [T,k] int32 and weights [T,k] fp32 are written, in order
  *       of falling logits; -1 and 0 where a token has no expert left.  A NaN
  *       logit counts as the largest and makes its token's weights NaN.
  *     logits null: ids and weights are read (scoring, renormalize and scale

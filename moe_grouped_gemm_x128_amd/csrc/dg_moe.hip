@@ -41,6 +41,7 @@ using namespace stream;
 constexpr int kMaxTokens = 64;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxExperts = 512;
+constexpr float kMasked = -745.f;  // below it e^l is 0 in 64 bits as well
 
 struct MoeParams {
   const uint16_t* x;         // bf16 [T,H]
@@ -159,11 +160,17 @@ __device__ __forceinline__ void route_rows(const MoeParams& p, Tables<TMAX>& tb,
       }
     }
     float w = 0.f;
-    if (my_id >= 0)
-      w = p.scoring == DG_SCORING_SOFTMAX ? expf(key_logit(mine) - key_logit(top)) : 1.f / (1.f + expf(-key_logit(mine)));
+    if (my_id >= 0) {
+      const float l = key_logit(mine), most = key_logit(top);
+      // Quotients of sigmoids that may all lie below fp32: from -20 down 1 + e^l is 1
+      // in fp32, so they are quotients of exponentials.  (kMasked and below: a mask's
+      // value, weight 0.)
+      const bool small = p.renormalize && most < -20.f && most >= kMasked;
+      w = small || p.scoring == DG_SCORING_SOFTMAX ? expf(l - most) : 1.f / (1.f + expf(-l));
+    }
     const float sum = row_sum(w);
     if (p.renormalize)
-      w = sum != 0.f ? w / sum : 0.f;  // sum is 0 where no expert is left (or every sigmoid underflows)
+      w = sum != 0.f ? w / sum : 0.f;  // sum is 0 where no expert is left or all are masked
     else if (p.scoring == DG_SCORING_SOFTMAX && my_id >= 0)
       w /= all;
     w *= p.scale;
