@@ -20,7 +20,8 @@
  *     workgroups and add the fp32 partials in a second kernel, in a fixed
  *     order (results are deterministic).  The partials (splits * rows * N * 4
  *     bytes, at most 256 MB) live in a workspace the library keeps per (device,
- *     stream) -- calls on one stream are ordered, so they share it -- taken
+ *     stream) -- calls on one stream are ordered, so they share it, whichever
+ *     host threads they come from -- taken
  *     from a memory pool the library owns per device and grown in the
  *     stream's order (no device synchronisation); it is the one piece of
  *     device memory the library holds beyond the caller's tensors, kept until

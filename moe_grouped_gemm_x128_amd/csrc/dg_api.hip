@@ -11,6 +11,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "../../include/dg.h"
 #include "dg_kernel.h"
@@ -304,7 +305,8 @@ dg_status plan(int kind, int rows, int n, int k, int groups, int num_cus, bool a
 }
 
 // Split-K partials live in a workspace cached per stream: calls on one stream
-// run in order, so they share it.  A stream is identified by its unique id
+// run in order, so they share it (a call enqueues both of its kernels in one
+// turn at the workspace, whichever host thread it comes from).  A stream is identified by its unique id
 // where the HIP runtime in the process provides one (hipStreamGetId, looked up
 // at run time: the runtime that torch loads may predate it), so a stream
 // created after another was destroyed never inherits that one's buffer; with
@@ -325,11 +327,12 @@ constexpr int kMaxCachedStreams = 64;
 struct StreamWorkspace {
   int dev;
   unsigned long long key;  // stream id, or the handle's bits
-  void* ptr;
-  size_t bytes;
+  std::mutex turn;         // held from the buffer's fetch until the kernels that use it are enqueued
+  void* ptr;               // (turn)
+  size_t bytes;            // (turn)
 };
 
-std::mutex g_ws_mutex;
+std::mutex g_ws_mutex;  // the pools, and which streams have an entry (entries stay)
 hipMemPool_t g_pool[kMaxDevices];
 StreamWorkspace g_ws[kMaxCachedStreams];
 int g_ws_count = 0;
@@ -361,40 +364,45 @@ hipMemPool_t device_pool(int dev) {  // caller holds g_ws_mutex
   return g_pool[dev];
 }
 
-// A split-K buffer of at least `bytes` usable in the order of `stream`, or
-// null.  *owned: the buffer is the call's own (return it with hipFreeAsync
-// after the kernels).
-void* stream_workspace(hipStream_t stream, size_t bytes, bool* owned) {
-  *owned = false;
+// A split-K buffer of at least `bytes` usable in the order of `stream`.
+dg::SplitBuffer stream_workspace(hipStream_t stream, size_t bytes) {
+  dg::SplitBuffer b;
   int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return b;
   const unsigned long long key = stream_key(stream);
-  std::lock_guard<std::mutex> lock(g_ws_mutex);
-  hipMemPool_t pool = device_pool(dev);
-  if (!pool) return nullptr;
+  hipMemPool_t pool = nullptr;
   StreamWorkspace* w = nullptr;
-  for (int i = 0; i < g_ws_count; ++i)
-    if (g_ws[i].dev == dev && g_ws[i].key == key) w = &g_ws[i];
-  if (w && w->bytes >= bytes) return w->ptr;
-  if (!w && g_ws_count < kMaxCachedStreams) {
-    w = &g_ws[g_ws_count++];
-    *w = StreamWorkspace{dev, key, nullptr, 0};
+  {
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    pool = device_pool(dev);
+    if (!pool) return b;
+    for (int i = 0; i < g_ws_count; ++i)
+      if (g_ws[i].dev == dev && g_ws[i].key == key) w = &g_ws[i];
+    if (!w && g_ws_count < kMaxCachedStreams) {
+      w = &g_ws[g_ws_count++];
+      w->dev = dev;
+      w->key = key;
+    }
   }
   if (!w) {  // not cached: a buffer for this call only
-    void* p = nullptr;
-    if (hipMallocFromPoolAsync(&p, bytes, pool, stream) != hipSuccess) return nullptr;
-    *owned = true;
-    return p;
+    if (hipMallocFromPoolAsync(&b.ptr, bytes, pool, stream) != hipSuccess) b.ptr = nullptr;
+    b.owned = b.ptr != nullptr;
+    return b;
   }
-  // grow geometrically so a sequence of slightly larger calls allocates rarely
-  size_t want = w->bytes * 2 > bytes ? w->bytes * 2 : bytes;
-  if (want > kMaxWorkspaceBytes) want = bytes;
-  void* p = nullptr;
-  if (hipMallocFromPoolAsync(&p, want, pool, stream) != hipSuccess) return nullptr;
-  if (w->ptr) (void)hipFreeAsync(w->ptr, stream);  // after the calls that used it
-  w->ptr = p;
-  w->bytes = want;
-  return p;
+  std::unique_lock<std::mutex> turn(w->turn);
+  if (w->bytes < bytes) {
+    // grow geometrically so a sequence of slightly larger calls allocates rarely
+    size_t want = w->bytes * 2 > bytes ? w->bytes * 2 : bytes;
+    if (want > kMaxWorkspaceBytes) want = bytes;
+    void* p = nullptr;
+    if (hipMallocFromPoolAsync(&p, want, pool, stream) != hipSuccess) return b;
+    if (w->ptr) (void)hipFreeAsync(w->ptr, stream);  // after the calls that used it
+    w->ptr = p;
+    w->bytes = want;
+  }
+  b.ptr = w->ptr;
+  b.turn = std::move(turn);
+  return b;
 }
 
 bool stream_capturing(hipStream_t stream) {
@@ -432,19 +440,17 @@ dg_status run(int kind, dg::Params& p, int rows, int n, int k, int groups, hipSt
     if (launch_gemm() != hipSuccess) return DG_ERROR_LAUNCH;
     return dg::launch_splitk_reduce(kind, p, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
   }
-  bool owned = false;
-  void* ws = stream_workspace(stream, bytes, &owned);
-  if (!ws) {
+  dg::SplitBuffer ws = stream_workspace(stream, bytes);
+  if (!ws.ptr) {
     // no workspace to be had (out of memory): the same call without a split
     (void)hipGetLastError();
     st = plan(kind, rows, n, k, groups, cus, false, p, l);
     if (st != DG_SUCCESS) return st;
     return launch_gemm() == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
   }
-  p.ws = static_cast<float*>(ws);
+  p.ws = static_cast<float*>(ws.ptr);
   const bool ok = launch_gemm() == hipSuccess && dg::launch_splitk_reduce(kind, p, stream) == hipSuccess;
-  // the call's own buffer goes back to the pool after both kernels, in stream order
-  const bool freed = !owned || hipFreeAsync(ws, stream) == hipSuccess;
+  const bool freed = dg::return_split_buffer(ws, stream);
   return ok && freed ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
@@ -519,8 +525,12 @@ int compute_units() {
 
 bool is_capturing(hipStream_t stream) { return stream_capturing(stream); }
 
-void* split_workspace(hipStream_t stream, size_t bytes, bool* owned) {
-  return stream_workspace(stream, bytes, owned);
+SplitBuffer split_buffer(hipStream_t stream, size_t bytes) { return stream_workspace(stream, bytes); }
+
+bool return_split_buffer(SplitBuffer& b, hipStream_t stream) {
+  const bool ok = !b.owned || hipFreeAsync(b.ptr, stream) == hipSuccess;
+  if (b.turn.owns_lock()) b.turn.unlock();
+  return ok;
 }
 }  // namespace dg
 

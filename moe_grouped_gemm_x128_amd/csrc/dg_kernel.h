@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/dg.h"
 #include "dg_epilogue.h"
 
@@ -122,13 +124,23 @@ dg_status grouped_masked(const void* a, const float* sa, const void* b, const fl
 // What the linear layer's host code (dg_linear.hip) shares with dg_api.hip:
 // the FP8 product with an epilogue for more rows than the streaming kernel
 // takes (arguments validated), the current device's compute units (0: none to
-// be had), whether a stream is being captured, and a split-K buffer in the
-// stream's order (null: none; *owned: to be returned with hipFreeAsync).
+// be had), whether a stream is being captured, and split-K buffers.
 dg_status linear_fp8(const void* a, const float* sa, const void* b, const float* sb, const Epilogue& e, int m, int n,
                      int k, hipStream_t stream);
 int compute_units();
 bool is_capturing(hipStream_t stream);
-void* split_workspace(hipStream_t stream, size_t bytes, bool* owned);
+
+// A split-K buffer in a stream's order.  While `turn` is held no other host
+// thread fetches the stream's buffer: it is kept until the kernels that write
+// and read the partials are both enqueued, so that another thread's call on the
+// stream neither comes between them nor replaces the buffer before them.
+struct SplitBuffer {
+  void* ptr = nullptr;  // null: none to be had
+  bool owned = false;   // the call's own: return_split_buffer gives it back
+  std::unique_lock<std::mutex> turn;
+};
+SplitBuffer split_buffer(hipStream_t stream, size_t bytes);
+bool return_split_buffer(SplitBuffer& b, hipStream_t stream);  // behind the kernels, in stream order
 
 // True if an instance exists for (kind, shape).
 bool has_instance(int kind, const TileShape& shape);

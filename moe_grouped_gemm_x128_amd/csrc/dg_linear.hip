@@ -206,16 +206,15 @@ dg_status gemm(int layout, GemmParams& p, int cus, bool may_split, hipStream_t s
                    p.k, g.bm, g.bn, g.wk, c.splits, grid);
     if (c.splits == 1) return launch_gemm(layout, c.tile, p, grid, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
     p.ws_stride = (int64_t)p.m * p.n;
-    bool owned = false;
-    void* ws = split_workspace(stream, (size_t)(4 * c.splits * p.ws_stride), &owned);
-    if (!ws) {
+    SplitBuffer ws = split_buffer(stream, (size_t)(4 * c.splits * p.ws_stride));
+    if (!ws.ptr) {
       (void)hipGetLastError();
       continue;  // no buffer to be had: the same product without a split
     }
-    p.ws = static_cast<float*>(ws);
+    p.ws = static_cast<float*>(ws.ptr);
     const bool ok = launch_gemm(layout, c.tile, p, grid, stream) == hipSuccess &&
                     launch_splitk_linear(p.epi, p.ws, p.ws_stride, p.splits, p.m, p.n, stream) == hipSuccess;
-    const bool freed = !owned || hipFreeAsync(ws, stream) == hipSuccess;
+    const bool freed = return_split_buffer(ws, stream);
     return ok && freed ? DG_SUCCESS : DG_ERROR_LAUNCH;
   }
   return DG_ERROR_LAUNCH;
