@@ -361,7 +361,7 @@ dg_status dg_gemm_fp8_nt_epilogue(const void* a, const float* sa, const void* b,
  * (dbias sums the unrounded values); sums are fp32.  A and B are read where they
  * lie: no transposed copies.  a [M,K], b [N,K] as in the forward call; the
  * gradients' rows are strided like C, and the rows of dc and pre may lie any
- * distance apart.  workspace: the bytes that
+ * distance apart.  M, N, K <= 2^22.  workspace: the bytes that
  * dg_gemm_bf16_nt_epilogue_backward_workspace returns, 16-byte aligned, the
  * call's until its kernels end. */
 dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const void* a, int64_t lda,

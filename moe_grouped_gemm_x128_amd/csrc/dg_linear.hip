@@ -323,6 +323,15 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
       !aligned(workspace, 16) || (da && (unfit_operand(b, ldb) || !aligned(da, 2))) ||
       (db && (unfit_operand(a, lda) || !aligned(db, 2))) || !aligned(dbias, 4))
     return DG_ERROR_UNSUPPORTED;
+  GemmParams nn{}, tn{};  // da, db
+  if (da) {
+    const dg_status st = make_epilogue(da, ldda, DG_TYPE_BF16, nullptr, k, &nn.epi);
+    if (st != DG_SUCCESS) return st;
+  }
+  if (db) {
+    const dg_status st = make_epilogue(db, lddb, DG_TYPE_BF16, nullptr, k, &tn.epi);
+    if (st != DG_SUCCESS) return st;
+  }
   const int cus = compute_units();
   if (cus <= 0) return DG_ERROR_LAUNCH;
   (void)hipGetLastError();
@@ -350,7 +359,6 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
   }
   const int chunks = ceil_div(m, dact_rows(m, n));  // of the bias partials
   const uint8_t* g = in_place ? static_cast<const uint8_t*>(dc) : reinterpret_cast<const uint8_t*>(dpre);
-  GemmParams nn{}, tn{};
   if (da) {
     nn.a = g;
     nn.lda = 2 * ldp;
@@ -360,8 +368,6 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
     nn.m = m;
     nn.n = k;
     nn.k = n;
-    const dg_status st = make_epilogue(da, ldda, DG_TYPE_BF16, nullptr, k, &nn.epi);
-    if (st != DG_SUCCESS) return st;
   }
   if (db) {
     tn.a = g;
@@ -373,8 +379,6 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
     tn.m = n;
     tn.n = k;
     tn.k = m;
-    const dg_status st = make_epilogue(db, lddb, DG_TYPE_BF16, nullptr, k, &tn.epi);
-    if (st != DG_SUCCESS) return st;
   }
   const bool may_split = !is_capturing(stream);
   if (da && db && nn.epi.vec8 && tn.epi.vec8) {
