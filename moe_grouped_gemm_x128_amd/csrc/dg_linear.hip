@@ -102,6 +102,11 @@ bool forced_out(const GemmTile& g) {  // DG_FORCE_TILE names another tile
   return got >= 4 && !(bm == g.bm && bn == g.bn && wm == g.wm && wn == g.wn && (got == 4 || wk == g.wk));
 }
 
+int forced_splits() {  // DG_FORCE_SPLITS, 0: not set
+  const char* e = std::getenv("DG_FORCE_SPLITS");
+  return e && *e ? std::atoi(e) : 0;
+}
+
 struct Plan {
   int tile, splits, kchunk;
   double us;
@@ -109,8 +114,7 @@ struct Plan {
 
 Plan plan(int m, int n, int k, int cus, bool may_split) {
   const int blocks = ceil_div(k, 64);
-  const char* fsplit = std::getenv("DG_FORCE_SPLITS");
-  const bool force = fsplit && *fsplit && may_split;
+  const int force = may_split ? forced_splits() : 0;
   Plan best{-1, 1, blocks, 1e300};
   for (int t = 0; t < kNumGemmTiles; ++t) {
     const GemmTile g = kGemmTiles[t];
@@ -118,7 +122,7 @@ Plan plan(int m, int n, int k, int cus, bool may_split) {
     const int64_t tiles = (int64_t)ceil_div(m, g.bm) * ceil_div(n, g.bn);
     const int64_t slots = (int64_t)cus * gemm_residents(t);
     for (int s = 1; s <= 16; ++s) {
-      if (force && s != std::atoi(fsplit)) continue;
+      if (force && s != force) continue;
       if (s > 1 && (!may_split || blocks < s)) break;
       const int chunk = ceil_div(blocks, s);
       if (ceil_div(blocks, chunk) != s) continue;  // a split would be empty
@@ -381,7 +385,8 @@ dg_status dg_gemm_bf16_nt_epilogue_backward(const void* dc, int64_t lddc, const 
     tn.k = m;
   }
   const bool may_split = !is_capturing(stream);
-  if (da && db && nn.epi.vec8 && tn.epi.vec8) {
+  // (the pair's products are not split)
+  if (da && db && nn.epi.vec8 && tn.epi.vec8 && !(may_split && forced_splits() > 1)) {
     const PairPlan c = plan_pair(nn, tn, cus);
     const Plan ca = plan(nn.m, nn.n, nn.k, cus, may_split), cb = plan(tn.m, tn.n, tn.k, cus, may_split);
     // Two launches where splitting K gains more than sharing the card does:
