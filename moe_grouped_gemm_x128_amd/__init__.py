@@ -492,10 +492,10 @@ def _ld(t, dev, name):
     if t.get_device() != dev:  # -1 on the host
         raise ValueError("all tensors must be on the same GPU")
     ld, one = t.stride()
-    cols = t.shape[1]
-    if (one != 1 and cols > 1) or (ld < cols and t.shape[0] > 1):
+    rows, cols = t.shape
+    if (one != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{name} must have contiguous, non-overlapping rows")
-    return ld if ld >= cols else cols
+    return ld if rows > 1 else cols  # one row: its stride may be anything (x[:, -1] of one sequence)
 
 
 def _epilogue(out, bias, activation, residual, pre, m, n, dev):

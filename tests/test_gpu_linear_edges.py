@@ -1,5 +1,6 @@
 """The linear layer and its backward pass where values or addresses are large:
-pre-activations up to bf16's largest value, rows any distance apart.
+pre-activations up to bf16's largest value, rows any distance apart, views of
+one row.
 
 Tolerances as in tests/test_gpu_linear.py, whose bounds hold for every finite
 value of the pre-activation: an activation's slope is 0 or 1 (or between) there
@@ -95,3 +96,22 @@ def test_backward_of_rows_far_apart(dg, m, n, ld, both):
     if both:
         pre = apart(pre)
     check_backward(dg, dc, rn(m, k).to(BF16), (rn(n, k) / 4).to(BF16), pre, "silu", f"far apart {m}x{n} {ld}")
+
+
+@pytest.mark.parametrize("steps,step", [(3, 1), (4096, 4095), (2, 0)])
+def test_one_row_of_a_longer_tensor(dg, steps, step):
+    """x[:, -1] of a batch of one sequence: the stride of its one row is the
+    whole sequence, and means nothing."""
+    say(f"linear one row of {steps}")
+    n, k = 264, 520
+    g = torch.Generator(device="cuda").manual_seed(24)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    x, res = rn(1, steps, k).to(BF16)[:, step], rn(1, steps, n + 1).to(BF16)[:, step, :n]
+    w = (rn(n, k) / k ** 0.5).to(BF16)
+    out, pre = (torch.full((1, steps, n + 3), float("nan"), dtype=BF16, device="cuda") for _ in range(2))
+    dg.gemm_bf16_nt_epilogue(x, w, out[:, step, :n], None, "silu", res, pre[:, step, :n])
+    want, wpre = (torch.empty((1, n), dtype=BF16, device="cuda") for _ in range(2))
+    dg.gemm_bf16_nt_epilogue(x.clone(), w, want, None, "silu", res.clone(), wpre)
+    assert torch.equal(out[:, step, :n], want) and torch.equal(pre[:, step, :n], wpre)
+    assert torch.isnan(out[:, step, n:].float()).all()
+    check_backward(dg, res, x, w, pre[:, step, :n], "silu", f"one row of {steps}")
