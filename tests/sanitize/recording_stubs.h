@@ -35,9 +35,35 @@ inline void pause() {
   if (g_pause_us) usleep(g_pause_us);
 }
 
+// What a driver checks of the launches: it defines these.
+void seen_gemm(int layout, int tile, const dg::GemmParams& p, int grid);
+void seen_pair(int tile, const dg::GemmParams& nn, const dg::GemmParams& tn, int first, int grid, int chunks);
+void seen_rows(const dg::RowsParams& p);
+void seen_dact(const dg::DactParams& p);
+void seen_fp8(int kind, const dg::TileShape& s, const dg::Params& p, int grid);
+inline std::vector<int> g_grids;  // of the kernels launched by name (hipLaunchKernel)
+
 }  // namespace rec
 
 extern "C" {
+// (kernel<<<grid, block>>>: push, then the kernel's host function pops and launches)
+static thread_local dim3 rec_grid, rec_block;
+hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t, hipStream_t) {
+  rec_grid = grid;
+  rec_block = block;
+  return hipSuccess;
+}
+hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* shared, hipStream_t* stream) {
+  *grid = rec_grid;
+  *block = rec_block;
+  *shared = 0;
+  *stream = nullptr;
+  return hipSuccess;
+}
+hipError_t hipLaunchKernel(const void*, dim3 grid, dim3, void**, size_t, hipStream_t) {
+  rec::g_grids.push_back((int)(grid.x * grid.y * grid.z));
+  return hipSuccess;
+}
 hipError_t hipGetDevice(int* dev) {
   *dev = 0;
   return hipSuccess;
@@ -73,8 +99,9 @@ hipError_t hipStreamIsCapturing(hipStream_t, hipStreamCaptureStatus* c) {
 
 namespace dg {
 
-hipError_t launch(int, const TileShape&, const Params& p, int, hipStream_t s) {
+hipError_t launch(int kind, const TileShape& shape, const Params& p, int grid, hipStream_t s) {
   rec::pause();
+  rec::seen_fp8(kind, shape, p, grid);
   if (p.splits > 1) rec::note(rec::SPLIT_GEMM, s, p.ws);
   return hipSuccess;
 }
@@ -88,16 +115,25 @@ hipError_t launch_splitk_linear(const Epilogue&, const float* ws, int64_t, int, 
   rec::note(rec::REDUCE, s, ws);
   return hipSuccess;
 }
-hipError_t launch_gemm(int, int, const GemmParams& p, int, hipStream_t s) {
+hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipStream_t s) {
   rec::pause();
+  rec::seen_gemm(layout, tile, p, grid);
   if (p.splits > 1) rec::note(rec::SPLIT_GEMM, s, p.ws);
   return hipSuccess;
 }
-hipError_t launch_gemm_pair(int, const GemmParams&, const GemmParams&, int, int, const float*, float*, int, hipStream_t) {
+hipError_t launch_gemm_pair(int tile, const GemmParams& nn, const GemmParams& tn, int first, int grid, const float*,
+                            float*, int chunks, hipStream_t) {
+  rec::seen_pair(tile, nn, tn, first, grid, chunks);
   return hipSuccess;
 }
-hipError_t launch_linear_rows(bool, const RowsParams&, int, hipStream_t) { return hipSuccess; }
-hipError_t launch_dact(const DactParams&, hipStream_t) { return hipSuccess; }
+hipError_t launch_linear_rows(bool, const RowsParams& p, int, hipStream_t) {
+  rec::seen_rows(p);
+  return hipSuccess;
+}
+hipError_t launch_dact(const DactParams& p, hipStream_t) {
+  rec::seen_dact(p);
+  return hipSuccess;
+}
 hipError_t launch_bias_sum(const float*, float*, int, int, hipStream_t) { return hipSuccess; }
 hipError_t launch_swiglu_quantize(const uint16_t*, uint8_t*, float*, int, int, int, hipStream_t) { return hipSuccess; }
 hipError_t launch_quantize(int, const float*, uint8_t*, float*, int, int, int, hipStream_t) { return hipSuccess; }

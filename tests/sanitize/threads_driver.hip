@@ -11,6 +11,12 @@
 
 #include "recording_stubs.h"
 
+void rec::seen_gemm(int, int, const dg::GemmParams&, int) {}
+void rec::seen_pair(int, const dg::GemmParams&, const dg::GemmParams&, int, int, int) {}
+void rec::seen_rows(const dg::RowsParams&) {}
+void rec::seen_dact(const dg::DactParams&) {}
+void rec::seen_fp8(int, const dg::TileShape&, const dg::Params&, int) {}
+
 namespace {
 
 void* const P = reinterpret_cast<void*>(uintptr_t(0x10000));
