@@ -24,25 +24,16 @@ struct Epilogue {
 
 #if defined(__HIPCC__)
 #include "dg_act.h"
+#include "dg_bf16.h"
 
 namespace dg {
 namespace epi {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ uint16_t to_bf16(float x) {
-  const __bf16 h = (__bf16)x;  // round to nearest even
-  return __builtin_bit_cast(uint16_t, h);
-}
-__device__ __forceinline__ float from_bf16(uint32_t h) { return __uint_as_float(h << 16); }
-__device__ __forceinline__ uint2 pack4(const v4f& v) {
-  return uint2{(uint32_t)to_bf16(v[0]) | ((uint32_t)to_bf16(v[1]) << 16),
-               (uint32_t)to_bf16(v[2]) | ((uint32_t)to_bf16(v[3]) << 16)};
-}
-__device__ __forceinline__ v4f unpack4(const uint2& v) {
-  return v4f{from_bf16(v.x & 0xffffu), __uint_as_float(v.x & 0xffff0000u), from_bf16(v.y & 0xffffu),
-             __uint_as_float(v.y & 0xffff0000u)};
-}
+using bf16::from_bf16;
+using bf16::pack4;
+using bf16::to_bf16;
+using bf16::unpack4;
+using bf16::v4f;
 
 // The bias of columns n .. n + 3 (0 past the last column or without a bias).
 __device__ __forceinline__ v4f bias4(const Epilogue& e, int n, int cols) {

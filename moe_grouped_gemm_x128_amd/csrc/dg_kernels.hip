@@ -196,16 +196,6 @@ __device__ __forceinline__ v4f mfma_block_bf16(const v8i& b_rows, const v8i& a_r
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1, a1, d, 0, 0, 0);
 }
 
-// 8 FP8 codes as bf16 (exact).
-__device__ __forceinline__ v8bf bf16_of_codes(int lo, int hi) {
-  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.f, false);
-  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.f, true);
-  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, false);
-  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, true);
-  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 // EXACT (the linear layer's fp32 outputs): the FP8 matrix instructions keep 16
 // bits or so of a block's sum (1.5e-5 of its size off, measured: far below a
 // bf16 output's rounding, not below an fp32 one's); bf16's are 1e-8 off.
@@ -215,8 +205,8 @@ __device__ __forceinline__ v4f mfma_block(const v8i& b_rows, const v8i& a_rows) 
     v4f d = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int h = 0; h < 8; h += 2)
-      d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16_of_codes(b_rows[h], b_rows[h + 1]),
-                                                  bf16_of_codes(a_rows[h], a_rows[h + 1]), d, 0, 0, 0);
+      d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf16::fp8_to_bf16(b_rows[h], b_rows[h + 1]),
+                                                  bf16::fp8_to_bf16(a_rows[h], a_rows[h + 1]), d, 0, 0, 0);
     return d;
   }
   // D[n][m] = sum over the 128 k of the block; both operands use the same

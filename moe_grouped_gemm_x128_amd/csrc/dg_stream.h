@@ -24,6 +24,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "dg_bf16.h"
 #include "dg_dma.h"
 
 namespace dg {
@@ -31,24 +32,18 @@ namespace stream {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+using bf16::fp8_to_bf16;
+using bf16::from_bf16;
+using bf16::pack4;
+using bf16::to_bf16;
+using bf16::v4f;
+using bf16::v8bf;
 
 constexpr uint32_t kOut = 0x80000000u;  // a lane offset past every resource's range: reads zero, touches no memory
 constexpr int kMaxTiles = 4;
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
-
-// 8 fp8 (e4m3) bytes as 8 bf16 values (exact: every e4m3 value is a bf16 value).
-__device__ __forceinline__ v8bf fp8_to_bf16(int lo, int hi) {
-  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.f, false);
-  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.f, true);
-  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, false);
-  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, true);
-  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
 
 __device__ __forceinline__ v4f mfma_bf16(const v4i& w, const v4i& x, const v4f& acc) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, x), acc, 0, 0,
@@ -72,16 +67,6 @@ __device__ __forceinline__ v4f mfma_fp8(const v4i& w0, const v4i& w1, const v4i&
   const v8i w = v8i{w0[0], w0[1], w0[2], w0[3], w1[0], w1[1], w1[2], w1[3]};
   const v8i x = v8i{x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-}
-
-__device__ __forceinline__ uint16_t to_bf16(float x) {
-  const __bf16 h = (__bf16)x;  // round to nearest even
-  return __builtin_bit_cast(uint16_t, h);
-}
-__device__ __forceinline__ float from_bf16(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
-__device__ __forceinline__ uint2 pack4(const v4f& v) {
-  return uint2{(uint32_t)to_bf16(v[0]) | ((uint32_t)to_bf16(v[1]) << 16),
-               (uint32_t)to_bf16(v[2]) | ((uint32_t)to_bf16(v[3]) << 16)};
 }
 
 // Operand types: bf16 by bf16; fp8 weights with bf16 activations; fp8 by fp8.
