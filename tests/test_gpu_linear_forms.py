@@ -264,3 +264,29 @@ def test_backward_two_launches_by_choice(dg, log):
 def test_backward_in_chunks_of_64_rows(dg, n):
     say(f"backward chunks of 64 rows n={n}")
     backward_case(dg, 2051, n, 64, "gelu_tanh")
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("side", ["a", "b"])
+def test_every_fp8_code(dg, out, side):
+    """Each of the 256 codes by itself times one: its value, and NaN for the two
+    NaN codes, whichever operand holds it, by the few-row kernel and on tiles."""
+    say(f"fp8 every code in {side} {out}")
+    k = 256
+    codes = torch.zeros((256, k), dtype=torch.uint8, device="cuda")
+    i = torch.arange(256, device="cuda")
+    codes[i, (7 * i) % k] = i.to(torch.uint8)
+    codes = codes.view(torch.float8_e4m3fn)
+    value = i.to(torch.uint8).view(torch.float8_e4m3fn).float()
+    assert torch.isnan(value).sum() == 2
+    one = lambda r: torch.ones((r, k), device="cuda").to(torch.float8_e4m3fn)
+    ones = lambda r: torch.ones((r, k // 128), device="cuda")
+    for m in ((16, 64, 256) if side == "a" else (3, 40, 100)):
+        for first in range(0, 256 if side == "a" else 1, m if side == "a" else 256):
+            n = 70 if side == "a" else 256
+            a, b = (codes[first:first + m], one(n)) if side == "a" else (one(m), codes)
+            o = torch.empty((m, n), dtype=out, device="cuda")
+            dg.gemm_fp8_nt_epilogue((a, ones(m)), (b, ones((n + 127) // 128)), o)
+            want = (value[first:first + m, None].expand(m, n) if side == "a" else value[None].expand(m, n)).to(out)
+            nan = torch.isnan(want)
+            assert torch.equal(torch.isnan(o), nan) and torch.equal(o[~nan], want[~nan]), (m, first)
