@@ -343,8 +343,9 @@ dg_status dg_gemm_bf16_nt_epilogue(const void* a, int64_t lda, const void* b, in
 
 /* FP8: operands and scales as dg_gemm_fp8_nt (contiguous rows, K % 128 == 0,
  * K <= 2^22).  An fp32 C is computed from exact products (the codes multiplied
- * as bf16); for a bf16 C the FP8 matrix instructions' sums are 1.5e-5 off, far
- * below its own rounding. */
+ * as bf16).  For a bf16 C the FP8 matrix instructions' sums are 1.5e-5 off in
+ * the norm, some 2e-5 of the products' sizes for one sum: below C's own
+ * rounding unless the products cancel. */
 dg_status dg_gemm_fp8_nt_epilogue(const void* a, const float* sa, const void* b, const float* sb,
                                   void* c, int64_t ldc, int c_type, const dg_epilogue* epi, int m,
                                   int n, int k, hipStream_t stream);

@@ -13,8 +13,9 @@
 //     is applied on the global side: the lane that lands on LDS chunk c of row
 //     r fetches logical chunk c ^ swz(r);
 //   * each 16x16 output subtile of a K block is one v_mfma_f32_16x16x128_f8f6f4
-//     with a zero accumulator: the exact fp32 block partial (DeepGEMM pages,
-//     "主要特点": tensor-core FP8 accumulation alone is imprecise);
+//     with a zero accumulator: the block's partial sum in fp32 (DeepGEMM pages,
+//     "主要特点": tensor-core FP8 accumulation alone is imprecise; within one
+//     block this instruction's sums are 1.5e-5 off, measured);
 //   * the partial is promoted into the fp32 main accumulator with one VALU
 //     FMA by sa[m,kb]*sb[n/128,kb] (the pages' two-level accumulation); the
 //     promotion of one fragment group is placed after the MFMAs of the next,
@@ -197,8 +198,9 @@ __device__ __forceinline__ v4f mfma_block_bf16(const v8i& b_rows, const v8i& a_r
 }
 
 // EXACT (the linear layer's fp32 outputs): the FP8 matrix instructions keep 16
-// bits or so of a block's sum (1.5e-5 of its size off, measured: far below a
-// bf16 output's rounding, not below an fp32 one's); bf16's are 1e-8 off.
+// bits or so of a block's sum (1.5e-5 off in the norm, measured, some 2e-5 of the
+// products' sizes for one sum: below a bf16 output's rounding unless the products
+// cancel, not below an fp32 one's); bf16's are 1e-8 off.
 template <bool EXACT>
 __device__ __forceinline__ v4f mfma_block(const v8i& b_rows, const v8i& a_rows) {
   if constexpr (EXACT) {
@@ -210,7 +212,7 @@ __device__ __forceinline__ v4f mfma_block(const v8i& b_rows, const v8i& a_rows) 
     return d;
   }
   // D[n][m] = sum over the 128 k of the block; both operands use the same
-  // (lane, byte) -> k assignment, so the sum covers exactly the block.
+  // (lane, byte) -> k assignment, so the sum covers the block and nothing else.
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b_rows, a_rows, v4f{0.f, 0.f, 0.f, 0.f},
                                                           0, 0, 0, 0, 0, 0);
 }

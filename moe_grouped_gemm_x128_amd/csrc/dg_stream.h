@@ -50,9 +50,10 @@ __device__ __forceinline__ v4f mfma_bf16(const v4i& w, const v4i& x, const v4f& 
                                                  0);
 }
 // One block of 128 FP8 products.  The FP8 matrix instructions (this one and the
-// 16x16x32 form alike) keep 16 bits or so of a block's sum: 1.5e-5 of its size
-// off, measured, where bf16's on the same values are 1e-8 off.  That is far
-// below a bf16 result's own rounding; where the result is fp32 (EXACT) the codes
+// 16x16x32 form alike) keep 16 bits or so of a block's sum: 1.5e-5 off in the
+// norm, measured, some 2e-5 of the products' sizes for one sum, where bf16's on
+// the same values are 1e-8 off.  That is below a bf16 result's own rounding
+// unless the products cancel; where the result is fp32 (EXACT) the codes
 // are converted, exactly, and multiplied as bf16 (64 x 4096 x 7168: 14.6 us
 // against 13.9).
 template <bool EXACT>
