@@ -245,14 +245,13 @@ def _run_own(s):
         if c["layout"] == "masked":
             first = s["masked_m"]
             dg.moe_sort_masked(s["ids"], c["m_max"], first, s["rows"])
-            m_indices = None
         else:
-            first = m_indices = s["m_indices"]
+            first = s["m_indices"]
             dg.moe_sort_contiguous(s["ids"], c["e"], first, s["rows"])
         if c["out"] == "fp8":
-            dg.moe_dispatch_fp8(s["x"], s["rows"], (s["a"], s["sa"]), m_indices)
+            dg.moe_dispatch_fp8(s["x"], s["rows"], (s["a"], s["sa"]))
             return [first, s["rows"], s["a"], s["sa"]]
-        dg.moe_dispatch_bf16(s["x"], s["rows"], s["a"], m_indices)
+        dg.moe_dispatch_bf16(s["x"], s["rows"], s["a"])
         return [first, s["rows"], s["a"]]
     if op == "combine":
         return dg.moe_combine_bf16(s["o"], s["rows"], s["y"], s["weights"], s["residual"])
