@@ -425,6 +425,149 @@ dg_status dg_moe_few_tokens_bf16(const void* x, const float* logits, int32_t* id
                                  int num_experts, int top_k, int scoring, int renormalize,
                                  float scale, hipStream_t stream);
 
+/* ---- root-mean-square norm with the residual's addition -------------------
+ *     z = x + residual;  r = 1 / sqrt(mean over a row of z^2 + eps);  y = z r w
+ * in fp32, each output rounded once (y comes from the unrounded z).  The step
+ * before a layer's GEMMs, with their operand as its output: bf16, FP8 with 1x128
+ * scales (the rules of dg_quantize_fp8_1x128 and its ue8m0 form, on the fp32 y;
+ * DeepGEMM pages, DeepSeek DeepGEMM 中文讲解, "注意事项": FP8 needs dynamic scale
+ * factors from amax), or INT8 with a scale per row (dg_quantize_int8_rows' rule).
+ * Rows are strided: ld_x, ld_residual, ... are the elements between the starts
+ * of two rows (at least H).  sum may be x or residual, and y may be any of the
+ * three (with the same stride); no other overlap.  A row must keep its sum of
+ * squares finite in fp32: one that does not (or holds a NaN) gets NaN scales. */
+typedef struct {
+  const void* x;        /* [T,H] bf16                                        */
+  int64_t ld_x;
+  const void* residual; /* [T,H] bf16, or null                               */
+  int64_t ld_residual;
+  const void* weight;   /* w: [H] of weight_type, or null (ones)             */
+  int weight_type;      /* dg_type                                           */
+  float eps;            /* finite, >= 0                                      */
+  void* sum;            /* [T,H] bf16: z rounded (the residual stream), or null */
+  int64_t ld_sum;
+  float* rstd;          /* [T] fp32: r, for the backward pass, or null       */
+} dg_norm;
+
+/* H <= 16384 here and below.  y [T,H] bf16: any H, alignment and stride (16-byte aligned rows
+ * and H % 8 == 0 are read 16 bytes at a time). */
+dg_status dg_rmsnorm_bf16(const dg_norm* in, void* y, int64_t ld_y, int tokens, int hidden, hipStream_t stream);
+
+/* q [T,H] fp8 (8-byte aligned), s [T,H/128] fp32, or int32 words of packed UE8M0
+ * [T,ceil(H/512)].  y's few ulp of error and the quotient y RN(1/s) let a code
+ * differ from exact evaluation only where y / s lies within about 2^-20
+ * (relative) of the midpoint between two e4m3 values.  H % 128 == 0; x, residual
+ * and sum 16-byte aligned with strides that are multiples of 8, weight 16-byte
+ * aligned.  A NaN scale is E = 255 in UE8M0. */
+dg_status dg_rmsnorm_quantize_fp8_1x128(const dg_norm* in, void* q, float* s, int tokens, int hidden,
+                                        hipStream_t stream);
+dg_status dg_rmsnorm_quantize_fp8_1x128_ue8m0(const dg_norm* in, void* q, int32_t* s, int tokens, int hidden,
+                                              hipStream_t stream);
+
+/* q [T,H] int8, s [T] fp32: the operand A of dg_gemm_int8_nt_epilogue (which needs
+ * H % 16 == 0; this call takes any H, alignment and stride). */
+dg_status dg_rmsnorm_quantize_int8(const dg_norm* in, void* q, float* s, int tokens, int hidden, hipStream_t stream);
+
+/* Backward pass.  With dy [T,H] bf16, the gradient of y (of the values that were
+ * quantised, where they were), z [T,H] bf16, the stored sum (or x), r [T] the
+ * stored 1/rms, and dsum [T,H] bf16 or null, the gradient that reaches the
+ * residual stream from elsewhere:
+ *     g = w dy;  dx = r (g - z r mean(g z r)) + dsum  [T,H] bf16
+ *     dweight = sum over rows of dy z r  [H] fp32, in a fixed order
+ * dx is the gradient of x and of residual.  Outputs that are null are not
+ * computed.  dx may be dy, z or dsum (same stride).  workspace: the bytes that
+ * dg_rmsnorm_bf16_backward_workspace returns, 16-byte aligned, the call's until
+ * its kernels end (null without dweight). */
+dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* z, int64_t ld_z, const void* weight,
+                                   int weight_type, const float* rstd, const void* dsum, int64_t ld_dsum, void* dx,
+                                   int64_t ld_dx, float* dweight, void* workspace, int tokens, int hidden,
+                                   hipStream_t stream);
+dg_status dg_rmsnorm_bf16_backward_workspace(int tokens, int hidden, int64_t* bytes);
+
+/* ---- tokens sorted by expert and back ---------------------------------------
+ * What stands before and behind the grouped GEMMs (DeepGEMM pages, "分组 GEMM":
+ * the contiguous layout for training and prefill, the masked one for decode): the
+ * row that every (token, expert) pair takes, the tokens copied there, the
+ * experts' outputs summed back with their weights, and the gradients.
+ * Slot (t, j) is token t's j-th expert, ids[t,j]; an id outside [0,E) has no row
+ * (an expert on another device), and an expert named twice by a token has two.
+ * rows [T,k] int32: the row of each slot in the layout, -1 for none.
+ * T, k >= 1, k <= 16, T k <= 2^23, E <= 1024.  Everything is deterministic. */
+
+/* Contiguous layout: expert e's slots take consecutive rows, in slot order, from
+ * a multiple of 128 on, the experts in order.
+ *   m_indices [M_total] int32: the expert of each row, -1 for the others (every
+ *     element is written);
+ *   counts [E] int32 or null: rows of each expert.
+ * M_total % 128 == 0; T k + min(E, T k) 127, rounded down to a multiple of 128,
+ * holds any routing.  Slots whose row lies at or past M_total get none. */
+dg_status dg_moe_sort_contiguous(const int32_t* ids, int32_t* m_indices, int32_t* rows, int32_t* counts,
+                                 void* workspace, int tokens, int top_k, int num_experts, int m_total,
+                                 hipStream_t stream);
+/* Masked layout: expert e's slots take rows e M_max, e M_max + 1, ..., in slot
+ * order; its slots past M_max get none.  masked_m [E] int32: rows of each expert.
+ * E M_max + T k < 2^31. */
+dg_status dg_moe_sort_masked(const int32_t* ids, int32_t* masked_m, int32_t* rows, void* workspace, int tokens,
+                             int top_k, int num_experts, int m_max, hipStream_t stream);
+/* The bytes of workspace of either (4-byte aligned, the call's until its kernels
+ * end): 0 for few slots, then workspace may be null. */
+dg_status dg_moe_sort_workspace(int tokens, int top_k, int num_experts, int64_t* bytes);
+
+/* a[rows[t,j]] = x[t] for every slot with a row in [0,M); a [M,H], contiguous
+ * (the masked layout's [E,M_max,H] has M = E M_max).  rows must not name a row
+ * twice.  With m_indices [M] (contiguous layout; M % 128 == 0) the rows of -1
+ * in the last block of each expert's segment are set to zero, as the weight-
+ * gradient GEMMs need them; null: they stay as they are.  Rows behind the last
+ * segment, and past masked_m, stay as they are.
+ * bf16: x [T,H] with stride ld_x, H % 8 == 0, rows 16-byte aligned.  FP8: x [T,H]
+ * with s [T,H/128] fp32 or packed UE8M0 words [T,ceil(H/512)], H % 128 == 0; sa is
+ * [M,...] of the same.  H <= 2^20, M < 2^31. */
+dg_status dg_moe_dispatch_bf16(const void* x, int64_t ld_x, const int32_t* rows, const int32_t* m_indices, void* a,
+                               int tokens, int top_k, int hidden, int64_t m, hipStream_t stream);
+dg_status dg_moe_dispatch_fp8(const void* x, const float* s, const int32_t* rows, const int32_t* m_indices, void* a,
+                              float* sa, int tokens, int top_k, int hidden, int64_t m, hipStream_t stream);
+dg_status dg_moe_dispatch_fp8_ue8m0(const void* x, const int32_t* s, const int32_t* rows, const int32_t* m_indices,
+                                    void* a, int32_t* sa, int tokens, int top_k, int hidden, int64_t m,
+                                    hipStream_t stream);
+
+/* y[t] = residual[t] + sum over j of weights[t,j] o[rows[t,j]], in fp32 in the
+ * order of j, rounded once; slots without a row in [0,M) add nothing, whatever
+ * their weight.  o [M,H] bf16, contiguous; weights [T,k] fp32 or null (ones);
+ * residual [T,H] bf16 or null (may be y); H % 8 == 0, rows 16-byte aligned.
+ * With weights null it is the backward pass of dg_moe_dispatch_bf16: o the
+ * gradient of a, y that of x. */
+dg_status dg_moe_combine_bf16(const void* o, const int32_t* rows, const float* weights, const void* residual,
+                              int64_t ld_residual, void* y, int64_t ld_y, int tokens, int top_k, int hidden, int64_t m,
+                              hipStream_t stream);
+/* Backward pass, with dy [T,H] bf16 the gradient of y:
+ *     dout[rows[t,j]] = weights[t,j] dy[t]    [M,H] bf16 (may be o)
+ *     dweights[t,j]   = <dy[t], o[rows[t,j]]> [T,k] fp32 (0 for a slot without a row)
+ * (the residual's gradient is dy).  Outputs that are null are not computed, and o
+ * is read for dweights only.  m_indices as in the dispatch, for dout. */
+dg_status dg_moe_combine_bf16_backward(const void* dy, int64_t ld_dy, const void* o, const int32_t* rows,
+                                       const float* weights, const int32_t* m_indices, void* dout, float* dweights,
+                                       int tokens, int top_k, int hidden, int64_t m, hipStream_t stream);
+
+/* ---- INT8 linear layer ------------------------------------------------------
+ *     pre = sa[m] sb[n] sum_k A[m,k] B[n,k] + bias;  C = activation(pre) + residual
+ * with one scale per row of A (token) and of B (channel), the sums exact in
+ * int32, the scales and the epilogue in fp32 and one rounding of C.
+ *   a [M,K] int8 with stride lda, sa [M] fp32; b [N,K] int8 with stride ldb, sb
+ *   [N] fp32; c, epi as dg_gemm_bf16_nt_epilogue.
+ * K % 16 == 0, K < 2^17 (so that no sum leaves int32); a, b 16-byte aligned with
+ * strides that are multiples of 16 up to 2^22.  K is split over workgroups, and
+ * not while capturing, as there; either way the result is the same. */
+dg_status dg_gemm_int8_nt_epilogue(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
+                                   const float* sb, void* c, int64_t ldc, int c_type, const dg_epilogue* epi, int m,
+                                   int n, int k, hipStream_t stream);
+
+/* Its operands: one scale per row of x [M,K] (x_type, stride ld_x), s = amax / 127
+ * (1 for a row of zeros), q = the whole number nearest to x RN(1/s), ties to even.
+ * q [M,K] int8, s [M] fp32.  Any K and alignment.  A row's amax must be 0 or at
+ * least 2^-140; a row with a NaN or an infinity gets a NaN scale. */
+dg_status dg_quantize_int8_rows(const void* x, int64_t ld_x, int x_type, void* q, float* s, int m, int k,
+                                hipStream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* dg_status_string(dg_status s);
 

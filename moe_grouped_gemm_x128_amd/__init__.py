@@ -76,6 +76,35 @@ _lib.dg_moe_few_tokens_fp8.argtypes = [_vp] * 11 + [_i32] * 7 + [_f32c, _vp]
 _lib.dg_moe_few_tokens_fp8.restype = ctypes.c_int
 _lib.dg_moe_few_tokens_bf16.argtypes = [_vp] * 9 + [_i32] * 7 + [_f32c, _vp]
 _lib.dg_moe_few_tokens_bf16.restype = ctypes.c_int
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = [("x", _vp), ("ld_x", _i64), ("residual", _vp), ("ld_residual", _i64), ("weight", _vp),
+                ("weight_type", _i32), ("eps", _f32c), ("sum", _vp), ("ld_sum", _i64), ("rstd", _vp)]
+
+
+_lib.dg_rmsnorm_bf16.argtypes = [_vp, _vp, _i64, _i32, _i32, _vp]
+_lib.dg_rmsnorm_bf16_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i32,
+                                          _i32, _vp]
+_lib.dg_rmsnorm_bf16_backward_workspace.argtypes = [_i32, _i32, ctypes.POINTER(_i64)]
+_lib.dg_moe_sort_contiguous.argtypes = [_vp] * 5 + [_i32] * 4 + [_vp]
+_lib.dg_moe_sort_masked.argtypes = [_vp] * 4 + [_i32] * 4 + [_vp]
+_lib.dg_moe_sort_workspace.argtypes = [_i32, _i32, _i32, ctypes.POINTER(_i64)]
+_lib.dg_moe_dispatch_bf16.argtypes = [_vp, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _vp]
+_lib.dg_moe_combine_bf16.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _i64, _vp]
+_lib.dg_moe_combine_bf16_backward.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _vp]
+_lib.dg_gemm_int8_nt_epilogue.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _i32, _i32, _i32, _vp]
+_lib.dg_quantize_int8_rows.argtypes = [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _vp]
+for _f in ("dg_rmsnorm_quantize_fp8_1x128", "dg_rmsnorm_quantize_fp8_1x128_ue8m0", "dg_rmsnorm_quantize_int8"):
+    getattr(_lib, _f).argtypes = [_vp, _vp, _vp, _i32, _i32, _vp]
+for _f in ("dg_moe_dispatch_fp8", "dg_moe_dispatch_fp8_ue8m0"):
+    getattr(_lib, _f).argtypes = [_vp] * 6 + [_i32] * 3 + [_i64, _vp]
+for _f in ("dg_rmsnorm_bf16", "dg_rmsnorm_quantize_fp8_1x128", "dg_rmsnorm_quantize_fp8_1x128_ue8m0",
+           "dg_rmsnorm_quantize_int8", "dg_rmsnorm_bf16_backward", "dg_rmsnorm_bf16_backward_workspace",
+           "dg_moe_sort_contiguous", "dg_moe_sort_masked", "dg_moe_sort_workspace", "dg_moe_dispatch_bf16",
+           "dg_moe_dispatch_fp8", "dg_moe_dispatch_fp8_ue8m0", "dg_moe_combine_bf16", "dg_moe_combine_bf16_backward",
+           "dg_gemm_int8_nt_epilogue", "dg_quantize_int8_rows"):
+    getattr(_lib, _f).restype = ctypes.c_int
 _lib.dg_status_string.argtypes = [ctypes.c_int]
 _lib.dg_status_string.restype = ctypes.c_char_p
 _lib.dg_version.restype = ctypes.c_int
@@ -690,6 +719,327 @@ def moe_few_tokens_bf16(x, w13, w2, out, ids, weights, logits=None, scoring="sof
                            renormalize, scale, residual, workspace)
 
 
+# ------------------------- norm with the residual's addition, INT8 layer ---
+
+def _norm(x, weight, eps, residual, sum_out, rstd, dev):
+    _bf16(x, "x")
+    t, h = x.shape
+    p = _Norm(_ptr(x), _ld(x, dev, "x"))
+    p.eps = eps
+    if weight is not None:
+        p.weight, p.weight_type = _weight(weight, h, dev)
+    if residual is not None:
+        _bf16(residual, "residual"); _shape(residual, (t, h), "residual")
+        p.residual, p.ld_residual = _ptr(residual), _ld(residual, dev, "residual")
+    if sum_out is not None:
+        _bf16(sum_out, "sum_out"); _shape(sum_out, (t, h), "sum_out")
+        p.sum, p.ld_sum = _ptr(sum_out), _ld(sum_out, dev, "sum_out")
+    if rstd is not None:
+        p.rstd = _vector(rstd, (t,), dev, "rstd")
+    return p, t, h
+
+
+def _weight(weight, h, dev):
+    kind = _TYPE.get(weight.dtype)
+    if kind is None:
+        raise TypeError(f"weight must be bfloat16 or float32, got {weight.dtype}")
+    if weight.shape != (h,) or weight.get_device() != dev or not weight.is_contiguous():
+        raise ValueError(f"weight must be contiguous with shape {(h,)}, on the same GPU, got {tuple(weight.shape)}")
+    return _ptr(weight), kind
+
+
+def _vector(t, shape, dev, name):
+    """Pointer of a contiguous fp32 tensor of the given shape on GPU `dev`."""
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {shape}, on the same GPU, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _plain(t, shape, dev, name):
+    """Pointer of a contiguous tensor of the given shape on GPU `dev`."""
+    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, on the same GPU, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _int32(t, shape, dev, name):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    return _plain(t, shape, dev, name)
+
+
+def _room(workspace, need, dev, like):
+    """Pointer of a workspace of at least `need` bytes, made if there is none."""
+    if not need:
+        return None
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must be contiguous, on the same GPU, with at least {need} bytes")
+    return workspace.data_ptr()
+
+
+def rmsnorm_bf16(x, weight, out, eps=1e-6, residual=None, sum_out=None, rstd=None):
+    """out bf16 [T,H] = z / sqrt(mean(z^2) + eps) * weight with z = x + residual
+    (see dg_rmsnorm_bf16 in include/dg.h).  weight [H] bf16, fp32 or None;
+    sum_out bf16 [T,H] receives z (may be x or residual), rstd fp32 [T] the
+    factor for the backward pass.  Rows may be strided."""
+    dev = _gpu(x)
+    p, t, h = _norm(x, weight, eps, residual, sum_out, rstd, dev)
+    _bf16(out, "out"); _shape(out, (t, h), "out")
+    _check(_lib.dg_rmsnorm_bf16(ctypes.addressof(p), _ptr(out), _ld(out, dev, "out"), t, h, _stream(x)),
+           "dg_rmsnorm_bf16")
+    return out
+
+
+def rmsnorm_quantize_fp8_1x128(x, weight, q, s, eps=1e-6, residual=None, sum_out=None, rstd=None):
+    """rmsnorm_bf16 with its fp32 result quantised: q fp8 [T,H], s fp32
+    [T,H/128], or int32 [T,ceil(H/512)] for packed UE8M0 scales."""
+    dev = _gpu(x)
+    p, t, h = _norm(x, weight, eps, residual, sum_out, rstd, dev)
+    _fp8(q, "q")
+    qp = _plain(q, (t, h), dev, "q")
+    if s.dtype == torch.int32:
+        _check(_lib.dg_rmsnorm_quantize_fp8_1x128_ue8m0(ctypes.addressof(p), qp, _plain(s, (t, (h + 511) // 512), dev, "s"),
+                                                        t, h, _stream(x)), "dg_rmsnorm_quantize_fp8_1x128_ue8m0")
+    else:
+        _check(_lib.dg_rmsnorm_quantize_fp8_1x128(ctypes.addressof(p), qp, _vector(s, (t, h // 128), dev, "s"), t, h,
+                                                  _stream(x)), "dg_rmsnorm_quantize_fp8_1x128")
+    return q, s
+
+
+def rmsnorm_quantize_int8(x, weight, q, s, eps=1e-6, residual=None, sum_out=None, rstd=None):
+    """rmsnorm_bf16 with its fp32 result quantised: q int8 [T,H], s fp32 [T]."""
+    dev = _gpu(x)
+    p, t, h = _norm(x, weight, eps, residual, sum_out, rstd, dev)
+    _int8(q, "q")
+    _check(_lib.dg_rmsnorm_quantize_int8(ctypes.addressof(p), _plain(q, (t, h), dev, "q"), _vector(s, (t,), dev, "s"), t,
+                                         h, _stream(x)), "dg_rmsnorm_quantize_int8")
+    return q, s
+
+
+def rmsnorm_bf16_backward_workspace(t, h):
+    """Bytes of workspace that rmsnorm_bf16_backward needs for dweight."""
+    need = _i64()
+    _check(_lib.dg_rmsnorm_bf16_backward_workspace(t, h, ctypes.byref(need)), "dg_rmsnorm_bf16_backward_workspace")
+    return need.value
+
+
+def rmsnorm_bf16_backward(dout, z, weight, rstd, dx=None, dweight=None, dsum=None, workspace=None):
+    """Gradients of the norm from dout bf16 [T,H], the stored sum z bf16 [T,H]
+    (or x) and rstd fp32 [T] (see include/dg.h): writes those of dx bf16 [T,H]
+    (the gradient of x and of residual; dsum bf16 [T,H], the gradient that
+    reaches sum_out from elsewhere, is added) and dweight fp32 [H] that are
+    given and returns both."""
+    _bf16(dout, "dout"); _bf16(z, "z")
+    t, h = dout.shape
+    _shape(z, (t, h), "z")
+    dev = _gpu(dout)
+    wp, wt = (None, 0) if weight is None else _weight(weight, h, dev)
+    dsp = dxp = dwp = wsp = None
+    ldds = lddx = 0
+    if dx is not None:
+        _bf16(dx, "dx"); _shape(dx, (t, h), "dx")
+        dxp, lddx = _ptr(dx), _ld(dx, dev, "dx")
+        if dsum is not None:
+            _bf16(dsum, "dsum"); _shape(dsum, (t, h), "dsum")
+            dsp, ldds = _ptr(dsum), _ld(dsum, dev, "dsum")
+    if dweight is not None:
+        dwp = _vector(dweight, (h,), dev, "dweight")
+        wsp = _room(workspace, rmsnorm_bf16_backward_workspace(t, h), dev, dout)
+    _check(_lib.dg_rmsnorm_bf16_backward(_ptr(dout), _ld(dout, dev, "dout"), _ptr(z), _ld(z, dev, "z"), wp, wt,
+                                         _vector(rstd, (t,), dev, "rstd"), dsp, ldds, dxp, lddx, dwp, wsp, t, h,
+                                         _stream(dout)), "dg_rmsnorm_bf16_backward")
+    return dx, dweight
+
+
+def _int8(t, name):
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be int8, got {t.dtype}")
+
+
+def gemm_int8_nt_epilogue(lhs, rhs, out, bias=None, activation="none", residual=None, pre=None):
+    """gemm_bf16_nt_epilogue on INT8 operands with a scale per row: lhs = (int8
+    [M,K], fp32 [M]), rhs = (int8 [N,K], fp32 [N]) (see
+    dg_gemm_int8_nt_epilogue in include/dg.h)."""
+    (a, sa), (b, sb) = lhs, rhs
+    _int8(a, "a"); _int8(b, "b")
+    m, k = a.shape
+    n = b.shape[0]
+    _shape(b, (n, k), "b")
+    dev = _gpu(a)
+    ldc = _linear_out(out, m, n, dev)
+    e = _epilogue(out, bias, activation, residual, pre, m, n, dev)
+    _check(_lib.dg_gemm_int8_nt_epilogue(_ptr(a), _ld(a, dev, "a"), _vector(sa, (m,), dev, "sa"), _ptr(b),
+                                         _ld(b, dev, "b"), _vector(sb, (n,), dev, "sb"), _ptr(out), ldc,
+                                         _TYPE[out.dtype], ctypes.addressof(e), m, n, k, _stream(a)),
+           "dg_gemm_int8_nt_epilogue")
+    return out
+
+
+def dg_quantize_int8_rows(x, q, s):
+    """x bf16 or fp32 [M,K] -> q int8 [M,K], s fp32 [M]: a scale per row (see
+    include/dg.h).  x's rows may be strided."""
+    kind = _TYPE.get(x.dtype)
+    if kind is None:
+        raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
+    _int8(q, "q")
+    m, k = x.shape
+    dev = _gpu(x)
+    _check(_lib.dg_quantize_int8_rows(_ptr(x), _ld(x, dev, "x"), kind, _plain(q, (m, k), dev, "q"),
+                                      _vector(s, (m,), dev, "s"), m, k, _stream(x)), "dg_quantize_int8_rows")
+    return q, s
+
+
+# ------------------------------------- tokens sorted by expert and back ---
+
+def moe_sort_workspace(tokens, top_k, num_experts):
+    """Bytes of workspace that moe_sort_contiguous and moe_sort_masked need."""
+    need = _i64()
+    _check(_lib.dg_moe_sort_workspace(tokens, top_k, num_experts, ctypes.byref(need)), "dg_moe_sort_workspace")
+    return need.value
+
+
+def moe_sort_rows(tokens, top_k, num_experts):
+    """Rows of the contiguous layout that hold any routing (M_total)."""
+    slots = tokens * top_k
+    return max(128, (slots + min(num_experts, slots) * 127) // 128 * 128)
+
+
+def moe_sort_contiguous(ids, num_experts, m_indices, rows, counts=None, workspace=None):
+    """Rows of the contiguous layout for the tokens' experts ids int32 [T,k] (see
+    dg_moe_sort_contiguous in include/dg.h): writes m_indices int32 [M_total]
+    (moe_sort_rows gives an M_total for any routing), rows int32 [T,k] and, if
+    given, counts int32 [E]; returns m_indices and rows."""
+    t, k = ids.shape
+    dev = _gpu(ids)
+    m = m_indices.shape[0]
+    cp = None if counts is None else _int32(counts, (num_experts,), dev, "counts")
+    _check(_lib.dg_moe_sort_contiguous(
+        _int32(ids, (t, k), dev, "ids"), _int32(m_indices, (m,), dev, "m_indices"), _int32(rows, (t, k), dev, "rows"), cp,
+        _room(workspace, moe_sort_workspace(t, k, num_experts), dev, ids), t, k, num_experts, m, _stream(ids)),
+        "dg_moe_sort_contiguous")
+    return m_indices, rows
+
+
+def moe_sort_masked(ids, m_max, masked_m, rows, workspace=None):
+    """Rows of the masked layout [E,M_max,..] for the tokens' experts ids int32
+    [T,k]: writes masked_m int32 [E] and rows int32 [T,k] and returns both."""
+    t, k = ids.shape
+    dev = _gpu(ids)
+    e = masked_m.shape[0]
+    _check(_lib.dg_moe_sort_masked(
+        _int32(ids, (t, k), dev, "ids"), _int32(masked_m, (e,), dev, "masked_m"), _int32(rows, (t, k), dev, "rows"),
+        _room(workspace, moe_sort_workspace(t, k, e), dev, ids), t, k, e, m_max, _stream(ids)), "dg_moe_sort_masked")
+    return masked_m, rows
+
+
+def _layout(a, h, dev, name):
+    """(M, pointer) of a grouped layout's rows [M,H] or [E,M_max,H]."""
+    shape = a.shape
+    if len(shape) not in (2, 3) or shape[-1] != h or a.get_device() != dev or not a.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [M,{h}] or [E,M_max,{h}], on the same GPU, got {tuple(shape)}")
+    return (shape[0] if len(shape) == 2 else shape[0] * shape[1]), a.data_ptr()
+
+
+def _slots(rows, dev):
+    if rows.dim() != 2:
+        raise ValueError(f"rows must be [T,k], got {tuple(rows.shape)}")
+    return rows.shape[1], _int32(rows, rows.shape, dev, "rows")
+
+
+def moe_dispatch_bf16(x, rows, a, m_indices=None):
+    """a[rows[t,j]] = x[t] for bf16 x [T,H] (see dg_moe_dispatch_bf16 in
+    include/dg.h); a bf16 [M,H] or [E,M_max,H].  With m_indices (contiguous
+    layout) the padding rows of the segments become zeros."""
+    _bf16(x, "x"); _bf16(a, "a")
+    t, h = x.shape
+    dev = _gpu(x)
+    m, ap = _layout(a, h, dev, "a")
+    k, rp = _slots(rows, dev)
+    _shape(rows, (t, k), "rows")
+    mi = None if m_indices is None else _int32(m_indices, (m,), dev, "m_indices")
+    _check(_lib.dg_moe_dispatch_bf16(_ptr(x), _ld(x, dev, "x"), rp, mi, ap, t, k, h, m, _stream(x)),
+           "dg_moe_dispatch_bf16")
+    return a
+
+
+def moe_dispatch_fp8(x, rows, a, m_indices=None):
+    """moe_dispatch_bf16 for FP8 rows with their scales: x = (fp8 [T,H], fp32
+    [T,H/128] or int32 [T,ceil(H/512)]), a = (fp8 [M,H] or [E,M_max,H], scales
+    of the same)."""
+    (q, s), (qa, sa) = x, a
+    _fp8(q, "x"); _fp8(qa, "a")
+    t, h = q.shape
+    dev = _gpu(q)
+    packed = s.dtype == torch.int32
+    if (not packed and s.dtype != torch.float32) or sa.dtype != s.dtype:
+        raise TypeError(f"scales must be float32, or int32 (packed UE8M0), in x and a: got {s.dtype} and {sa.dtype}")
+    words = (h + 511) // 512 if packed else h // 128
+    m, ap = _layout(qa, h, dev, "a")
+    m2, sap = _layout(sa, words, dev, "a's scales")
+    if m2 != m:
+        raise ValueError(f"a has {m} rows and its scales {m2}")
+    k, rp = _slots(rows, dev)
+    _shape(rows, (t, k), "rows")
+    mi = None if m_indices is None else _int32(m_indices, (m,), dev, "m_indices")
+    fn = _lib.dg_moe_dispatch_fp8_ue8m0 if packed else _lib.dg_moe_dispatch_fp8
+    _check(fn(_plain(q, (t, h), dev, "x"), _plain(s, (t, words), dev, "x's scales"), rp, mi, ap, sap, t, k, h, m,
+              _stream(q)), "dg_moe_dispatch_fp8")
+    return a
+
+
+def moe_combine_bf16(o, rows, out, weights=None, residual=None):
+    """out[t] = residual[t] + sum_j weights[t,j] o[rows[t,j]] (see
+    dg_moe_combine_bf16 in include/dg.h): o bf16 [M,H] or [E,M_max,H], weights
+    fp32 [T,k] or None (ones), residual bf16 [T,H] (may be out)."""
+    _bf16(o, "o"); _bf16(out, "out")
+    t, h = out.shape
+    dev = _gpu(o)
+    m, op = _layout(o, h, dev, "o")
+    k, rp = _slots(rows, dev)
+    _shape(rows, (t, k), "rows")
+    wp = None if weights is None else _vector(weights, (t, k), dev, "weights")
+    res, ldr = None, 0
+    if residual is not None:
+        _bf16(residual, "residual"); _shape(residual, (t, h), "residual")
+        res, ldr = _ptr(residual), _ld(residual, dev, "residual")
+    _check(_lib.dg_moe_combine_bf16(op, rp, wp, res, ldr, _ptr(out), _ld(out, dev, "out"), t, k, h, m, _stream(o)),
+           "dg_moe_combine_bf16")
+    return out
+
+
+def moe_dispatch_bf16_backward(da, rows, dx):
+    """dx[t] = sum_j da[rows[t,j]]: moe_dispatch_bf16's gradient."""
+    return moe_combine_bf16(da, rows, dx)
+
+
+def moe_combine_bf16_backward(dout, o, rows, weights=None, do=None, dweights=None, m_indices=None):
+    """Gradients of moe_combine_bf16 from dout bf16 [T,H] (see include/dg.h):
+    writes those of do bf16, of o's shape (may be o), and dweights fp32 [T,k]
+    that are given and returns both.  With m_indices (contiguous layout) the
+    padding rows of do become zeros."""
+    _bf16(dout, "dout"); _bf16(o, "o")
+    t, h = dout.shape
+    dev = _gpu(dout)
+    m, op = _layout(o, h, dev, "o")
+    k, rp = _slots(rows, dev)
+    _shape(rows, (t, k), "rows")
+    wp = None if weights is None else _vector(weights, (t, k), dev, "weights")
+    dp = None
+    if do is not None:
+        _bf16(do, "do"); _shape(do, o.shape, "do")
+        dp = _layout(do, h, dev, "do")[1]
+    dwp = None if dweights is None else _vector(dweights, (t, k), dev, "dweights")
+    mi = None if m_indices is None else _int32(m_indices, (m,), dev, "m_indices")
+    _check(_lib.dg_moe_combine_bf16_backward(_ptr(dout), _ld(dout, dev, "dout"), op, rp, wp, mi, dp, dwp, t, k, h, m,
+                                             _stream(dout)), "dg_moe_combine_bf16_backward")
+    return do, dweights
+
+
 # ------------------------------------------------------ page-style names ---
 
 def gemm_fp8_fp8_bf16_nt(lhs, rhs, out):
@@ -783,6 +1133,12 @@ def quantize_fp8_1x128_transposed(x):
     t, f = x.shape
     return dg_quantize_fp8_1x128_transposed(x, torch.empty((f, t), dtype=FP8, device=x.device),
                                             torch.empty((f, t // 128), dtype=torch.float32, device=x.device))
+
+
+def quantize_int8_rows(x):
+    """Operand of gemm_int8_nt_epilogue from x bf16 or fp32 [M,K]: (int8 [M,K], fp32 scales [M])."""
+    return dg_quantize_int8_rows(x, torch.empty(x.shape, dtype=torch.int8, device=x.device),
+                                 torch.empty(x.shape[0], dtype=torch.float32, device=x.device))
 
 
 def swiglu_quantize_fp8_1x128(c):

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg_mi355x.so")
 SOURCES = ["dg_api.hip", "dg_shapes.hip", "dg_kernels.hip", "dg_quant.hip", "dg_noalloc.hip", "dg_moe.hip",
-           "dg_linear.hip", "dg_linear_rows.hip", "dg_linear_gemm.hip"]
+           "dg_linear.hip", "dg_linear_rows.hip", "dg_linear_gemm.hip", "dg_linear_int8.hip", "dg_linear_int8_gemm.hip",
+           "dg_norm.hip", "dg_moe_rows.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

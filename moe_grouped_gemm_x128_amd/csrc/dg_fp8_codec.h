@@ -23,6 +23,22 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return (uint32_t)w;
 }
 
+// Power-of-two (UE8M0) scales (DeepGEMM pages, aikraft.ru support table:
+// packed UE8M0, four values in one torch.int): a group's scale is the
+// smallest 2^(E - 127), E in [0, 254], not below s0 = scale_of(amax), read off
+// s0's fp32 fields -- an exact power keeps its exponent field, anything above
+// it takes the next; a subnormal s0 is at most 2^-127 (E = 0, the field 0
+// with mantissa 2^22) or below 2^-126 (E = 1).
+__device__ __forceinline__ uint32_t ue8m0_code(float amax) {
+  const uint32_t b = __float_as_uint(scale_of(amax));
+  const uint32_t ex = b >> 23, man = b & 0x7fffffu;
+  if (ex == 0) return man > 0x400000u ? 1u : 0u;
+  return min(ex + (man != 0u ? 1u : 0u), 254u);
+}
+__device__ __forceinline__ float ue8m0_value(uint32_t e) {
+  return __uint_as_float(e == 0 ? 0x400000u : e << 23);
+}
+
 // silu(g) = g / (1 + e^-g) for a bf16 gate g.  e^-g = 2^(-g log2 e) with
 // log2 e split into a 15-bit head, whose product with g (8 significant bits)
 // is exact in fp32, and a tail t = log2 e - head applied as the factor

@@ -24,6 +24,8 @@ struct RowsParams {
 // Columns of C per workgroup: 16 where 32 would occupy at most half of the CUs
 constexpr int few_rows_columns(int n, int num_cus) { return n <= 16 * num_cus ? 16 : 32; }
 hipError_t launch_linear_rows(bool fp8, const RowsParams& p, int num_cus, hipStream_t stream);
+// INT8: k counts pairs of values (the bytes of as many bf16 ones), sa [M], sb [N]
+hipError_t launch_linear_rows_int8(const RowsParams& p, int num_cus, hipStream_t stream);
 
 // Tiles, BF16: C[m, n] = sum_k A(m, k) B(n, k).  An operand is stored with K
 // contiguous ([rows, K]) or, "transposed", with K as the row index ([K, rows]).
@@ -52,6 +54,16 @@ constexpr int kNumGemmTiles = 8, kNumPairTiles = 5;  // the first kNumPairTiles 
 // workgroups of a tile that share a CU (LDS)
 constexpr int gemm_residents(int tile) { return tile >= 2 && tile <= 4 ? 2 : 1; }
 hipError_t launch_gemm(int layout, int tile, const GemmParams& p, int grid, hipStream_t stream);
+
+// INT8, both operands with K contiguous (launch_gemm's kNT): p.k counts pairs of values, p.ws holds int32 partials,
+// and launch_splitk_int8 turns those into C.
+hipError_t launch_gemm_int8(int tile, const GemmParams& p, const float* sa, const float* sb, int grid,
+                            hipStream_t stream);
+hipError_t launch_splitk_int8(const GemmParams& p, const float* sa, const float* sb, hipStream_t stream);
+
+// Rows of x [m, k] as INT8 with a scale each.
+hipError_t launch_quantize_int8(const void* x, bool f32, int64_t ldx, int8_t* q, float* s, int m, int k,
+                                hipStream_t stream);
 
 // An NN and a TN product (neither split, both with Epilogue::vec8) in one launch: `first` workgroups (a multiple of 8) on
 // the first, the rest on the second; and the bias sum of launch_bias_sum (dbias

@@ -7,6 +7,8 @@
 // the CUs idle it owns 16 (the groups are two lines of K of the same rows): more
 // CUs load, though each loads A once more.  No second kernel and no
 // workspace: the split over K is inside the workgroup.
+#include <type_traits>
+
 #include "dg_linear.h"
 #include "dg_stream.h"
 
@@ -57,9 +59,10 @@ template <int MODE, int NT, bool SAME, bool EXACT, int W, int D>
 __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[ring_bytes(MODE, W, D)];
   // the waves' sums meet where the ring was
+  using Acc = std::conditional_t<MODE == kInt8, v4i, v4f>;
   constexpr int G = SAME ? 1 : 2;  // groups of 16 columns
   static_assert(ring_bytes(MODE, W, D) >= W * G * NT * 1024, "the sums fit the ring");
-  v4f(*red)[G * NT][64] = reinterpret_cast<v4f(*)[G * NT][64]>(ring);
+  Acc(*red)[G * NT][64] = reinterpret_cast<Acc(*)[G * NT][64]>(ring);
   const int tid = threadIdx.x, lane = tid & 63, wave = (int)uniform(tid >> 6);
   const int l16 = lane & 15, lq = lane >> 4;
   const int n0 = blockIdx.x * 16 * G;
@@ -88,11 +91,18 @@ __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p)
   const bool mine_out = wave < G * NT && em < p.m && en < p.n;
   v4f bias = v4f{0.f, 0.f, 0.f, 0.f};
   if (mine_out) bias = epi::bias4(p.epi, en, p.n);
+  float row_scale = 1.f;  // INT8
+  v4f col_scale = v4f{1.f, 1.f, 1.f, 1.f};
+  if (MODE == kInt8 && mine_out) {
+    row_scale = p.sa[em];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) col_scale[r] = p.sb[min(en + r, p.n - 1)];
+  }
   Pipe<MODE, D, true, SAME, RowsCursor, EXACT> pipe;
   pipe.init(dma::lds_addr(ring) + wave * D * entry_bytes(MODE), c, lane);
-  v4f a[NT], b[NT];
+  Acc a[NT], b[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) a[t] = b[t] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < NT; ++t) a[t] = b[t] = Acc{0, 0, 0, 0};
   for (int k = 0; k < mine; ++k) pipe.template unit<NT>(NT, a, b);
   dma::wait<0>();   // no load lands in the ring any more
   dma::barrier();   // on any wave
@@ -108,9 +118,16 @@ __global__ __launch_bounds__(W * 64) void linear_rows_kernel(const RowsParams p)
   __syncthreads();
   static_assert(G * NT <= W, "one group of sums per wave");
   if (mine_out) {
-    v4f v = red[0][wave][lane];
+    Acc sum = red[0][wave][lane];
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += red[w][wave][lane];
+    for (int w = 1; w < W; ++w) sum += red[w][wave][lane];
+    v4f v;
+    if constexpr (MODE == kInt8) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = (float)sum[r] * col_scale[r] * row_scale;
+    } else {
+      v = sum;
+    }
     epi::finish4(p.epi, em, en, p.n, v + bias);
   }
 }
@@ -144,6 +161,10 @@ hipError_t launch_mode(const RowsParams& p, int cus, hipStream_t stream) {
 hipError_t launch_linear_rows(bool fp8, const RowsParams& p, int num_cus, hipStream_t stream) {
   if (!fp8) return launch_mode<kBf16, false>(p, num_cus, stream);
   return p.epi.out_f32 ? launch_mode<kFp8, true>(p, num_cus, stream) : launch_mode<kFp8, false>(p, num_cus, stream);
+}
+
+hipError_t launch_linear_rows_int8(const RowsParams& p, int num_cus, hipStream_t stream) {
+  return launch_mode<kInt8, false>(p, num_cus, stream);
 }
 
 }  // namespace dg

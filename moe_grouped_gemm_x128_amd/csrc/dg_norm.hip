@@ -1,0 +1,583 @@
+// dg_norm.hip -- root-mean-square norm of rows with the residual's addition
+// (include/dg.h): output in bf16, FP8 with 1x128 scales or INT8 with a scale per
+// row; and its backward pass.
+//
+//     z = x + residual,  r = 1 / sqrt(mean(z^2) + eps),  y = z r w
+//
+// A workgroup of W waves owns a row and keeps it in registers: a thread holds V
+// consecutive columns (8, or 1 where rows do not start on 16-byte boundaries)
+// of each of I pieces of the row, so x and the residual are read once and z, y
+// are written once, and one barrier separates them.  INT8's scale needs the
+// row's largest |y| too: max |z w| is met at the same barrier as sum z^2 and
+// multiplied by r after it.
+#include <initializer_list>
+
+#include "dg_bf16.h"
+#include "dg_fp8_codec.h"
+#include "dg_kernel.h"
+
+namespace dg {
+namespace {
+
+using bf16::from_bf16;
+using bf16::to_bf16;
+
+enum Out : int { kBf16 = 0, kFp8 = 1, kFp8Ue8m0 = 2, kInt8 = 3 };
+
+constexpr int kMaxHidden = 16384;  // what 8 waves hold in registers
+constexpr int64_t kMaxLd = (int64_t)1 << 40;
+
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* res;  // or null
+  const void* w;        // or null
+  uint16_t* sum;        // or null
+  float* rstd;          // or null
+  void* y;              // bf16, FP8 or INT8
+  void* s;              // scales
+  int64_t ldx, ldr, lds, ldy;
+  int t, h, w_f32;
+  float eps;
+};
+
+// ---- a thread's V consecutive values ----
+template <int V>
+struct Raw;
+template <>
+struct Raw<8> {
+  uint4 v;
+};
+template <>
+struct Raw<1> {
+  uint16_t v;
+};
+
+template <int V>
+__device__ __forceinline__ Raw<V> load(const uint16_t* p) {
+  if constexpr (V == 8)
+    return Raw<8>{*reinterpret_cast<const uint4*>(p)};
+  else
+    return Raw<1>{*p};
+}
+template <int V>
+__device__ __forceinline__ void widen(const Raw<V>& r, float* f) {
+  if constexpr (V == 8) {
+    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = from_bf16(w[e]);
+      f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  } else {
+    f[0] = from_bf16(r.v);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store(uint16_t* p, const float* f) {
+  if constexpr (V == 8) {
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = (uint32_t)to_bf16(f[2 * e]) | ((uint32_t)to_bf16(f[2 * e + 1]) << 16);
+    *reinterpret_cast<uint4*>(p) = uint4{o[0], o[1], o[2], o[3]};
+  } else {
+    *p = to_bf16(f[0]);
+  }
+}
+// The weight's values of columns c .. c + V - 1.
+template <int V>
+__device__ __forceinline__ void load_weight(const void* w, int f32, int c, float* f) {
+  if (!w) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = 1.f;
+  } else if (f32) {
+    const float* p = static_cast<const float*>(w) + c;
+    if constexpr (V == 8) {
+      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+      f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+      f[0] = *p;
+    }
+  } else {
+    widen<V>(load<V>(static_cast<const uint16_t*>(w) + c), f);
+  }
+}
+
+// ---- reductions ----
+// v combined with the value `n` lanes round in the lane's row of 16.
+template <int N>
+__device__ __forceinline__ float round16(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float max16(float v) {  // over a row of 16 lanes, in all of them
+  v = fmaxf(v, round16<8>(v));
+  v = fmaxf(v, round16<4>(v));
+  v = fmaxf(v, round16<2>(v));
+  return fmaxf(v, round16<1>(v));
+}
+__device__ __forceinline__ float max64(float v) {
+  v = max16(v);
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float sum64(float v) {
+  v += round16<8>(v);
+  v += round16<4>(v);
+  v += round16<2>(v);
+  v += round16<1>(v);
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+template <int OUT, int V, int I>
+__global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
+  __shared__ float part[2][2][8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  int turn = 0;  // (two sets of sums: a wave writes its next row's while others still read this one's)
+  for (int64_t row = blockIdx.x; row < p.t; row += gridDim.x, turn ^= 1) {
+    const uint16_t* x = p.x + row * p.ldx;
+    const uint16_t* res = p.res ? p.res + row * p.ldr : nullptr;
+    Raw<V> xr[I], rr[I];
+    float w[I][V], z[I][V];
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (i * blockDim.x + tid) * V;
+      if (c < p.h) {
+        xr[i] = load<V>(x + c);
+        if (res) rr[i] = load<V>(res + c);
+        load_weight<V>(p.w, p.w_f32, c, w[i]);
+      }
+    }
+    float ss = 0.f, most = 0.f;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (i * blockDim.x + tid) * V;
+      if (c < p.h) {
+        widen<V>(xr[i], z[i]);
+        if (res) {
+          float f[V];
+          widen<V>(rr[i], f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) z[i][e] += f[e];
+        }
+        if (p.sum) store<V>(p.sum + row * p.lds + c, z[i]);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          ss = __builtin_fmaf(z[i][e], z[i][e], ss);
+          if constexpr (OUT == kInt8) most = fmaxf(most, fabsf(z[i][e] * w[i][e]));
+        }
+      }
+    }
+    ss = sum64(ss);
+    if constexpr (OUT == kInt8) most = max64(most);
+    if (waves > 1) {
+      if (lane == 0) {
+        part[turn][0][wave] = ss;
+        if constexpr (OUT == kInt8) part[turn][1][wave] = most;
+      }
+      __syncthreads();
+      ss = part[turn][0][0];
+      for (int k = 1; k < waves; ++k) ss += part[turn][0][k];
+      if constexpr (OUT == kInt8) {
+        most = part[turn][1][0];
+        for (int k = 1; k < waves; ++k) most = fmaxf(most, part[turn][1][k]);
+      }
+    }
+    const float r = 1.f / __builtin_sqrtf(ss / (float)p.h + p.eps);
+    // a row with a NaN, or whose sum of squares is not finite: NaN scales, so
+    // that what is computed from its codes is NaN too
+    const bool bad = !(ss < __builtin_inff());
+    if (p.rstd && tid == 0) p.rstd[row] = r;
+    float is = 1.f, ik = 1.f;  // INT8: 1 / scale, in two factors
+    if constexpr (OUT == kInt8) {
+      const float amax = most * r;
+      const float s = amax == 0.f ? 1.f : amax / 127.f;
+      const codec::GroupRecip g = codec::group_recip(s);
+      ik = g.k;
+      is = g.r;
+      if (tid == 0) static_cast<float*>(p.s)[row] = bad ? __builtin_nanf("") : s;
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (i * blockDim.x + tid) * V;
+      const bool in = c < p.h;
+      float y[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = in ? z[i][e] * r * w[i][e] : 0.f;
+      if constexpr (OUT == kBf16) {
+        if (in) store<V>(static_cast<uint16_t*>(p.y) + row * p.ldy + c, y);
+      } else if constexpr (OUT == kInt8) {
+        int q[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) q[e] = (int)__builtin_rintf(fminf(fmaxf(y[e] * ik * is, -127.f), 127.f));
+        int8_t* out = static_cast<int8_t*>(p.y) + row * p.h + c;
+        if (in) {
+          if constexpr (V == 8) {
+            uint32_t o[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              o[e] = (uint32_t)(q[4 * e] & 0xff) | ((uint32_t)(q[4 * e + 1] & 0xff) << 8) |
+                     ((uint32_t)(q[4 * e + 2] & 0xff) << 16) | ((uint32_t)q[4 * e + 3] << 24);
+            *reinterpret_cast<uint2*>(out) = uint2{o[0], o[1]};
+          } else {
+            *out = (int8_t)q[0];
+          }
+        }
+      } else {
+        // a group of 128 columns is 16 lanes
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) m = fmaxf(m, fabsf(y[e]));
+        m = max16(m);
+        float s;
+        uint32_t code = 0;
+        if constexpr (OUT == kFp8Ue8m0) {
+          code = codec::ue8m0_code(m);
+          s = codec::ue8m0_value(code);
+        } else {
+          s = codec::scale_of(m);
+        }
+        const codec::GroupRecip g = codec::group_recip(s);
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = codec::scaled(y[e], g);
+        if (in) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.h + c) =
+              uint2{codec::encode4(y[0], y[1], y[2], y[3]), codec::encode4(y[4], y[5], y[6], y[7])};
+          if ((lane & 15) == 0) {
+            const int group = c >> 7, groups = p.h >> 7;
+            if constexpr (OUT == kFp8Ue8m0) {
+              const int bytes = (groups + 3) / 4 * 4;
+              uint8_t* at = static_cast<uint8_t*>(p.s) + row * bytes;
+              at[group] = bad ? 255 : (uint8_t)code;
+              if (group == groups - 1)
+                for (int k = groups; k < bytes; ++k) at[k] = 0;
+            } else {
+              static_cast<float*>(p.s)[row * groups + group] = bad ? __builtin_nanf("") : s;
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---- backward ----
+//     g = w dy,  dz = r g - z r^3 / H sum(g z) + dsum,  dw = sum over rows of dy z r
+// A workgroup walks rows blockIdx.x, + gridDim.x, ...; a thread owns the same
+// columns of each, so dw is a sum in its registers, written once to
+// partial[workgroup] and summed in workgroup order by a second kernel (no
+// atomics: the same inputs give the same bits).
+struct BackwardParams {
+  const uint16_t* dy;
+  const uint16_t* x;
+  const uint16_t* dsum;  // or null
+  const void* w;         // or null
+  const float* rstd;
+  uint16_t* dx;          // or null
+  float* partial;        // or null
+  int64_t lddy, ldx, ldds, lddx;
+  int t, h, w_f32;
+};
+
+template <int V, int I>
+__global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams p) {
+  __shared__ float part[2][8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  float w[I][V], dw[I][V];
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int c = (i * blockDim.x + tid) * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[i][e] = 0.f;
+    if (c < p.h) load_weight<V>(p.w, p.w_f32, c, w[i]);
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.t; row += gridDim.x, turn ^= 1) {
+    float z[I][V], d[I][V];
+    Raw<V> ds[I];
+    const float r = p.rstd[row];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (i * blockDim.x + tid) * V;
+      if (c < p.h) {
+        widen<V>(load<V>(p.x + row * p.ldx + c), z[i]);
+        widen<V>(load<V>(p.dy + row * p.lddy + c), d[i]);
+        if (p.dsum) ds[i] = load<V>(p.dsum + row * p.ldds + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (i * blockDim.x + tid) * V;
+      if (c < p.h) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float n = z[i][e] * r;
+          dw[i][e] = __builtin_fmaf(d[i][e], n, dw[i][e]);
+          d[i][e] *= w[i][e];
+          z[i][e] = n;
+          dot = __builtin_fmaf(d[i][e], n, dot);
+        }
+      }
+    }
+    if (!p.dx) continue;  // (uniform over the workgroup)
+    dot = sum64(dot);
+    if (waves > 1) {
+      // (two sets: a wave writes its next row's while others still read this one's)
+      if (lane == 0) part[turn][wave] = dot;
+      __syncthreads();
+      dot = part[turn][0];
+      for (int k = 1; k < waves; ++k) dot += part[turn][k];
+    }
+    const float mean = dot / (float)p.h;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (i * blockDim.x + tid) * V;
+      if (c < p.h) {
+        float o[V], f[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = r * __builtin_fmaf(-z[i][e], mean, d[i][e]);
+        if (p.dsum) {
+          widen<V>(ds[i], f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] += f[e];
+        }
+        store<V>(p.dx + row * p.lddx + c, o);
+      }
+    }
+  }
+  if (p.partial) {
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (i * blockDim.x + tid) * V;
+      if (c < p.h) {
+        float* q = p.partial + (int64_t)blockIdx.x * p.h + c;
+#pragma unroll
+        for (int e = 0; e < V; ++e) q[e] = dw[i][e];
+      }
+    }
+  }
+}
+
+// dw of columns 64 b .. 64 b + 63: 16 waves sum a sixteenth of the partials each.
+__global__ __launch_bounds__(1024) void norm_weight_sum_kernel(const float* partial, float* dw, int parts, int h) {
+  __shared__ float sum[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane, per = (parts + 15) / 16;
+  float v = 0.f;
+  if (c < h) {
+#pragma unroll 8
+    for (int k = wave * per; k < min(parts, (wave + 1) * per); ++k) v += partial[(int64_t)k * h + c];
+  }
+  sum[wave][lane] = v;
+  __syncthreads();
+  if (wave == 0 && c < h) {
+    v = sum[0][lane];
+#pragma unroll
+    for (int k = 1; k < 16; ++k) v += sum[k][lane];
+    dw[c] = v;
+  }
+}
+
+// ---- host ----
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Rows that start on 16-byte boundaries.
+bool rows8(const void* p, int64_t ld, int t) { return aligned(p, 16) && (t == 1 || ld % 8 == 0); }
+
+// Pieces per thread (I) and waves (W) of a row of h columns.
+struct Shape {
+  int pieces, waves;
+};
+Shape shape_of(int h, bool vec) {
+  const int per = vec ? 512 : 64;  // columns per wave and piece
+  const int units = ceil_div(h, per);
+  for (int pieces : vec ? std::initializer_list<int>{1, 2, 4} : std::initializer_list<int>{4, 8, 16, 32}) {
+    const int waves = ceil_div(units, pieces);
+    if (waves <= 8) return Shape{pieces, waves};
+  }
+  return Shape{0, 0};
+}
+
+// (a launch holds fewer than 2^32 threads: more rows than that go several to a workgroup)
+template <int OUT, int V, int I>
+hipError_t launch_norm(const NormParams& p, int waves, hipStream_t stream) {
+  norm_kernel<OUT, V, I><<<p.t < (1 << 21) ? p.t : 1 << 21, 64 * waves, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <int OUT>
+hipError_t launch_out(const NormParams& p, bool vec, hipStream_t stream) {
+  const Shape s = shape_of(p.h, vec);
+  if (vec) {
+    if (s.pieces == 1) return launch_norm<OUT, 8, 1>(p, s.waves, stream);
+    if (s.pieces == 2) return launch_norm<OUT, 8, 2>(p, s.waves, stream);
+    return launch_norm<OUT, 8, 4>(p, s.waves, stream);
+  }
+  if constexpr (OUT == kBf16 || OUT == kInt8) {
+    if (s.pieces == 4) return launch_norm<OUT, 1, 4>(p, s.waves, stream);
+    if (s.pieces == 8) return launch_norm<OUT, 1, 8>(p, s.waves, stream);
+    if (s.pieces == 16) return launch_norm<OUT, 1, 16>(p, s.waves, stream);
+    return launch_norm<OUT, 1, 32>(p, s.waves, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <int V, int I>
+hipError_t launch_backward(const BackwardParams& p, int grid, int waves, hipStream_t stream) {
+  norm_backward_kernel<V, I><<<grid, 64 * waves, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+bool bad_weight(const void* w, int type) { return w && type != DG_TYPE_BF16 && type != DG_TYPE_F32; }
+bool unfit_weight(const void* w, int type) { return w && !aligned(w, type == DG_TYPE_F32 ? 4 : 2); }
+bool unfit_rows(const void* p, int64_t ld) { return !aligned(p, 2) || ld > kMaxLd; }
+
+// Checks `in` and fills `p`; *vec: every row in memory starts on a 16-byte boundary.
+dg_status make_norm(const dg_norm* in, int t, int h, NormParams* p, bool* vec) {
+  if (!in || !in->x || t <= 0 || h <= 0 || in->ld_x < h || !(in->eps >= 0.f) || in->eps > 3.4e38f)
+    return DG_ERROR_INVALID_VALUE;
+  if ((in->residual && in->ld_residual < h) || (in->sum && in->ld_sum < h) || bad_weight(in->weight, in->weight_type))
+    return DG_ERROR_INVALID_VALUE;
+  if (h > kMaxHidden || unfit_rows(in->x, in->ld_x) || (in->residual && unfit_rows(in->residual, in->ld_residual)) ||
+      (in->sum && unfit_rows(in->sum, in->ld_sum)) || unfit_weight(in->weight, in->weight_type) || !aligned(in->rstd, 4))
+    return DG_ERROR_UNSUPPORTED;
+  *p = NormParams{};
+  p->x = static_cast<const uint16_t*>(in->x);
+  p->res = static_cast<const uint16_t*>(in->residual);
+  p->w = in->weight;
+  p->w_f32 = in->weight_type == DG_TYPE_F32;
+  p->sum = static_cast<uint16_t*>(in->sum);
+  p->rstd = in->rstd;
+  p->ldx = in->ld_x;
+  p->ldr = in->ld_residual;
+  p->lds = in->ld_sum;
+  p->t = t;
+  p->h = h;
+  p->eps = in->eps;
+  *vec = h % 8 == 0 && rows8(in->x, in->ld_x, t) && (!in->residual || rows8(in->residual, in->ld_residual, t)) &&
+         (!in->sum || rows8(in->sum, in->ld_sum, t)) && (!in->weight || aligned(in->weight, 16));
+  return DG_SUCCESS;
+}
+
+dg_status fp8(const dg_norm* in, void* q, void* s, int t, int h, bool ue8m0, hipStream_t stream) {
+  NormParams p;
+  bool vec;
+  const dg_status st = make_norm(in, t, h, &p, &vec);
+  if (st != DG_SUCCESS) return st;
+  if (!q || !s) return DG_ERROR_INVALID_VALUE;
+  if (h % 128 != 0 || !vec || !aligned(q, 8) || !aligned(s, 4)) return DG_ERROR_UNSUPPORTED;
+  p.y = q;
+  p.s = s;
+  (void)hipGetLastError();  // clear a stale error from unrelated work
+  const hipError_t e = ue8m0 ? launch_out<kFp8Ue8m0>(p, true, stream) : launch_out<kFp8>(p, true, stream);
+  return e == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+}
+
+// Workgroups of the backward pass: each keeps a partial dw of h values (4 bytes
+// written and read again), so there are at most 512 of them.
+int backward_parts(int t) { return t < 512 ? t : 512; }
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+dg_status dg_rmsnorm_bf16(const dg_norm* in, void* y, int64_t ld_y, int tokens, int hidden, hipStream_t stream) {
+  NormParams p;
+  bool vec;
+  const dg_status st = make_norm(in, tokens, hidden, &p, &vec);
+  if (st != DG_SUCCESS) return st;
+  if (!y || ld_y < hidden) return DG_ERROR_INVALID_VALUE;
+  if (unfit_rows(y, ld_y)) return DG_ERROR_UNSUPPORTED;
+  p.y = y;
+  p.ldy = ld_y;
+  (void)hipGetLastError();
+  return launch_out<kBf16>(p, vec && rows8(y, ld_y, tokens), stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+}
+
+dg_status dg_rmsnorm_quantize_fp8_1x128(const dg_norm* in, void* q, float* s, int tokens, int hidden,
+                                        hipStream_t stream) {
+  return fp8(in, q, s, tokens, hidden, false, stream);
+}
+
+dg_status dg_rmsnorm_quantize_fp8_1x128_ue8m0(const dg_norm* in, void* q, int32_t* s, int tokens, int hidden,
+                                              hipStream_t stream) {
+  return fp8(in, q, s, tokens, hidden, true, stream);
+}
+
+dg_status dg_rmsnorm_quantize_int8(const dg_norm* in, void* q, float* s, int tokens, int hidden, hipStream_t stream) {
+  NormParams p;
+  bool vec;
+  const dg_status st = make_norm(in, tokens, hidden, &p, &vec);
+  if (st != DG_SUCCESS) return st;
+  if (!q || !s) return DG_ERROR_INVALID_VALUE;
+  if (!aligned(s, 4)) return DG_ERROR_UNSUPPORTED;
+  p.y = q;
+  p.s = s;
+  (void)hipGetLastError();
+  return launch_out<kInt8>(p, vec && aligned(q, 8), stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+}
+
+dg_status dg_rmsnorm_bf16_backward_workspace(int tokens, int hidden, int64_t* bytes) {
+  if (!bytes || tokens <= 0 || hidden <= 0) return DG_ERROR_INVALID_VALUE;
+  *bytes = 4 * (int64_t)backward_parts(tokens) * hidden;
+  return DG_SUCCESS;
+}
+
+dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, const void* weight,
+                                   int weight_type, const float* rstd, const void* dsum, int64_t ld_dsum, void* dx,
+                                   int64_t ld_dx, float* dweight, void* workspace, int tokens, int hidden,
+                                   hipStream_t stream) {
+  const int t = tokens, h = hidden;
+  if (!dy || !x || !rstd || t <= 0 || h <= 0 || ld_dy < h || ld_x < h || (dx && ld_dx < h) ||
+      (dx && dsum && ld_dsum < h) || bad_weight(weight, weight_type) || (dweight && !workspace))
+    return DG_ERROR_INVALID_VALUE;
+  const bool with_dsum = dx && dsum;
+  if (h > kMaxHidden || unfit_rows(dy, ld_dy) || unfit_rows(x, ld_x) || (dx && unfit_rows(dx, ld_dx)) ||
+      (with_dsum && unfit_rows(dsum, ld_dsum)) || unfit_weight(weight, weight_type) || !aligned(rstd, 4) ||
+      !aligned(dweight, 4) || (dweight && !aligned(workspace, 16)))
+    return DG_ERROR_UNSUPPORTED;
+  if (!dx && !dweight) return DG_SUCCESS;
+  BackwardParams p{};
+  p.dy = static_cast<const uint16_t*>(dy);
+  p.x = static_cast<const uint16_t*>(x);
+  p.dsum = with_dsum ? static_cast<const uint16_t*>(dsum) : nullptr;
+  p.w = weight;
+  p.w_f32 = weight_type == DG_TYPE_F32;
+  p.rstd = rstd;
+  p.dx = static_cast<uint16_t*>(dx);
+  p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+  p.lddy = ld_dy;
+  p.ldx = ld_x;
+  p.ldds = ld_dsum;
+  p.lddx = ld_dx;
+  p.t = t;
+  p.h = h;
+  const bool vec = h % 8 == 0 && rows8(dy, ld_dy, t) && rows8(x, ld_x, t) && (!dx || rows8(dx, ld_dx, t)) &&
+                   (!with_dsum || rows8(dsum, ld_dsum, t)) && (!weight || aligned(weight, 16));
+  const Shape s = shape_of(h, vec);
+  const int parts = backward_parts(t);
+  (void)hipGetLastError();
+  hipError_t e;
+  if (vec)
+    e = s.pieces == 1   ? launch_backward<8, 1>(p, parts, s.waves, stream)
+        : s.pieces == 2 ? launch_backward<8, 2>(p, parts, s.waves, stream)
+                        : launch_backward<8, 4>(p, parts, s.waves, stream);
+  else
+    e = s.pieces == 4   ? launch_backward<1, 4>(p, parts, s.waves, stream)
+        : s.pieces == 8 ? launch_backward<1, 8>(p, parts, s.waves, stream)
+        : s.pieces == 16 ? launch_backward<1, 16>(p, parts, s.waves, stream)
+                        : launch_backward<1, 32>(p, parts, s.waves, stream);
+  if (e != hipSuccess) return DG_ERROR_LAUNCH;
+  if (dweight) {
+    norm_weight_sum_kernel<<<ceil_div(h, 64), 1024, 0, stream>>>(p.partial, dweight, parts, h);
+    if (hipGetLastError() != hipSuccess) return DG_ERROR_LAUNCH;
+  }
+  return DG_SUCCESS;
+}
+
+}  // extern "C"

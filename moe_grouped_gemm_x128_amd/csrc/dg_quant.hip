@@ -41,28 +41,16 @@ constexpr int kQStrips = 8;      // float4 loads per thread: 128 rows x 32 float
 using codec::kE4m3Max;
 using codec::scale_of;
 using codec::encode4;
+using codec::ue8m0_code;
+using codec::ue8m0_value;
 using codec::silu;
 
 enum QuantMode : int { Q_ROWS = 0, Q_BLOCKS = 1, Q_TRANSPOSED = 2, Q_ROWS_UE8M0 = 3, Q_BLOCKS_UE8M0 = 4 };
 
-// Power-of-two (UE8M0) scales (DeepGEMM pages, aikraft.ru support table:
-// packed UE8M0, four values in one torch.int): a group's scale is the
-// smallest 2^(E - 127), E in [0, 254], not below s0 = scale_of(amax), read off
-// s0's fp32 fields -- an exact power keeps its exponent field, anything above
-// it takes the next; a subnormal s0 is at most 2^-127 (E = 0, the field 0
-// with mantissa 2^22) or below 2^-126 (E = 1).  The quotient by 2^(E - 127)
-// is exact, so the codes are those of an exact division.  E goes to byte
-// (group mod 4) of word group/4 of the row's packed words; a row's last group
-// also zeroes the bytes past it.
-__device__ __forceinline__ uint32_t ue8m0_code(float amax) {
-  const uint32_t b = __float_as_uint(scale_of(amax));
-  const uint32_t ex = b >> 23, man = b & 0x7fffffu;
-  if (ex == 0) return man > 0x400000u ? 1u : 0u;
-  return min(ex + (man != 0u ? 1u : 0u), 254u);
-}
-__device__ __forceinline__ float ue8m0_value(uint32_t e) {
-  return __uint_as_float(e == 0 ? 0x400000u : e << 23);
-}
+// Power-of-two (UE8M0) scales: codec::ue8m0_code of a group's amax.  The
+// quotient by 2^(E - 127) is exact, so the codes are those of an exact
+// division.  E goes to byte (group mod 4) of word group/4 of the row's packed
+// words; a row's last group also zeroes the bytes past it.
 // byte `g` of a row of `kw` packed words, plus the row's padding bytes when g
 // is its last group
 __device__ __forceinline__ void put_code(uint8_t* row_bytes, int g, int groups, int kw, uint32_t e) {

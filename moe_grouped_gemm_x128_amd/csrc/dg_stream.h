@@ -70,10 +70,16 @@ __device__ __forceinline__ v4f mfma_fp8(const v4i& w0, const v4i& w1, const v4i&
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-// Operand types: bf16 by bf16; fp8 weights with bf16 activations; fp8 by fp8.
-enum Mode : int { kBf16 = 0, kW8A16 = 1, kFp8 = 2 };
+__device__ __forceinline__ v4i mfma_int8(const v4i& w, const v4i& x, const v4i& acc) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, acc, 0, 0, 0);
+}
 
-constexpr int entry_bytes(int mode) { return 4096 + (mode == kBf16 ? 0 : mode == kW8A16 ? 16 : 128); }
+// Operand types: bf16 by bf16; fp8 weights with bf16 activations; fp8 by fp8;
+// int8 by int8 (int32 sums; moves its bytes as bf16 does).
+enum Mode : int { kBf16 = 0, kW8A16 = 1, kFp8 = 2, kInt8 = 3 };
+
+constexpr bool block_scales(int mode) { return mode == kW8A16 || mode == kFp8; }  // in the stream
+constexpr int entry_bytes(int mode) { return 4096 + (!block_scales(mode) ? 0 : mode == kW8A16 ? 16 : 128); }
 constexpr int ring_bytes(int mode, int waves, int depth) { return waves * depth * entry_bytes(mode); }
 
 // The unit a cursor stands on, as wave-uniform values; Cursor adds
@@ -103,7 +109,7 @@ struct Unit {
 template <int MODE, int D, bool PARTIAL, bool SAME, class Cursor, bool EXACT = false>
 struct Pipe {
   static constexpr int kEntry = entry_bytes(MODE);
-  static constexpr int kLoads = MODE == kBf16 ? 4 : 5;
+  static constexpr int kLoads = block_scales(MODE) ? 5 : 4;
   static constexpr int WE = SAME || MODE == kW8A16 ? 1 : 2;  // weight entries per unit
   static constexpr int XE = SAME && MODE == kW8A16 ? 2 : 1;  // activation entries per tile
   static_assert((D - 1) * kLoads < 64, "vmcnt range");
@@ -154,7 +160,7 @@ struct Pipe {
         for (int j = 0; j < 2; ++j)
           dma::load16_nt(lds + (2 * g + j) * 1024, r, !PARTIAL || (int)xc[j] < lg ? wv[j] : kOut);
       }
-      if constexpr (MODE != kBf16) {
+      if constexpr (block_scales(MODE)) {
         // lane 0: A's scale, lane 1: B's
         const uint32_t so = (lane ? u.so[1] : u.so[0]) + (MODE == kFp8 && !SAME ? 4u * phase : 0u);
         const dma::v4i r = dma::resource(u.s, left > 0 ? u.srange : 0u);
@@ -173,7 +179,7 @@ struct Pipe {
         for (int j = 0; j < 2; ++j)
           dma::load16(lds + (2 * l + j) * 1024, r, !part || at + (int)xc[j] < u.xbytes ? off[j] + xc[j] : kOut);
       }
-      if constexpr (MODE != kBf16) {
+      if constexpr (block_scales(MODE)) {
         if constexpr (MODE == kFp8) {
           const dma::v4i r = dma::resource(u.xs, u.xsrange);
           const uint32_t so = ic.scale(t);
@@ -214,8 +220,8 @@ struct Pipe {
   // l16, rows 4 lq .. 4 lq + 3 of the group; SAME: two parts of one sum).  The
   // last weight entry and the first activation entry are read together: one
   // LDS latency for both.
-  template <int NT>
-  __device__ __forceinline__ void unit(int tiles, v4f* a, v4f* b) {
+  template <int NT, class Acc>
+  __device__ __forceinline__ void unit(int tiles, Acc* a, Acc* b) {
     v4i w[2][WE][2];  // [group][entry][chunk lq, lq + 4]
     float s[2][WE];
 #pragma unroll
@@ -225,7 +231,7 @@ struct Pipe {
       for (int g = 0; g < 2; ++g) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) w[g][e][j] = *(lv)(uintptr_t)(lds + 2048 * g + o[j]);
-        s[g][e] = MODE != kBf16 ? *(lf)(uintptr_t)(lds + 4096 + 4 * g) : 1.f;
+        s[g][e] = block_scales(MODE) ? *(lf)(uintptr_t)(lds + 4096 + 4 * g) : 1.f;
       }
       if (e + 1 < WE) release<1>();
     }
@@ -247,14 +253,19 @@ struct Pipe {
         if (held) release<2>(); else release<1>();
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          v4f& acc = g ? b[t] : a[t];
-          if constexpr (MODE == kBf16) {
+          Acc& acc = g ? b[t] : a[t];
+          if constexpr (MODE == kBf16 || MODE == kInt8) {
             // group g by every line of the unit, or (SAME) its own
 #pragma unroll
             for (int l = 0; l < 2; ++l)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                if (!SAME || l == g) acc = mfma_bf16(w[g][SAME ? 0 : l][j], x[l][j], acc);
+                if (!SAME || l == g) {
+                  if constexpr (MODE == kInt8)
+                    acc = mfma_int8(w[g][SAME ? 0 : l][j], x[l][j], acc);
+                  else
+                    acc = mfma_bf16(w[g][SAME ? 0 : l][j], x[l][j], acc);
+                }
           } else if constexpr (MODE == kW8A16) {
             if (SAME && xe != g) continue;
             v4f p = v4f{0.f, 0.f, 0.f, 0.f};
