@@ -22,21 +22,24 @@ constexpr int kMaxHidden = 1 << 20;
 
 // ---- sort: the row of every slot ----
 // Stable counting sort.  Slots go in chunks, a workgroup each; a wave owns a run
-// of its chunk.  Lanes of a wave with the same expert find each other by ballots
-// over the bits of the expert's number, so a slot's rank is the count of its
-// expert in the chunks before, the waves before, the wave's rounds before and
-// the lanes before -- slots of an expert keep their order, whatever runs first.
+// of its chunk, 64 slots a round.  Lanes of a wave with the same expert find each
+// other by ballots over the bits of the expert's number, so a slot's rank is the
+// count of its expert in the chunks before, the waves before, the wave's rounds
+// before and the lanes before -- slots of an expert keep their order, whatever
+// runs first.  What bounds it is the chain of those steps, not their work: chunks
+// are one round long where there are few, and up to kCountedHere slots every
+// workgroup counts all of them itself, instead of a launch before it (2048 x 8
+// slots, 64 experts: 9.8 us with that launch and two rounds).
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kOneChunk = 8192;    // slots that one workgroup sorts alone, in one launch
-constexpr int kChunk = 2048;       // more slots: at least this many per workgroup
 constexpr int kMaxChunks = 256;
+constexpr int kCountedHere = 16384;
 
 struct SortParams {
   const int32_t* ids;
   int32_t* m_indices;  // contiguous layout
   int32_t* rows;
   int32_t* counts;     // rows of each expert, or null
-  int32_t* hist;       // [chunks][experts] (chunks > 1)
+  int32_t* hist;       // [chunks][experts], counted by sort_count_kernel, or null: counted here
   int slots, experts, chunk, chunks;
   int limit;           // contiguous: M_total; masked: M_max
 };
@@ -71,9 +74,10 @@ __device__ __forceinline__ uint64_t same_lanes(int e, int bits) {
   return m;
 }
 
-template <bool MASKED>
+// ONE: a wave's run is one round.
+template <bool MASKED, bool ONE>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortParams p) {
-  __shared__ uint16_t before[kSortWaves][kMaxExperts];  // of an expert, in the waves before (and rounds done)
+  __shared__ __attribute__((aligned(16))) uint16_t before[kSortWaves][kMaxExperts];  // of an expert, in the waves before (and rounds done)
   __shared__ int base[kMaxExperts];                      // row of the chunk's first slot of an expert
   __shared__ int first_row[kMaxExperts], total[kMaxExperts];
   __shared__ int part[2][kSortThreads];
@@ -81,52 +85,76 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortPara
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int E = p.experts, bits = 32 - __builtin_clz(E);  // (E itself stands for "no expert")
   const int c0 = blockIdx.x * p.chunk, c1 = min(p.slots, c0 + p.chunk);
-  const int run = ((p.chunk + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
+  const int run = ONE ? 64 : ((p.chunk + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
   const int w0 = c0 + wave * run, w1 = min(c1, w0 + run);
-  for (int i = tid; i < kSortWaves * E; i += kSortThreads) before[i / E][i % E] = 0;
+  auto expert = [&](int s) {
+    const int id = s < w1 ? p.ids[s] : -1;
+    return (uint32_t)id < (uint32_t)E ? id : E;
+  };
+  int mine = ONE ? expert(w0 + lane) : 0;
+  for (int i = tid; i < kSortWaves * (kMaxExperts / 2); i += kSortThreads)
+    if ((i % (kMaxExperts / 2)) * 2 < E) reinterpret_cast<uint32_t*>(before)[i] = 0;
+  part[0][tid] = part[1][tid] = 0;
   __syncthreads();
   // counts per wave
-  for (int s = w0; s < w1; s += 64) {
-    const int id = s + lane < w1 ? p.ids[s + lane] : -1;
-    const int e = (uint32_t)id < (uint32_t)E ? id : E;
-    const uint64_t same = same_lanes(e, bits);
-    if (e < E && (same & ((1ull << lane) - 1)) == 0) before[wave][e] += (uint16_t)__popcll(same);
-    wave_sync();
-  }
-  // counts of the other chunks: all of them, and those before this one
-  int mine = 0, earlier = 0, all = 0;  // of expert `tid`
-  if (p.chunks > 1) {
-    int per = 1;  // threads per expert, a power of two
-    while (per * 2 * E <= kSortThreads) per *= 2;
-    const int e = tid / per, k = tid % per;
-    int a = 0, b = 0;
-    if (e < E) {
-#pragma unroll 8
-      for (int c = k; c < p.chunks; c += per) {
-        const int n = p.hist[(int64_t)c * E + e];
-        a += n;
-        b += c < (int)blockIdx.x ? n : 0;
-      }
-    }
-    part[0][tid] = a;
-    part[1][tid] = b;
-    __syncthreads();
-    if (tid < E) {
-      for (int k2 = 0; k2 < per; ++k2) {
-        all += part[0][tid * per + k2];
-        earlier += part[1][tid * per + k2];
-      }
-    }
+  uint64_t same = ONE ? same_lanes(mine, bits) : 0;
+  if constexpr (ONE) {
+    if (mine < E && (same & ((1ull << lane) - 1)) == 0) before[wave][mine] = (uint16_t)__popcll(same);
   } else {
-    __syncthreads();
-  }
-  if (tid < E) {
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int n = before[w][tid];
-      before[w][tid] = (uint16_t)mine;
-      mine += n;
+    for (int s = w0; s < w1; s += 64) {
+      const int e = expert(s + lane);
+      const uint64_t m = same_lanes(e, bits);
+      if (e < E && (m & ((1ull << lane) - 1)) == 0) before[wave][e] += (uint16_t)__popcll(m);
+      wave_sync();
     }
-    if (p.chunks == 1) all = mine;
+  }
+  // counts of all chunks, and of those before this one
+  int per = 1;  // threads per expert, a power of two
+  if (p.chunks > 1) {
+    if (p.hist) {
+      while (per * 2 * E <= kSortThreads) per *= 2;
+      const int e = tid / per, k = tid % per;
+      int a = 0, b = 0;
+      if (e < E) {
+#pragma unroll 8
+        for (int c = k; c < p.chunks; c += per) {
+          const int n = p.hist[(int64_t)c * E + e];
+          a += n;
+          b += c < (int)blockIdx.x ? n : 0;
+        }
+      }
+      part[0][tid] = a;
+      part[1][tid] = b;
+    } else {
+#pragma unroll 4
+      for (int s = tid; s < p.slots; s += kSortThreads) {
+        const int id = p.ids[s];
+        if ((uint32_t)id < (uint32_t)E) {
+          atomicAdd(&part[0][id], 1);
+          if (s < c0) atomicAdd(&part[1][id], 1);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  int earlier = 0, all = 0;  // of expert `tid`
+  if (tid < E) {
+    int n[kSortWaves], sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) n[w] = before[w][tid];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      before[w][tid] = (uint16_t)sum;
+      sum += n[w];
+    }
+    all = sum;
+    if (p.chunks > 1) {
+      all = 0;
+      for (int k = 0; k < per; ++k) {
+        all += part[0][tid * per + k];
+        earlier += part[1][tid * per + k];
+      }
+    }
   }
   // the experts' first rows
   int start;
@@ -154,36 +182,69 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortPara
   }
   __syncthreads();
   // rows of the slots
-  for (int s = w0; s < w1; s += 64) {
-    const int id = s + lane < w1 ? p.ids[s + lane] : -1;
-    const int e = (uint32_t)id < (uint32_t)E ? id : E;
-    const uint64_t same = same_lanes(e, bits);
-    const uint64_t lower = same & ((1ull << lane) - 1);
+  auto place = [&](int s, int e, uint64_t m) {
+    const int lower = __popcll(m & ((1ull << lane) - 1));
     int row = -1;
     if (e < E) {
-      const int rank = before[wave][e] + __popcll(lower);
-      row = base[e] + rank;
+      row = base[e] + before[wave][e] + lower;
       if (MASKED ? row >= first_row[e] + p.limit : row >= p.limit) row = -1;
     }
-    wave_sync();  // (every lane has read its count)
-    if (e < E && lower == 0) before[wave][e] += (uint16_t)__popcll(same);
-    wave_sync();
-    if (s + lane < w1) {
-      p.rows[s + lane] = row;
-      if (!MASKED && row >= 0) p.m_indices[row] = e;
+    if constexpr (!ONE) {
+      wave_sync();  // (every lane has read its count)
+      if (e < E && lower == 0) before[wave][e] += (uint16_t)__popcll(m);
+      wave_sync();
+    }
+    if (s < w1) p.rows[s] = row;
+  };
+  if constexpr (ONE) {
+    place(w0 + lane, mine, same);
+  } else {
+    for (int s = w0; s < w1; s += 64) {
+      const int e = expert(s + lane);
+      place(s + lane, e, same_lanes(e, bits));
     }
   }
   if constexpr (!MASKED) {
-    // rows without a slot: behind each expert's, and behind the last segment
-    for (int e = blockIdx.x * kSortWaves + wave; e < E; e += p.chunks * kSortWaves) {
-      const int n = total[e], r0 = first_row[e] + n;
-      const int r1 = min(p.limit, first_row[e] + (n + kSegment - 1) / kSegment * kSegment);
-      for (int r = r0 + lane; r < r1; r += 64) p.m_indices[r] = -1;
+    // the experts of the rows, a wave per block of 128: the last expert that
+    // starts at or before the block is the only one that can have rows in it
+    for (int64_t r0 = ((int64_t)blockIdx.x * kSortWaves + wave) * kSegment; r0 < p.limit;
+         r0 += (int64_t)p.chunks * kSortWaves * kSegment) {
+      int lo = 0, hi = E;  // first_row[lo] <= r0, and first_row[hi] > r0 or hi == E
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (first_row[mid] <= r0)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int64_t end = first_row[lo] + total[lo], r = r0 + 2 * lane;
+      p.m_indices[r] = r < end ? lo : -1;
+      p.m_indices[r + 1] = r + 1 < end ? lo : -1;
     }
-    const int64_t end = first_row[E - 1] + (total[E - 1] + kSegment - 1) / kSegment * kSegment;
-    for (int64_t r = end + (int64_t)blockIdx.x * kSortThreads + tid; r < p.limit; r += (int64_t)p.chunks * kSortThreads)
-      p.m_indices[r] = -1;
   }
+}
+
+// ---- 16 bytes per lane ----
+// Rows that are gathered are read once, with the nontemporal cache policy (the
+// gradients of 4096 x 8 rows of 8 KB: 183 -> 169 us).  Rows that are scattered
+// are written with it from 256 MB on, the size of the last cache, which
+// would keep none of them for the GEMM that reads them (470 MB: 108 -> 88 us, with
+// that GEMM 753 -> 729); fewer are left in the caches (59 MB, with the GEMM: 184 us,
+// 197 with the policy).
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+constexpr int64_t kLastCache = 256 << 20;
+
+__device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<const uint4*>(p); }
+__device__ __forceinline__ uint4 load16_once(const void* p) {
+  const v4u v = __builtin_nontemporal_load(static_cast<const v4u*>(p));
+  return uint4{v[0], v[1], v[2], v[3]};
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(void* p, const uint4& v) {
+  if constexpr (STREAM)
+    __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, static_cast<v4u*>(p));
+  else
+    *static_cast<uint4*>(p) = v;
 }
 
 // ---- rows without a token in the segments' last blocks: zeros ----
@@ -197,15 +258,16 @@ __device__ void zero_padding(const int32_t* m_indices, int group, int groups, in
     if (m_indices[r0 / kSegment * kSegment] < 0) continue;
     for (int64_t r = r0 + wave; r < r0 + kPadRows; r += waves) {
       if (m_indices[r] >= 0) continue;
-      for (int64_t b = lane * 16; b < row_bytes; b += 1024) *reinterpret_cast<uint4*>(a + r * row_bytes + b) = uint4{0, 0, 0, 0};
+      for (int64_t b = lane * 16; b < row_bytes; b += 1024) store16<false>(a + r * row_bytes + b, uint4{0, 0, 0, 0});
       for (int b = lane * 4; b < scale_bytes; b += 256) *reinterpret_cast<uint32_t*>(sa + r * scale_bytes + b) = 0;
     }
   }
 }
 
 // ---- dispatch: a[row of slot] = x[token] ----
-// A wave takes U KB of a token's row into registers and writes them to each of
-// its slots' rows: x is read once.
+// A wave takes one KB of a token's row into registers and writes it to each of
+// its slots' rows: x is read once.  (Two, four and eight KB per wave are 3 to 6%
+// slower at 8192 tokens of 7 KB to 8 rows each, and leave CUs idle at few tokens.)
 struct DispatchParams {
   const uint8_t* x;
   const uint8_t* s;   // scales, or null
@@ -217,7 +279,7 @@ struct DispatchParams {
   int tokens, top_k, row_bytes, scale_bytes, pieces, copies;  // pieces: waves per token; copies: workgroups that copy
 };
 
-template <int U>
+template <bool STREAM>
 __global__ __launch_bounds__(256) void dispatch_kernel(const DispatchParams p) {
   if ((int)blockIdx.x >= p.copies) {
     zero_padding(p.m_indices, blockIdx.x - p.copies, gridDim.x - p.copies, p.m, p.a, p.row_bytes, p.sa, p.scale_bytes);
@@ -230,22 +292,16 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const DispatchParams p) {
     const int64_t token = item / p.pieces;
     const int piece = (int)(item - token * p.pieces);
     const uint8_t* x = p.x + token * p.ldx;
-    const int at = piece * U * 1024 + lane * 16;
-    uint4 v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      v[u] = uint4{0, 0, 0, 0};
-      if (at + u * 1024 < p.row_bytes) v[u] = *reinterpret_cast<const uint4*>(x + at + u * 1024);
-    }
+    const int at = piece * 1024 + lane * 16;
+    const bool in = at < p.row_bytes;
+    uint4 v{0, 0, 0, 0};
+    if (in) v = load16(x + at);
     // (the rows of the token's slots, one per lane)
     const int32_t own = lane < p.top_k ? p.rows[token * p.top_k + lane] : -1;
     for (int j = 0; j < p.top_k; ++j) {
       const int64_t row = __builtin_amdgcn_readlane(own, j);
       if (row < 0 || row >= p.m) continue;
-      uint8_t* a = p.a + row * p.row_bytes;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (at + u * 1024 < p.row_bytes) *reinterpret_cast<uint4*>(a + at + u * 1024) = v[u];
+      if (in) store16<STREAM>(p.a + row * p.row_bytes + at, v);
       if (piece == 0)
         for (int b = lane * 4; b < p.scale_bytes; b += 256)
           *reinterpret_cast<uint32_t*>(p.sa + row * p.scale_bytes + b) =
@@ -293,7 +349,7 @@ __device__ __forceinline__ void combine_piece(const CombineParams& p, int64_t to
   }
   float y[8];
   uint4 r{0, 0, 0, 0};
-  if (p.res && in) r = *reinterpret_cast<const uint4*>(p.res + token * p.ldr + c);
+  if (p.res && in) r = load16(p.res + token * p.ldr + c);
   widen8(r, y);
   for (int j0 = 0; j0 < p.top_k; j0 += 8) {
     uint4 v[8];
@@ -301,7 +357,7 @@ __device__ __forceinline__ void combine_piece(const CombineParams& p, int64_t to
     for (int j = 0; j < 8; ++j) {
       const int row = __builtin_amdgcn_readlane(own, (j0 + j) & 63);
       v[j] = uint4{0, 0, 0, 0};
-      if (row >= 0 && in) v[j] = *reinterpret_cast<const uint4*>(p.o + (int64_t)row * p.h + c);
+      if (row >= 0 && in) v[j] = load16_once(p.o + (int64_t)row * p.h + c);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -314,7 +370,7 @@ __device__ __forceinline__ void combine_piece(const CombineParams& p, int64_t to
       for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(w, f[e], y[e]);
     }
   }
-  if (in) *reinterpret_cast<uint4*>(p.y + token * p.ldy + c) = pack8(y);
+  if (in) store16<false>(p.y + token * p.ldy + c, pack8(y));
 }
 
 __global__ __launch_bounds__(256) void combine_kernel(const CombineParams p) {
@@ -340,7 +396,7 @@ struct CombineBackwardParams {
   int tokens, top_k, h, copies;  // copies: workgroups that take tokens
 };
 
-template <int K>
+template <int K, bool STREAM>
 __global__ __launch_bounds__(512) void combine_backward_kernel(const CombineBackwardParams p) {
   __shared__ float part[2][8][kMaxTopK];
   if ((int)blockIdx.x >= p.copies) {
@@ -368,7 +424,7 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(const CombineBack
     }
     for (int c = tid * 8; c < p.h; c += blockDim.x * 8) {
       float d[8];
-      widen8(*reinterpret_cast<const uint4*>(p.dy + token * p.lddy + c), d);
+      widen8(load16(p.dy + token * p.lddy + c), d);
 #pragma unroll
       for (int j0 = 0; j0 < K; j0 += 8) {
         uint4 v[8];
@@ -376,7 +432,7 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(const CombineBack
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             v[j] = uint4{0, 0, 0, 0};
-            if (row[j0 + j] >= 0) v[j] = *reinterpret_cast<const uint4*>(p.o + (int64_t)row[j0 + j] * p.h + c);
+            if (row[j0 + j] >= 0) v[j] = load16_once(p.o + (int64_t)row[j0 + j] * p.h + c);
           }
         }
 #pragma unroll
@@ -392,7 +448,7 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(const CombineBack
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = w[j0 + j] * d[e];
-            *reinterpret_cast<uint4*>(p.dout + (int64_t)row[j0 + j] * p.h + c) = pack8(f);
+            store16<STREAM>(p.dout + (int64_t)row[j0 + j] * p.h + c, pack8(f));
           }
         }
       }
@@ -419,11 +475,8 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 void chunks_of(int slots, int* chunk, int* chunks) {
-  *chunk = slots;
-  if (slots > kOneChunk) {
-    const int even = ceil_div(slots, kMaxChunks);
-    *chunk = even > kChunk ? even : kChunk;
-  }
+  const int even = ceil_div(slots, kMaxChunks);
+  *chunk = even > kSortThreads ? even : kSortThreads;  // at least a round of every wave
   *chunks = ceil_div(slots, *chunk);
 }
 
@@ -437,16 +490,18 @@ dg_status bad_routing(int tokens, int top_k, int experts) {
 dg_status sort(SortParams p, int tokens, int top_k, bool masked, void* workspace, hipStream_t stream) {
   p.slots = tokens * top_k;
   chunks_of(p.slots, &p.chunk, &p.chunks);
-  p.hist = static_cast<int32_t*>(workspace);
+  p.hist = p.slots > kCountedHere ? static_cast<int32_t*>(workspace) : nullptr;
   (void)hipGetLastError();  // clear a stale error from unrelated work
-  if (p.chunks > 1) {
+  if (p.hist) {
     sort_count_kernel<<<p.chunks, kSortThreads, 0, stream>>>(p);
     if (hipGetLastError() != hipSuccess) return DG_ERROR_LAUNCH;
   }
-  if (masked)
-    sort_place_kernel<true><<<p.chunks, kSortThreads, 0, stream>>>(p);
+  if (p.chunk == kSortThreads)
+    masked ? sort_place_kernel<true, true><<<p.chunks, kSortThreads, 0, stream>>>(p)
+           : sort_place_kernel<false, true><<<p.chunks, kSortThreads, 0, stream>>>(p);
   else
-    sort_place_kernel<false><<<p.chunks, kSortThreads, 0, stream>>>(p);
+    masked ? sort_place_kernel<true, false><<<p.chunks, kSortThreads, 0, stream>>>(p)
+           : sort_place_kernel<false, false><<<p.chunks, kSortThreads, 0, stream>>>(p);
   return hipGetLastError() == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
@@ -464,20 +519,21 @@ constexpr int kMostGroups = 1 << 21;
 int groups_of(int64_t n) { return n < kMostGroups ? (int)n : kMostGroups; }
 int pad_groups(const int32_t* m_indices, int64_t m) { return m_indices ? groups_of(m / kPadRows) : 0; }
 
+// Bytes that the slots' rows are at most.
+int64_t written(int tokens, int top_k, int64_t m, int64_t row_bytes) {
+  const int64_t slots = (int64_t)tokens * top_k;
+  return (slots < m ? slots : m) * row_bytes;
+}
+
 dg_status dispatch(DispatchParams p, hipStream_t stream) {
-  const int kb = ceil_div(p.row_bytes, 1024);  // a wave's 16 bytes per lane
-  // Few tokens: as many waves as there are KB, so that a row's pieces move at once
-  const int u = (int64_t)p.tokens * kb <= 4096 ? 1 : kb <= 2 ? 2 : 4;
-  p.pieces = ceil_div(kb, u);
+  p.pieces = ceil_div(p.row_bytes, 1024);
   p.copies = groups_of(((int64_t)p.tokens * p.pieces + 3) / 4);
   const int grid = p.copies + pad_groups(p.m_indices, p.m);
   (void)hipGetLastError();
-  if (u == 1)
-    dispatch_kernel<1><<<grid, 256, 0, stream>>>(p);
-  else if (u == 2)
-    dispatch_kernel<2><<<grid, 256, 0, stream>>>(p);
+  if (written(p.tokens, p.top_k, p.m, p.row_bytes) >= kLastCache)
+    dispatch_kernel<true><<<grid, 256, 0, stream>>>(p);
   else
-    dispatch_kernel<4><<<grid, 256, 0, stream>>>(p);
+    dispatch_kernel<false><<<grid, 256, 0, stream>>>(p);
   return hipGetLastError() == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
@@ -523,7 +579,7 @@ dg_status dg_moe_sort_workspace(int tokens, int top_k, int num_experts, int64_t*
   if (st != DG_SUCCESS) return st;
   int chunk, chunks;
   chunks_of(tokens * top_k, &chunk, &chunks);
-  *bytes = chunks > 1 ? 4 * (int64_t)chunks * num_experts : 0;
+  *bytes = tokens * top_k > kCountedHere ? 4 * (int64_t)chunks * num_experts : 0;
   return DG_SUCCESS;
 }
 
@@ -655,10 +711,13 @@ dg_status dg_moe_combine_bf16_backward(const void* dy, int64_t ld_dy, const void
   p.copies = groups_of(tokens);
   const int grid = p.copies + pad_groups(p.m_indices, m);
   (void)hipGetLastError();
+  const bool many = dout && written(tokens, top_k, m, 2 * (int64_t)hidden) >= kLastCache;
   if (top_k <= 8)
-    combine_backward_kernel<8><<<grid, 64 * waves, 0, stream>>>(p);
+    many ? combine_backward_kernel<8, true><<<grid, 64 * waves, 0, stream>>>(p)
+         : combine_backward_kernel<8, false><<<grid, 64 * waves, 0, stream>>>(p);
   else
-    combine_backward_kernel<16><<<grid, 64 * waves, 0, stream>>>(p);
+    many ? combine_backward_kernel<16, true><<<grid, 64 * waves, 0, stream>>>(p)
+         : combine_backward_kernel<16, false><<<grid, 64 * waves, 0, stream>>>(p);
   return hipGetLastError() == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
