@@ -14,7 +14,9 @@ preallocated by the caller).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch  # loads torch's HIP runtime first, so the library binds to it
 
@@ -27,6 +29,12 @@ if not os.path.exists(LIB_PATH):
         "(python moe_grouped_gemm_x128_amd/build.py); there is no fallback path")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+try:
+    from . import _tensors
+except ImportError as e:
+    raise ImportError(f"the binding's native helper cannot be loaded ({e}): build it with the library "
+                      "(python moe_grouped_gemm_x128_amd/build.py); there is no fallback path") from e
 
 _vp, _i32 = ctypes.c_void_p, ctypes.c_int
 _lib.dg_gemm_fp8_nt.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp]
@@ -76,13 +84,6 @@ _lib.dg_moe_few_tokens_fp8.argtypes = [_vp] * 11 + [_i32] * 7 + [_f32c, _vp]
 _lib.dg_moe_few_tokens_fp8.restype = ctypes.c_int
 _lib.dg_moe_few_tokens_bf16.argtypes = [_vp] * 9 + [_i32] * 7 + [_f32c, _vp]
 _lib.dg_moe_few_tokens_bf16.restype = ctypes.c_int
-
-
-class _Norm(ctypes.Structure):
-    _fields_ = [("x", _vp), ("ld_x", _i64), ("residual", _vp), ("ld_residual", _i64), ("weight", _vp),
-                ("weight_type", _i32), ("eps", _f32c), ("sum", _vp), ("ld_sum", _i64), ("rstd", _vp)]
-
-
 _lib.dg_rmsnorm_bf16.argtypes = [_vp, _vp, _i64, _i32, _i32, _vp]
 _lib.dg_rmsnorm_bf16_backward.argtypes = [_vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i32,
                                           _i32, _vp]
@@ -720,54 +721,59 @@ def moe_few_tokens_bf16(x, w13, w2, out, ids, weights, logits=None, scoring="sof
 
 
 # ------------------------- norm with the residual's addition, INT8 layer ---
+# Small calls are bound by what happens before the launch, so each tensor is
+# looked at once, natively (csrc/dg_tensors.cpp); the reason for a refusal is
+# worked out only then.
 
-def _norm(x, weight, eps, residual, sum_out, rstd, dev):
-    _bf16(x, "x")
-    t, h = x.shape
-    p = _Norm(_ptr(x), _ld(x, dev, "x"))
-    p.eps = eps
-    if weight is not None:
-        p.weight, p.weight_type = _weight(weight, h, dev)
-    if residual is not None:
-        _bf16(residual, "residual"); _shape(residual, (t, h), "residual")
-        p.residual, p.ld_residual = _ptr(residual), _ld(residual, dev, "residual")
-    if sum_out is not None:
-        _bf16(sum_out, "sum_out"); _shape(sum_out, (t, h), "sum_out")
-        p.sum, p.ld_sum = _ptr(sum_out), _ld(sum_out, dev, "sum_out")
-    if rstd is not None:
-        p.rstd = _vector(rstd, (t,), dev, "rstd")
-    return p, t, h
+_BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
+_norm_fields = struct.Struct("PqPqPifPqP").pack   # dg_norm
+_epilogue_fields = struct.Struct("PiiPqPq").pack  # dg_epilogue
 
 
-def _weight(weight, h, dev):
-    kind = _TYPE.get(weight.dtype)
+def _device_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+_stream_of = _raw_stream or _device_stream
+
+
+def _refuse(t, dtype, shape, dev, name):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same GPU as the call's first tensor")
+    raise ValueError(f"{name} must be contiguous (a matrix whose stride the call takes: contiguous rows that do not "
+                     f"overlap), got strides {t.stride()}")
+
+
+_tensors.refuse_with(_refuse)
+_whole = _tensors.whole  # address of a contiguous tensor of the given type and shape on GPU `dev`
+_rows = _tensors.rows    # address and row stride of a matrix with contiguous rows
+
+
+def _bytes8(t, shape, dev, name):
+    """Pointer of a contiguous tensor of FP8 values or their bytes."""
+    _fp8(t, name)
+    return _whole(t, t.dtype, shape, dev, name)
+
+
+def _vector_type(t, n, dev, name):
+    """Pointer and type of a contiguous vector in bf16 or fp32."""
+    kind = _TYPE.get(t.dtype)
     if kind is None:
-        raise TypeError(f"weight must be bfloat16 or float32, got {weight.dtype}")
-    if weight.shape != (h,) or weight.get_device() != dev or not weight.is_contiguous():
-        raise ValueError(f"weight must be contiguous with shape {(h,)}, on the same GPU, got {tuple(weight.shape)}")
-    return _ptr(weight), kind
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return _whole(t, t.dtype, (n,), dev, name), kind
 
 
-def _vector(t, shape, dev, name):
-    """Pointer of a contiguous fp32 tensor of the given shape on GPU `dev`."""
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be float32, got {t.dtype}")
-    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {shape}, on the same GPU, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _plain(t, shape, dev, name):
-    """Pointer of a contiguous tensor of the given shape on GPU `dev`."""
-    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, on the same GPU, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _int32(t, shape, dev, name):
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    return _plain(t, shape, dev, name)
+def _matrix(t, name):
+    """Shape and GPU of a call's first tensor."""
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    return t.shape, t.get_device()
 
 
 def _room(workspace, need, dev, like):
@@ -775,11 +781,26 @@ def _room(workspace, need, dev, like):
     if not need:
         return None
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = like.new_empty(need, dtype=torch.uint8)
     elif workspace.get_device() != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be contiguous, on the same GPU, with at least {need} bytes")
     return workspace.data_ptr()
+
+
+def _norm(x, shape, weight, eps, residual, sum_out, rstd, dev):
+    """The call's dg_norm, as bytes."""
+    xp, ldx = _rows(x, _BF16, shape, dev, "x")
+    wp = rp = sp = dp = wt = ldr = lds = 0
+    if weight is not None:
+        wp, wt = _vector_type(weight, shape[1], dev, "weight")
+    if residual is not None:
+        rp, ldr = _rows(residual, _BF16, shape, dev, "residual")
+    if sum_out is not None:
+        sp, lds = _rows(sum_out, _BF16, shape, dev, "sum_out")
+    if rstd is not None:
+        dp = _whole(rstd, _F32, shape[:1], dev, "rstd")
+    return _norm_fields(xp, ldx, rp, ldr, wp, wt, eps, sp, lds, dp)
 
 
 def rmsnorm_bf16(x, weight, out, eps=1e-6, residual=None, sum_out=None, rstd=None):
@@ -787,40 +808,46 @@ def rmsnorm_bf16(x, weight, out, eps=1e-6, residual=None, sum_out=None, rstd=Non
     (see dg_rmsnorm_bf16 in include/dg.h).  weight [H] bf16, fp32 or None;
     sum_out bf16 [T,H] receives z (may be x or residual), rstd fp32 [T] the
     factor for the backward pass.  Rows may be strided."""
-    dev = _gpu(x)
-    p, t, h = _norm(x, weight, eps, residual, sum_out, rstd, dev)
-    _bf16(out, "out"); _shape(out, (t, h), "out")
-    _check(_lib.dg_rmsnorm_bf16(ctypes.addressof(p), _ptr(out), _ld(out, dev, "out"), t, h, _stream(x)),
-           "dg_rmsnorm_bf16")
+    shape, dev = _matrix(x, "x")
+    p = _norm(x, shape, weight, eps, residual, sum_out, rstd, dev)
+    op, ldo = _rows(out, _BF16, shape, dev, "out")
+    st = _lib.dg_rmsnorm_bf16(p, op, ldo, *shape, _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_rmsnorm_bf16")
     return out
 
 
 def rmsnorm_quantize_fp8_1x128(x, weight, q, s, eps=1e-6, residual=None, sum_out=None, rstd=None):
     """rmsnorm_bf16 with its fp32 result quantised: q fp8 [T,H], s fp32
     [T,H/128], or int32 [T,ceil(H/512)] for packed UE8M0 scales."""
-    dev = _gpu(x)
-    p, t, h = _norm(x, weight, eps, residual, sum_out, rstd, dev)
-    _fp8(q, "q")
-    qp = _plain(q, (t, h), dev, "q")
-    if s.dtype == torch.int32:
-        _check(_lib.dg_rmsnorm_quantize_fp8_1x128_ue8m0(ctypes.addressof(p), qp, _plain(s, (t, (h + 511) // 512), dev, "s"),
-                                                        t, h, _stream(x)), "dg_rmsnorm_quantize_fp8_1x128_ue8m0")
+    shape, dev = _matrix(x, "x")
+    t, h = shape
+    p = _norm(x, shape, weight, eps, residual, sum_out, rstd, dev)
+    qp = _bytes8(q, shape, dev, "q")
+    if s.dtype is _I32:
+        fn, name, sp = _lib.dg_rmsnorm_quantize_fp8_1x128_ue8m0, "dg_rmsnorm_quantize_fp8_1x128_ue8m0", \
+            _whole(s, _I32, (t, (h + 511) // 512), dev, "s")
     else:
-        _check(_lib.dg_rmsnorm_quantize_fp8_1x128(ctypes.addressof(p), qp, _vector(s, (t, h // 128), dev, "s"), t, h,
-                                                  _stream(x)), "dg_rmsnorm_quantize_fp8_1x128")
+        fn, name, sp = _lib.dg_rmsnorm_quantize_fp8_1x128, "dg_rmsnorm_quantize_fp8_1x128", \
+            _whole(s, _F32, (t, h // 128), dev, "s")
+    st = fn(p, qp, sp, t, h, _stream_of(dev))
+    if st:
+        raise DGError(st, name)
     return q, s
 
 
 def rmsnorm_quantize_int8(x, weight, q, s, eps=1e-6, residual=None, sum_out=None, rstd=None):
     """rmsnorm_bf16 with its fp32 result quantised: q int8 [T,H], s fp32 [T]."""
-    dev = _gpu(x)
-    p, t, h = _norm(x, weight, eps, residual, sum_out, rstd, dev)
-    _int8(q, "q")
-    _check(_lib.dg_rmsnorm_quantize_int8(ctypes.addressof(p), _plain(q, (t, h), dev, "q"), _vector(s, (t,), dev, "s"), t,
-                                         h, _stream(x)), "dg_rmsnorm_quantize_int8")
+    shape, dev = _matrix(x, "x")
+    p = _norm(x, shape, weight, eps, residual, sum_out, rstd, dev)
+    st = _lib.dg_rmsnorm_quantize_int8(p, _whole(q, _I8, shape, dev, "q"), _whole(s, _F32, shape[:1], dev, "s"), *shape,
+                                       _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_rmsnorm_quantize_int8")
     return q, s
 
 
+@functools.lru_cache(maxsize=256)
 def rmsnorm_bf16_backward_workspace(t, h):
     """Bytes of workspace that rmsnorm_bf16_backward needs for dweight."""
     need = _i64()
@@ -834,31 +861,25 @@ def rmsnorm_bf16_backward(dout, z, weight, rstd, dx=None, dweight=None, dsum=Non
     (the gradient of x and of residual; dsum bf16 [T,H], the gradient that
     reaches sum_out from elsewhere, is added) and dweight fp32 [H] that are
     given and returns both."""
-    _bf16(dout, "dout"); _bf16(z, "z")
-    t, h = dout.shape
-    _shape(z, (t, h), "z")
-    dev = _gpu(dout)
-    wp, wt = (None, 0) if weight is None else _weight(weight, h, dev)
+    shape, dev = _matrix(dout, "dout")
+    t, h = shape
+    op, ldo = _rows(dout, _BF16, shape, dev, "dout")
+    zp, ldz = _rows(z, _BF16, shape, dev, "z")
+    wp, wt = (None, 0) if weight is None else _vector_type(weight, h, dev, "weight")
     dsp = dxp = dwp = wsp = None
     ldds = lddx = 0
     if dx is not None:
-        _bf16(dx, "dx"); _shape(dx, (t, h), "dx")
-        dxp, lddx = _ptr(dx), _ld(dx, dev, "dx")
+        dxp, lddx = _rows(dx, _BF16, shape, dev, "dx")
         if dsum is not None:
-            _bf16(dsum, "dsum"); _shape(dsum, (t, h), "dsum")
-            dsp, ldds = _ptr(dsum), _ld(dsum, dev, "dsum")
+            dsp, ldds = _rows(dsum, _BF16, shape, dev, "dsum")
     if dweight is not None:
-        dwp = _vector(dweight, (h,), dev, "dweight")
+        dwp = _whole(dweight, _F32, (h,), dev, "dweight")
         wsp = _room(workspace, rmsnorm_bf16_backward_workspace(t, h), dev, dout)
-    _check(_lib.dg_rmsnorm_bf16_backward(_ptr(dout), _ld(dout, dev, "dout"), _ptr(z), _ld(z, dev, "z"), wp, wt,
-                                         _vector(rstd, (t,), dev, "rstd"), dsp, ldds, dxp, lddx, dwp, wsp, t, h,
-                                         _stream(dout)), "dg_rmsnorm_bf16_backward")
+    st = _lib.dg_rmsnorm_bf16_backward(op, ldo, zp, ldz, wp, wt, _whole(rstd, _F32, (t,), dev, "rstd"), dsp, ldds, dxp,
+                                       lddx, dwp, wsp, t, h, _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_rmsnorm_bf16_backward")
     return dx, dweight
-
-
-def _int8(t, name):
-    if t.dtype != torch.int8:
-        raise TypeError(f"{name} must be int8, got {t.dtype}")
 
 
 def gemm_int8_nt_epilogue(lhs, rhs, out, bias=None, activation="none", residual=None, pre=None):
@@ -866,36 +887,48 @@ def gemm_int8_nt_epilogue(lhs, rhs, out, bias=None, activation="none", residual=
     [M,K], fp32 [M]), rhs = (int8 [N,K], fp32 [N]) (see
     dg_gemm_int8_nt_epilogue in include/dg.h)."""
     (a, sa), (b, sb) = lhs, rhs
-    _int8(a, "a"); _int8(b, "b")
-    m, k = a.shape
+    (m, k), dev = _matrix(a, "a")
     n = b.shape[0]
-    _shape(b, (n, k), "b")
-    dev = _gpu(a)
-    ldc = _linear_out(out, m, n, dev)
-    e = _epilogue(out, bias, activation, residual, pre, m, n, dev)
-    _check(_lib.dg_gemm_int8_nt_epilogue(_ptr(a), _ld(a, dev, "a"), _vector(sa, (m,), dev, "sa"), _ptr(b),
-                                         _ld(b, dev, "b"), _vector(sb, (n,), dev, "sb"), _ptr(out), ldc,
-                                         _TYPE[out.dtype], ctypes.addressof(e), m, n, k, _stream(a)),
-           "dg_gemm_int8_nt_epilogue")
+    ap, lda = _rows(a, _I8, (m, k), dev, "a")
+    bp, ldb = _rows(b, _I8, (n, k), dev, "b")
+    kind = _TYPE.get(out.dtype)
+    if kind is None:
+        raise TypeError(f"out must be bfloat16 or float32, got {out.dtype}")
+    cp, ldc = _rows(out, out.dtype, (m, n), dev, "out")
+    bip = bit = rp = ldr = pp = ldp = 0
+    if bias is not None:
+        bip, bit = _vector_type(bias, n, dev, "bias")
+    if residual is not None:
+        rp, ldr = _rows(residual, _BF16, (m, n), dev, "residual")
+    if pre is not None:
+        pp, ldp = _rows(pre, _BF16, (m, n), dev, "pre")
+    st = _lib.dg_gemm_int8_nt_epilogue(ap, lda, _whole(sa, _F32, (m,), dev, "sa"), bp, ldb,
+                                       _whole(sb, _F32, (n,), dev, "sb"), cp, ldc, kind,
+                                       _epilogue_fields(bip, bit, _activation(activation), rp, ldr, pp, ldp), m, n, k,
+                                       _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_gemm_int8_nt_epilogue")
     return out
 
 
 def dg_quantize_int8_rows(x, q, s):
     """x bf16 or fp32 [M,K] -> q int8 [M,K], s fp32 [M]: a scale per row (see
     include/dg.h).  x's rows may be strided."""
+    shape, dev = _matrix(x, "x")
     kind = _TYPE.get(x.dtype)
     if kind is None:
         raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
-    _int8(q, "q")
-    m, k = x.shape
-    dev = _gpu(x)
-    _check(_lib.dg_quantize_int8_rows(_ptr(x), _ld(x, dev, "x"), kind, _plain(q, (m, k), dev, "q"),
-                                      _vector(s, (m,), dev, "s"), m, k, _stream(x)), "dg_quantize_int8_rows")
+    xp, ldx = _rows(x, x.dtype, shape, dev, "x")
+    st = _lib.dg_quantize_int8_rows(xp, ldx, kind, _whole(q, _I8, shape, dev, "q"),
+                                    _whole(s, _F32, shape[:1], dev, "s"), *shape, _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_quantize_int8_rows")
     return q, s
 
 
 # ------------------------------------- tokens sorted by expert and back ---
 
+@functools.lru_cache(maxsize=256)
 def moe_sort_workspace(tokens, top_k, num_experts):
     """Bytes of workspace that moe_sort_contiguous and moe_sort_masked need."""
     need = _i64()
@@ -914,56 +947,68 @@ def moe_sort_contiguous(ids, num_experts, m_indices, rows, counts=None, workspac
     dg_moe_sort_contiguous in include/dg.h): writes m_indices int32 [M_total]
     (moe_sort_rows gives an M_total for any routing), rows int32 [T,k] and, if
     given, counts int32 [E]; returns m_indices and rows."""
-    t, k = ids.shape
-    dev = _gpu(ids)
+    shape, dev = _matrix(ids, "ids")
+    t, k = shape
     m = m_indices.shape[0]
-    cp = None if counts is None else _int32(counts, (num_experts,), dev, "counts")
-    _check(_lib.dg_moe_sort_contiguous(
-        _int32(ids, (t, k), dev, "ids"), _int32(m_indices, (m,), dev, "m_indices"), _int32(rows, (t, k), dev, "rows"), cp,
-        _room(workspace, moe_sort_workspace(t, k, num_experts), dev, ids), t, k, num_experts, m, _stream(ids)),
-        "dg_moe_sort_contiguous")
+    st = _lib.dg_moe_sort_contiguous(
+        _whole(ids, _I32, shape, dev, "ids"), _whole(m_indices, _I32, (m,), dev, "m_indices"),
+        _whole(rows, _I32, shape, dev, "rows"),
+        None if counts is None else _whole(counts, _I32, (num_experts,), dev, "counts"),
+        _room(workspace, moe_sort_workspace(t, k, num_experts), dev, ids), t, k, num_experts, m, _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_moe_sort_contiguous")
     return m_indices, rows
 
 
 def moe_sort_masked(ids, m_max, masked_m, rows, workspace=None):
     """Rows of the masked layout [E,M_max,..] for the tokens' experts ids int32
     [T,k]: writes masked_m int32 [E] and rows int32 [T,k] and returns both."""
-    t, k = ids.shape
-    dev = _gpu(ids)
+    shape, dev = _matrix(ids, "ids")
+    t, k = shape
     e = masked_m.shape[0]
-    _check(_lib.dg_moe_sort_masked(
-        _int32(ids, (t, k), dev, "ids"), _int32(masked_m, (e,), dev, "masked_m"), _int32(rows, (t, k), dev, "rows"),
-        _room(workspace, moe_sort_workspace(t, k, e), dev, ids), t, k, e, m_max, _stream(ids)), "dg_moe_sort_masked")
+    st = _lib.dg_moe_sort_masked(
+        _whole(ids, _I32, shape, dev, "ids"), _whole(masked_m, _I32, (e,), dev, "masked_m"),
+        _whole(rows, _I32, shape, dev, "rows"), _room(workspace, moe_sort_workspace(t, k, e), dev, ids), t, k, e, m_max,
+        _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_moe_sort_masked")
     return masked_m, rows
 
 
-def _layout(a, h, dev, name):
-    """(M, pointer) of a grouped layout's rows [M,H] or [E,M_max,H]."""
+def _layout(a, dtype, cols, dev, name):
+    """Pointer and row count of a grouped layout's rows [M,cols] or [E,M_max,cols]."""
     shape = a.shape
-    if len(shape) not in (2, 3) or shape[-1] != h or a.get_device() != dev or not a.is_contiguous():
-        raise ValueError(f"{name} must be contiguous [M,{h}] or [E,M_max,{h}], on the same GPU, got {tuple(shape)}")
-    return (shape[0] if len(shape) == 2 else shape[0] * shape[1]), a.data_ptr()
+    n = len(shape)
+    if n not in (2, 3) or shape[-1] != cols:
+        raise ValueError(f"{name} must be [M,{cols}] or [E,M_max,{cols}], got {tuple(shape)}")
+    return _whole(a, dtype, shape, dev, name), shape[0] if n == 2 else shape[0] * shape[1]
 
 
-def _slots(rows, dev):
-    if rows.dim() != 2:
-        raise ValueError(f"rows must be [T,k], got {tuple(rows.shape)}")
-    return rows.shape[1], _int32(rows, rows.shape, dev, "rows")
+def _slots(rows, t, dev):
+    """Pointer and width of the rows int32 [T,k] of the tokens' slots."""
+    shape = rows.shape
+    if len(shape) != 2 or shape[0] != t:
+        raise ValueError(f"rows must be [{t},k], got {tuple(shape)}")
+    return _whole(rows, _I32, shape, dev, "rows"), shape[1]
+
+
+def _optional(t, dtype, shape, dev, name):
+    return None if t is None else _whole(t, dtype, shape, dev, name)
 
 
 def moe_dispatch_bf16(x, rows, a, m_indices=None):
     """a[rows[t,j]] = x[t] for bf16 x [T,H] (see dg_moe_dispatch_bf16 in
     include/dg.h); a bf16 [M,H] or [E,M_max,H].  With m_indices (contiguous
     layout) the padding rows of the segments become zeros."""
-    _bf16(x, "x"); _bf16(a, "a")
-    t, h = x.shape
-    dev = _gpu(x)
-    m, ap = _layout(a, h, dev, "a")
-    k, rp = _slots(rows, dev)
-    _shape(rows, (t, k), "rows")
-    mi = None if m_indices is None else _int32(m_indices, (m,), dev, "m_indices")
-    _check(_lib.dg_moe_dispatch_bf16(_ptr(x), _ld(x, dev, "x"), rp, mi, ap, t, k, h, m, _stream(x)),
-           "dg_moe_dispatch_bf16")
+    shape, dev = _matrix(x, "x")
+    t, h = shape
+    xp, ldx = _rows(x, _BF16, shape, dev, "x")
+    ap, m = _layout(a, _BF16, h, dev, "a")
+    rp, k = _slots(rows, t, dev)
+    st = _lib.dg_moe_dispatch_bf16(xp, ldx, rp, _optional(m_indices, _I32, (m,), dev, "m_indices"), ap, t, k, h, m,
+                                   _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_moe_dispatch_bf16")
     return a
 
 
@@ -972,23 +1017,24 @@ def moe_dispatch_fp8(x, rows, a, m_indices=None):
     [T,H/128] or int32 [T,ceil(H/512)]), a = (fp8 [M,H] or [E,M_max,H], scales
     of the same)."""
     (q, s), (qa, sa) = x, a
-    _fp8(q, "x"); _fp8(qa, "a")
-    t, h = q.shape
-    dev = _gpu(q)
-    packed = s.dtype == torch.int32
-    if (not packed and s.dtype != torch.float32) or sa.dtype != s.dtype:
-        raise TypeError(f"scales must be float32, or int32 (packed UE8M0), in x and a: got {s.dtype} and {sa.dtype}")
-    words = (h + 511) // 512 if packed else h // 128
-    m, ap = _layout(qa, h, dev, "a")
-    m2, sap = _layout(sa, words, dev, "a's scales")
-    if m2 != m:
-        raise ValueError(f"a has {m} rows and its scales {m2}")
-    k, rp = _slots(rows, dev)
-    _shape(rows, (t, k), "rows")
-    mi = None if m_indices is None else _int32(m_indices, (m,), dev, "m_indices")
-    fn = _lib.dg_moe_dispatch_fp8_ue8m0 if packed else _lib.dg_moe_dispatch_fp8
-    _check(fn(_plain(q, (t, h), dev, "x"), _plain(s, (t, words), dev, "x's scales"), rp, mi, ap, sap, t, k, h, m,
-              _stream(q)), "dg_moe_dispatch_fp8")
+    shape, dev = _matrix(q, "x")
+    t, h = shape
+    qp = _bytes8(q, shape, dev, "x")
+    _fp8(qa, "a")
+    ap, m = _layout(qa, qa.dtype, h, dev, "a")
+    kind = s.dtype
+    if kind is _I32:
+        fn, words = _lib.dg_moe_dispatch_fp8_ue8m0, (h + 511) // 512
+    else:
+        fn, words, kind = _lib.dg_moe_dispatch_fp8, h // 128, _F32
+    sp = _whole(s, kind, (t, words), dev, "x's scales")
+    sap, ms = _layout(sa, kind, words, dev, "a's scales")
+    if ms != m:
+        raise ValueError(f"a has {m} rows and its scales {ms}")
+    rp, k = _slots(rows, t, dev)
+    st = fn(qp, sp, rp, _optional(m_indices, _I32, (m,), dev, "m_indices"), ap, sap, t, k, h, m, _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_moe_dispatch_fp8")
     return a
 
 
@@ -996,19 +1042,16 @@ def moe_combine_bf16(o, rows, out, weights=None, residual=None):
     """out[t] = residual[t] + sum_j weights[t,j] o[rows[t,j]] (see
     dg_moe_combine_bf16 in include/dg.h): o bf16 [M,H] or [E,M_max,H], weights
     fp32 [T,k] or None (ones), residual bf16 [T,H] (may be out)."""
-    _bf16(o, "o"); _bf16(out, "out")
-    t, h = out.shape
-    dev = _gpu(o)
-    m, op = _layout(o, h, dev, "o")
-    k, rp = _slots(rows, dev)
-    _shape(rows, (t, k), "rows")
-    wp = None if weights is None else _vector(weights, (t, k), dev, "weights")
-    res, ldr = None, 0
-    if residual is not None:
-        _bf16(residual, "residual"); _shape(residual, (t, h), "residual")
-        res, ldr = _ptr(residual), _ld(residual, dev, "residual")
-    _check(_lib.dg_moe_combine_bf16(op, rp, wp, res, ldr, _ptr(out), _ld(out, dev, "out"), t, k, h, m, _stream(o)),
-           "dg_moe_combine_bf16")
+    shape, dev = _matrix(out, "out")
+    t, h = shape
+    yp, ldy = _rows(out, _BF16, shape, dev, "out")
+    op, m = _layout(o, _BF16, h, dev, "o")
+    rp, k = _slots(rows, t, dev)
+    res, ldr = (None, 0) if residual is None else _rows(residual, _BF16, shape, dev, "residual")
+    st = _lib.dg_moe_combine_bf16(op, rp, _optional(weights, _F32, (t, k), dev, "weights"), res, ldr, yp, ldy, t, k, h, m,
+                                  _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_moe_combine_bf16")
     return out
 
 
@@ -1022,21 +1065,17 @@ def moe_combine_bf16_backward(dout, o, rows, weights=None, do=None, dweights=Non
     writes those of do bf16, of o's shape (may be o), and dweights fp32 [T,k]
     that are given and returns both.  With m_indices (contiguous layout) the
     padding rows of do become zeros."""
-    _bf16(dout, "dout"); _bf16(o, "o")
-    t, h = dout.shape
-    dev = _gpu(dout)
-    m, op = _layout(o, h, dev, "o")
-    k, rp = _slots(rows, dev)
-    _shape(rows, (t, k), "rows")
-    wp = None if weights is None else _vector(weights, (t, k), dev, "weights")
-    dp = None
-    if do is not None:
-        _bf16(do, "do"); _shape(do, o.shape, "do")
-        dp = _layout(do, h, dev, "do")[1]
-    dwp = None if dweights is None else _vector(dweights, (t, k), dev, "dweights")
-    mi = None if m_indices is None else _int32(m_indices, (m,), dev, "m_indices")
-    _check(_lib.dg_moe_combine_bf16_backward(_ptr(dout), _ld(dout, dev, "dout"), op, rp, wp, mi, dp, dwp, t, k, h, m,
-                                             _stream(dout)), "dg_moe_combine_bf16_backward")
+    shape, dev = _matrix(dout, "dout")
+    t, h = shape
+    dp, ldd = _rows(dout, _BF16, shape, dev, "dout")
+    op, m = _layout(o, _BF16, h, dev, "o")
+    rp, k = _slots(rows, t, dev)
+    st = _lib.dg_moe_combine_bf16_backward(
+        dp, ldd, op, rp, _optional(weights, _F32, (t, k), dev, "weights"),
+        _optional(m_indices, _I32, (m,), dev, "m_indices"), _optional(do, _BF16, o.shape, dev, "do"),
+        _optional(dweights, _F32, (t, k), dev, "dweights"), t, k, h, m, _stream_of(dev))
+    if st:
+        raise DGError(st, "dg_moe_combine_bf16_backward")
     return do, dweights
 
 

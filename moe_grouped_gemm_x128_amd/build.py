@@ -1,4 +1,5 @@
-"""Build the gfx950 HIP library (libdg_mi355x.so) in-tree with hipcc.
+"""Build the gfx950 HIP library (libdg_mi355x.so) in-tree with hipcc, and the
+binding's native helper (_tensors.so) with the host compiler.
 
     python moe_grouped_gemm_x128_amd/build.py        # or build() from Python
 
@@ -20,6 +21,8 @@ LIB = os.path.join(HERE, "libdg_mi355x.so")
 SOURCES = ["dg_api.hip", "dg_shapes.hip", "dg_kernels.hip", "dg_quant.hip", "dg_noalloc.hip", "dg_moe.hip",
            "dg_linear.hip", "dg_linear_rows.hip", "dg_linear_gemm.hip", "dg_linear_int8.hip", "dg_linear_int8_gemm.hip",
            "dg_norm.hip", "dg_moe_rows.hip"]
+TENSORS = os.path.join(HERE, "_tensors.so")
+CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -47,9 +50,34 @@ def _hipcc(args, verbose):
         raise RuntimeError(f"hipcc failed with exit code {res.returncode}")
 
 
+def build_tensors(verbose: bool = False) -> str:
+    """Compile csrc/dg_tensors.cpp against the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TENSORS + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]),
+           os.path.join(CSRC, "dg_tensors.cpp"), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"{CXX} failed with exit code {res.returncode}")
+    os.replace(tmp, TENSORS)
+    return TENSORS
+
+
 def build(verbose: bool = False, extra=None) -> str:
     """Compile every source (one hipcc each, in parallel) and link the shared
     library; always recompiles."""
+    build_tensors(verbose)
     tmp = LIB + ".tmp"
     flags = [*FLAGS, *(extra or [])]
     with tempfile.TemporaryDirectory() as objs:
