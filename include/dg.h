@@ -476,8 +476,8 @@ dg_status dg_rmsnorm_quantize_int8(const dg_norm* in, void* q, float* s, int tok
  *     dweight = sum over rows of dy z r  [H] fp32, in a fixed order
  * dx is the gradient of x and of residual.  Outputs that are null are not
  * computed.  dx may be dy, z or dsum (same stride).  workspace: the bytes that
- * dg_rmsnorm_bf16_backward_workspace returns, 16-byte aligned, the call's until
- * its kernels end (null without dweight). */
+ * dg_rmsnorm_bf16_backward_workspace returns (0 for few rows), 16-byte aligned,
+ * the call's until its kernels end; null where that is 0 or without dweight. */
 dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* z, int64_t ld_z, const void* weight,
                                    int weight_type, const float* rstd, const void* dsum, int64_t ld_dsum, void* dx,
                                    int64_t ld_dx, float* dweight, void* workspace, int tokens, int hidden,

@@ -267,6 +267,10 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
 // columns of each, so dw is a sum in its registers, written once to
 // partial[workgroup] and summed in workgroup order by a second kernel (no
 // atomics: the same inputs give the same bits).
+//
+// Few rows: dw needs nothing of the rows' sums (r is given), so workgroups of
+// their own sum its columns, beside those of the rows and in the same launch,
+// reading dy and z again from the caches: no partials, no second kernel.
 struct BackwardParams {
   const uint16_t* dy;
   const uint16_t* x;
@@ -275,14 +279,75 @@ struct BackwardParams {
   const float* rstd;
   uint16_t* dx;          // or null
   float* partial;        // or null
+  float* dw;             // few rows: or null
   int64_t lddy, ldx, ldds, lddx;
   int t, h, w_f32;
+  int columns;           // few rows: workgroups that sum columns of dw, the first ones
 };
+
+// dw's columns of `tile`: a wave takes 64 V / C rows at a time, C = 64 columns
+// (V = 8) or 32 (whole lines either way are read by the workgroups of both halves).
+template <int V>
+constexpr int kTileColumns = V == 8 ? 64 : 32;
+
+template <int V>
+__device__ __forceinline__ void sum_columns(const BackwardParams& p, int tile, float (*part)[64]) {
+  constexpr int C = kTileColumns<V>, LPR = C / V, RPW = 64 / LPR, U = V == 8 ? 4 : 8;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int c = tile * C + (lane % LPR) * V;
+  const int step = waves * RPW;
+  float dw[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) dw[e] = 0.f;
+  // (columns past the last are read from the last ones again and dropped)
+  const int cl = c + V <= p.h ? c : p.h - V;
+  for (int r0 = wave * RPW + lane / LPR; r0 < p.t; r0 += step * U) {
+    Raw<V> x[U], d[U];
+    float r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = min(r0 + u * step, p.t - 1);
+      x[u] = load<V>(p.x + row * p.ldx + cl);
+      d[u] = load<V>(p.dy + row * p.lddy + cl);
+      r[u] = p.rstd[row];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float z[V], g[V];
+      widen<V>(x[u], z);
+      widen<V>(d[u], g);
+      if (r0 + u * step < p.t) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) dw[e] = __builtin_fmaf(g[e], z[e] * r[u], dw[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = LPR; m < 64; m *= 2)
+#pragma unroll
+    for (int e = 0; e < V; ++e) dw[e] += __shfl_xor(dw[e], m, 64);
+  if (lane < LPR) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) part[wave][lane * V + e] = dw[e];
+  }
+  __syncthreads();
+  if (tid < C && tile * C + tid < p.h) {
+    float v = part[0][tid];
+    for (int w = 1; w < waves; ++w) v += part[w][tid];
+    p.dw[tile * C + tid] = v;
+  }
+}
 
 template <int V, int I>
 __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams p) {
   __shared__ float part[2][8];
+  __shared__ float columns[8][64];
+  if ((int)blockIdx.x < p.columns) {
+    sum_columns<V>(p, blockIdx.x, columns);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int group = blockIdx.x - p.columns, groups = gridDim.x - p.columns;
   float w[I][V], dw[I][V];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
@@ -292,7 +357,7 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
     if (c < p.h) load_weight<V>(p.w, p.w_f32, c, w[i]);
   }
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < p.t; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = group; row < p.t; row += groups, turn ^= 1) {
     float z[I][V], d[I][V];
     Raw<V> ds[I];
     const float r = p.rstd[row];
@@ -320,7 +385,7 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
         }
       }
     }
-    if (!p.dx) continue;  // (uniform over the workgroup)
+    if (!p.dx) continue;  // (for dw alone; uniform over the workgroup)
     dot = sum64(dot);
     if (waves > 1) {
       // (two sets: a wave writes its next row's while others still read this one's)
@@ -351,7 +416,7 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
     for (int i = 0; i < I; ++i) {
       const int c = (i * blockDim.x + tid) * V;
       if (c < p.h) {
-        float* q = p.partial + (int64_t)blockIdx.x * p.h + c;
+        float* q = p.partial + (int64_t)group * p.h + c;
 #pragma unroll
         for (int e = 0; e < V; ++e) q[e] = dw[i][e];
       }
@@ -479,6 +544,21 @@ dg_status fp8(const dg_norm* in, void* q, void* s, int t, int h, bool ue8m0, hip
 // written and read again), so there are at most 512 of them.
 int backward_parts(int t) { return t < 512 ? t : 512; }
 
+// Whether the memory of two matrices' rows may meet.
+bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int t, int h) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + 2 * ((uintptr_t)(t - 1) * ldb + h) && b0 < a0 + 2 * ((uintptr_t)(t - 1) * lda + h);
+}
+
+// Few rows: dw's columns are summed beside the rows.  A tile's rows are read by
+// one workgroup, so the time grows with them, while the partials' way pays a
+// second launch and their traffic (us beside : by partials): 17 x 1161 3.3 : 5.8,
+// 512 x 4096 5.8 : 11.6, 1000 x 2111 9.6 : 14.3, 1024 x 4096 13.9 : 12.7, 2048 x
+// 2048 21.6 : 12.2.
+constexpr int kFewRows = 768;
+constexpr int64_t kFewValues = 8 << 20;  // dy and z are read twice: 32 MB of them stay in the caches
+bool few(int t, int h) { return t <= kFewRows && (int64_t)t * h <= kFewValues; }
+
 }  // namespace
 }  // namespace dg
 
@@ -524,7 +604,7 @@ dg_status dg_rmsnorm_quantize_int8(const dg_norm* in, void* q, float* s, int tok
 
 dg_status dg_rmsnorm_bf16_backward_workspace(int tokens, int hidden, int64_t* bytes) {
   if (!bytes || tokens <= 0 || hidden <= 0) return DG_ERROR_INVALID_VALUE;
-  *bytes = 4 * (int64_t)backward_parts(tokens) * hidden;
+  *bytes = few(tokens, hidden) ? 0 : 4 * (int64_t)backward_parts(tokens) * hidden;
   return DG_SUCCESS;
 }
 
@@ -534,12 +614,14 @@ dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x,
                                    hipStream_t stream) {
   const int t = tokens, h = hidden;
   if (!dy || !x || !rstd || t <= 0 || h <= 0 || ld_dy < h || ld_x < h || (dx && ld_dx < h) ||
-      (dx && dsum && ld_dsum < h) || bad_weight(weight, weight_type) || (dweight && !workspace))
+      (dx && dsum && ld_dsum < h) || bad_weight(weight, weight_type) ||
+      (dweight && !few(t, h) && !workspace))
     return DG_ERROR_INVALID_VALUE;
+  const bool beside = dweight && few(t, h);
   const bool with_dsum = dx && dsum;
   if (h > kMaxHidden || unfit_rows(dy, ld_dy) || unfit_rows(x, ld_x) || (dx && unfit_rows(dx, ld_dx)) ||
       (with_dsum && unfit_rows(dsum, ld_dsum)) || unfit_weight(weight, weight_type) || !aligned(rstd, 4) ||
-      !aligned(dweight, 4) || (dweight && !aligned(workspace, 16)))
+      !aligned(dweight, 4) || (dweight && !beside && !aligned(workspace, 16)))
     return DG_ERROR_UNSUPPORTED;
   if (!dx && !dweight) return DG_SUCCESS;
   BackwardParams p{};
@@ -550,7 +632,8 @@ dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x,
   p.w_f32 = weight_type == DG_TYPE_F32;
   p.rstd = rstd;
   p.dx = static_cast<uint16_t*>(dx);
-  p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+  p.partial = dweight && !beside ? static_cast<float*>(workspace) : nullptr;
+  p.dw = beside ? dweight : nullptr;
   p.lddy = ld_dy;
   p.ldx = ld_x;
   p.ldds = ld_dsum;
@@ -559,21 +642,35 @@ dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x,
   p.h = h;
   const bool vec = h % 8 == 0 && rows8(dy, ld_dy, t) && rows8(x, ld_x, t) && (!dx || rows8(dx, ld_dx, t)) &&
                    (!with_dsum || rows8(dsum, ld_dsum, t)) && (!weight || aligned(weight, 16));
-  const Shape s = shape_of(h, vec);
+  Shape s = shape_of(h, vec);
   const int parts = backward_parts(t);
+  int grid = parts;
   (void)hipGetLastError();
   hipError_t e;
+  if (beside) {
+    const int columns = ceil_div(h, vec ? kTileColumns<8> : kTileColumns<1>);
+    p.columns = columns;
+    s.waves = 8;  // (the rows' workgroups too, where they share the launch)
+    grid = columns + (dx ? t : 0);
+    if (dx && (overlap(dx, ld_dx, dy, ld_dy, t, h) || overlap(dx, ld_dx, x, ld_x, t, h))) {
+      // dx over what dw's columns are summed from: those first, in a launch of their own
+      e = vec ? launch_backward<8, 1>(p, columns, 8, stream) : launch_backward<1, 4>(p, columns, 8, stream);
+      if (e != hipSuccess) return DG_ERROR_LAUNCH;
+      p.columns = 0;
+      grid = t;
+    }
+  }
   if (vec)
-    e = s.pieces == 1   ? launch_backward<8, 1>(p, parts, s.waves, stream)
-        : s.pieces == 2 ? launch_backward<8, 2>(p, parts, s.waves, stream)
-                        : launch_backward<8, 4>(p, parts, s.waves, stream);
+    e = s.pieces == 1   ? launch_backward<8, 1>(p, grid, s.waves, stream)
+        : s.pieces == 2 ? launch_backward<8, 2>(p, grid, s.waves, stream)
+                        : launch_backward<8, 4>(p, grid, s.waves, stream);
   else
-    e = s.pieces == 4   ? launch_backward<1, 4>(p, parts, s.waves, stream)
-        : s.pieces == 8 ? launch_backward<1, 8>(p, parts, s.waves, stream)
-        : s.pieces == 16 ? launch_backward<1, 16>(p, parts, s.waves, stream)
-                        : launch_backward<1, 32>(p, parts, s.waves, stream);
+    e = s.pieces == 4   ? launch_backward<1, 4>(p, grid, s.waves, stream)
+        : s.pieces == 8 ? launch_backward<1, 8>(p, grid, s.waves, stream)
+        : s.pieces == 16 ? launch_backward<1, 16>(p, grid, s.waves, stream)
+                        : launch_backward<1, 32>(p, grid, s.waves, stream);
   if (e != hipSuccess) return DG_ERROR_LAUNCH;
-  if (dweight) {
+  if (p.partial) {
     norm_weight_sum_kernel<<<ceil_div(h, 64), 1024, 0, stream>>>(p.partial, dweight, parts, h);
     if (hipGetLastError() != hipSuccess) return DG_ERROR_LAUNCH;
   }

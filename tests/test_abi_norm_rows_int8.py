@@ -100,13 +100,13 @@ def backward(lib, dy=P, lddy=256, z=P, ldz=256, w=P, wt=F32, rstd=P, dsum=P, ldd
 
 
 @pytest.mark.parametrize("kw", [dict(dy=NONE), dict(z=NONE), dict(rstd=NONE), dict(t=0), dict(h=-1), dict(lddy=255),
-                                dict(ldz=1), dict(lddx=128), dict(ldds=255), dict(wt=3), dict(ws=NONE)])
+                                dict(ldz=1), dict(lddx=128), dict(ldds=255), dict(wt=3), dict(ws=NONE, t=5000)])
 def test_norm_backward_invalid(lib, kw):
     assert backward(lib, **kw) == INVALID
 
 
 @pytest.mark.parametrize("kw", [dict(dy=P + 1), dict(z=P + 1), dict(rstd=P + 1), dict(dsum=P + 1), dict(dx=P + 1),
-                                dict(dw=P + 2), dict(ws=P + 4), dict(w=P + 2),
+                                dict(dw=P + 2), dict(ws=P + 4, t=5000), dict(w=P + 2),
                                 dict(h=1 << 15, lddy=1 << 15, ldz=1 << 15, ldds=1 << 15, lddx=1 << 15)])
 def test_norm_backward_unsupported(lib, kw):
     assert backward(lib, **kw) == UNSUPPORTED
@@ -122,8 +122,9 @@ def test_norm_backward_workspace(lib):
     assert lib.dg_rmsnorm_bf16_backward_workspace(0, 4, ctypes.byref(need)) == INVALID
     assert lib.dg_rmsnorm_bf16_backward_workspace(4, -1, ctypes.byref(need)) == INVALID
     assert lib.dg_rmsnorm_bf16_backward_workspace(4, 4, None) == INVALID
+    assert lib.dg_rmsnorm_bf16_backward_workspace(3, 100, ctypes.byref(need)) == OK and need.value == 0
     last = 0
-    for t, h in ((1, 1), (3, 100), (600, 1000), (600000, 16384)):
+    for t, h in ((5000, 1), (6000, 1000), (600000, 16384)):
         assert lib.dg_rmsnorm_bf16_backward_workspace(t, h, ctypes.byref(need)) == OK
         assert need.value >= 4 * h and need.value > last
         last = need.value

@@ -155,11 +155,11 @@ def test_strided_rows_and_their_neighbours(dg, h, stride, offset):
     within(q.to(F64) * s.to(F64)[:, None], y, 0.5 * s.to(F64)[:, None] + 2.0 ** -15 * y.abs(), "codes")
 
 
-@pytest.mark.parametrize("h", [384, 2111])
-def test_outputs_over_inputs(dg, h):
+@pytest.mark.parametrize("t,h", [(21, 384), (21, 2111), (768, 264), (1600, 2000)])
+def test_outputs_over_inputs(dg, t, h):
     """The residual stream in place, y over x; and the backward pass over each of its inputs."""
-    say(f"norm in place {h}")
-    x, r, w = inputs(21, h, True, F32, 4)
+    say(f"norm in place {t}x{h}")
+    x, r, w = inputs(t, h, True, F32, 4)
     want, total = torch.empty_like(x), torch.empty_like(x)
     dg.rmsnorm_bf16(x, w, want, 1e-6, r, total)
     for which in ("residual", "x"):
@@ -168,7 +168,7 @@ def test_outputs_over_inputs(dg, h):
         dg.rmsnorm_bf16(xc, w, out, 1e-6, rc, sum_out)
         assert torch.equal(sum_out, total) and torch.equal(out, want), which
     rstd = torch.rsqrt(total.float().square().mean(1) + 1e-6)
-    dy, ds = inputs(21, h, True, None, 5)[:2]
+    dy, ds = inputs(t, h, True, None, 5)[:2]
     dx, dw = torch.empty_like(x), torch.empty(h, device="cuda")
     dg.rmsnorm_bf16_backward(dy, total, w, rstd, dx, dw, ds)
     for which in range(3):
@@ -236,7 +236,8 @@ def backward64(dy, z, w, r, ds):
     return dx, slack + 2.0 ** -8 * dx.abs(), (dy * n).sum(0), 2.0 ** -17 * (dy * n).abs().sum(0)
 
 
-@pytest.mark.parametrize("t,h", SIZES + [(513, 264), (1500, 65), (600, 4096)])
+@pytest.mark.parametrize("t,h", SIZES + [(513, 264), (1500, 65), (600, 4096), (768, 72), (769, 72), (700, 12000),
+                                             (5000, 256), (777, 33), (130, 999)])
 @pytest.mark.parametrize("ds,weight", [(True, F32), (False, BF16), (True, None)])
 def test_backward(dg, t, h, ds, weight):
     say(f"norm backward {t}x{h} dsum={ds} weight={weight}")
@@ -293,16 +294,15 @@ def test_backward_against_differences(dg):
         assert abs(got - diff) <= (bx * ez.abs()).sum() + (bw * ew.abs()).sum() + 1e-5
 
 
-@pytest.mark.parametrize("h", [512, 777])
-def test_captured_and_replayed(dg, h):
-    say(f"norm captured {h}")
-    t = 40
+@pytest.mark.parametrize("t,h", [(40, 512), (40, 777), (1100, 512)])
+def test_captured_and_replayed(dg, t, h):
+    say(f"norm captured {t}x{h}")
     x, r, w = inputs(t, h, True, F32, 16)
     dy, ds, _ = inputs(t, h, True, None, 17)
     q, s = torch.empty((t, h), dtype=torch.int8, device="cuda"), torch.empty(t, device="cuda")
     total, y, dx = (torch.empty((t, h), dtype=BF16, device="cuda") for _ in range(3))
     rstd, dw = torch.empty(t, device="cuda"), torch.empty(h, device="cuda")
-    ws = torch.empty(dg.rmsnorm_bf16_backward_workspace(t, h), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(1, dg.rmsnorm_bf16_backward_workspace(t, h)), dtype=torch.uint8, device="cuda")
 
     def step():
         dg.rmsnorm_quantize_int8(x, w, q, s, 1e-6, r, total)
@@ -352,7 +352,8 @@ def test_refusals_of_the_binding(dg):
     with pytest.raises(TypeError):
         dg.rmsnorm_quantize_int8(x, w, q.view(torch.uint8), s)
     with pytest.raises(ValueError):
-        dg.rmsnorm_bf16_backward(x, r, w, s, out, torch.empty(256, device="cuda"),
+        many = torch.empty((5000, 256), dtype=BF16, device="cuda")
+        dg.rmsnorm_bf16_backward(many, many, w, torch.ones(5000, device="cuda"), None, torch.empty(256, device="cuda"),
                                  workspace=torch.empty(16, device="cuda"))
     with pytest.raises(dg.DGError):
         dg.rmsnorm_bf16(x, w, out, -1.0)
