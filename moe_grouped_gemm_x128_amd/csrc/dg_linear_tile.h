@@ -72,8 +72,11 @@ struct Scales {
 };
 
 // One operand's share of the tile: BX rows of C (or columns), stored K
-// contiguous (TR = false) or transposed.
-template <int BX, int WX, int NW, bool TR>
+// contiguous (TR = false) or transposed.  PAIRS: a half's fragments are chunks
+// 2 lq + s instead of lq + 4 s (any order of K that both operands share): no
+// bank conflicts, against 22% of the cycles in SQ_LDS_BANK_CONFLICT (INT8; with
+// the loads spread 1 to 3% faster).
+template <int BX, int WX, int NW, bool TR, bool PAIRS>
 struct Operand {
   static constexpr int kBytes = BX * 128;                    // LDS bytes per stage
   static constexpr int kPieces = BX / 8;                     // 1 KB loads per stage
@@ -107,7 +110,7 @@ struct Operand {
     if constexpr (!TR) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
-        off[s] = (uint32_t)((wx * WTX + l16) * 128 + (((4 * s + lq) ^ swz(l16)) << 4));
+        off[s] = (uint32_t)((wx * WTX + l16) * 128 + (((PAIRS ? 2 * lq + s : 4 * s + lq) ^ swz(l16)) << 4));
     } else {
       const int h = hsw<RB>(8 * lq + (l16 >> 2));  // the same for all rows that this lane addresses
 #pragma unroll
@@ -132,6 +135,22 @@ struct Operand {
     const uint32_t v = TR || 8 * chunk < kv ? voff : kOut;
 #pragma unroll
     for (int q = 0; q < kQ; ++q) dma::load16(lds + (wave + NW * q) * 1024, r, v + q * step);
+  }
+
+  // The same (K contiguous) to be issued one by one.
+  struct Block {
+    v4i r;
+    uint32_t v, lds;
+  };
+  __device__ __forceinline__ Block block(const uint8_t* base, int64_t ld, int rows, int left, uint32_t lds,
+                                         int wave) const {
+    const int kv = min(left, 64);
+    const uint32_t bytes =
+        left > 0 && rows > 0 ? (uint32_t)(min(rows, BX) - 1) * (uint32_t)ld + 2u * ((kv + 7) & ~7) : 0u;
+    return Block{dma::resource(base, bytes), 8 * chunk < kv ? voff : kOut, lds + wave * 1024};
+  }
+  __device__ __forceinline__ void load(const Block& b, int q) const {
+    dma::load16(b.lds + NW * q * 1024, b.r, b.v + q * step);
   }
 
   // Fragment i of half s from the stage at LDS address `lds`.
@@ -164,8 +183,8 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
                                           const Scales& scales = Scales{}) {
   using Acc = std::conditional_t<INT8, v4i, v4f>;
   constexpr int NW = WM * WN;  // waves of a group
-  using OpA = Operand<BM, WM, NW, TA>;
-  using OpB = Operand<BN, WN, NW, TB>;
+  using OpA = Operand<BM, WM, NW, TA, INT8>;
+  using OpB = Operand<BN, WN, NW, TB, INT8>;
   constexpr int FM = OpA::F, FN = OpB::F;
   constexpr int PART = OpA::kBytes + OpB::kBytes;  // a group's share of a stage
   constexpr int STAGE = WK * PART;
@@ -182,7 +201,8 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
   // LDS that a wave's sums pass through, and (WK > 1) its rows that others finish
   constexpr int kRows = 16 * RS, kGiven = (FM - FR) * FN * 1024;
   static_assert(kOwnRows || (kRows <= PART / NW && kGiven <= PART / NW), "a wave's rows fit its share of the slot");
-  static_assert((S - 2) * LOADS + 2 * kStores < 64, "vmcnt range");
+  constexpr int kCounted = (S - 2) * LOADS + 2 * kStores < 64 ? 2 : 1;  // kStores that a wait may leave in flight
+  static_assert((S - 2) * LOADS + kCounted * kStores < 64, "vmcnt range");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = (int)uniform((tid >> 6) % NW), wk = WK == 1 ? 0 : (int)uniform((tid >> 6) / NW);
@@ -242,10 +262,7 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
     pa = p.a + (TA ? k0 * p.lda + 2 * li.m0 : (int64_t)li.m0 * p.lda + 2 * k0);
     pb = p.b + (TB ? k0 * p.ldb + 2 * li.n0 : (int64_t)li.n0 * p.ldb + 2 * k0);
   };
-  auto issue = [&](int slot) {
-    const uint32_t st = uniform(lds0 + slot * STAGE);
-    oa.issue(pa, p.lda, (TA ? p.wa : p.m) - li.m0, left - 64 * wk, st, wave);
-    ob.issue(pb, p.ldb, (TB ? p.wb : p.n) - li.n0, left - 64 * wk, st + OpA::kBytes, wave);
+  auto advance = [&]() {
     left -= 64 * WK;
     if (left <= 0) {
       if (li.live) enter();
@@ -253,6 +270,12 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
       pa += WK * (TA ? 64 * p.lda : 128);
       pb += WK * (TB ? 64 * p.ldb : 128);
     }
+  };
+  auto issue = [&](int slot) {
+    const uint32_t st = uniform(lds0 + slot * STAGE);
+    oa.issue(pa, p.lda, (TA ? p.wa : p.m) - li.m0, left - 64 * wk, st, wave);
+    ob.issue(pb, p.ldb, (TB ? p.wb : p.n) - li.n0, left - 64 * wk, st + OpA::kBytes, wave);
+    advance();
   };
 
   int ct = wg;
@@ -281,13 +304,38 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
 #pragma unroll
       for (int i = 0; i < FN; ++i) fb[set][i] = ob.frag(lds0 + slot * STAGE + OpA::kBytes, i, s);
     };
-    auto multiply = [&](int set, int slot, int s) {
-      read_b(set ^ 1, slot, s);
+    // INT8: the fences keep a fragment's read right behind the last product that
+    // needs the old one (left to itself the compiler gathers the reads where
+    // their registers spill, or moves them behind the barrier), and the next
+    // block's loads go out one row of products apart instead of all at once
+    // behind the barrier.  (4096 x 7168 x 4096: 138 us without either, 136 with
+    // the fences, 128 with both.)
+    typename OpA::Block next_a;
+    typename OpB::Block next_b;
+    auto multiply = [&](int set, int slot, int s, bool spread = false) {
+      if constexpr (!INT8) read_b(set ^ 1, slot, s);
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
 #pragma unroll
         for (int i = 0; i < FN; ++i) acc[i][j] = mfma(fb[set][i], fa[j], acc[i][j]);
+        if constexpr (INT8) __builtin_amdgcn_sched_barrier(0);
         fa[j] = oa.frag(lds0 + slot * STAGE, j, s);
+        if constexpr (INT8) {
+#pragma unroll
+          for (int i = j * FN / FM; i < (j + 1) * FN / FM; ++i)
+            fb[set ^ 1][i] = ob.frag(lds0 + slot * STAGE + OpA::kBytes, i, s);
+          __builtin_amdgcn_sched_barrier(0);
+          if (spread) {
+#pragma unroll
+            for (int l = j * LOADS / FM; l < (j + 1) * LOADS / FM; ++l) {
+              if (l < OpA::kQ)
+                oa.load(next_a, l);
+              else
+                ob.load(next_b, l - OpA::kQ);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
       }
     };
     read_b(0, q, 0);
@@ -305,17 +353,25 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
       // stores are younger than the blocks that were loaded before them)
       if (kb < kBehind && stores == 1)
         dma::wait<(S - 2) * LOADS + kStores>();
-      else if (kb < kBehind && stores == 2)
-        dma::wait<(S - 2) * LOADS + 2 * kStores>();
+      else if (kCounted == 2 && kb < kBehind && stores == 2)
+        dma::wait<(S - 2) * LOADS + kCounted * kStores>();
       else
         dma::wait<(S - 2) * LOADS>();
       dma::barrier();
-      if (kOwnRows || kb + 1 < nkb) issue(q);
+      constexpr bool kSpread = INT8 && kOwnRows;
+      if constexpr (kSpread) {
+        const uint32_t st = uniform(lds0 + q * STAGE);
+        next_a = oa.block(pa, p.lda, p.m - li.m0, left - 64 * wk, st, wave);
+        next_b = ob.block(pb, p.ldb, p.n - li.n0, left - 64 * wk, st + OpA::kBytes, wave);
+      } else {
+        if (kOwnRows || kb + 1 < nkb) issue(q);
+      }
       const int done = q;
       q = q + 1 == S ? 0 : q + 1;
       // (after the item's last block this reads the next item's first fragments,
       // which are read again behind the epilogue: one form of the loop's body)
-      multiply(1, q, 0);
+      multiply(1, q, 0, kSpread);
+      if constexpr (kSpread) advance();
       last = done;
     }
 
@@ -546,7 +602,7 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
         issue(last);
       }
       const int per = !LINES ? 0 : (ep.out_f32 ? 2 : 1) + (ep.pre ? 1 : 0);
-      stores = per <= 2 ? per : 0;
+      stores = per <= kCounted ? per : 0;
     }
     cur = next(ct);
   }
