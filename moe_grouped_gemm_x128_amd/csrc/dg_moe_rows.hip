@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const SortPara
 
 // ---- 16 bytes per lane ----
 // Rows that are gathered are read once, with the nontemporal cache policy (the
-// gradients of 4096 x 8 rows of 8 KB: 183 -> 169 us).  Rows that are scattered
+// gradients of 4096 x 8 rows of 8 KB: 179 -> 168 us).  Rows that are scattered
 // are written with it from 256 MB on, the size of the last cache, which
 // would keep none of them for the GEMM that reads them (470 MB: 108 -> 88 us, with
 // that GEMM 753 -> 729); fewer are left in the caches (59 MB, with the GEMM: 184 us,
@@ -251,6 +251,7 @@ __device__ __forceinline__ void store16(void* p, const uint4& v) {
 // (a segment starts on a block of 128 with at least one row: a block whose first
 // row is taken belongs to a segment, and its rows of -1 are the padding)
 constexpr int kPadRows = 32;  // rows of a block per workgroup
+template <bool STREAM>
 __device__ void zero_padding(const int32_t* m_indices, int group, int groups, int64_t m, uint8_t* a, int64_t row_bytes,
                              uint8_t* sa, int scale_bytes) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
@@ -258,7 +259,7 @@ __device__ void zero_padding(const int32_t* m_indices, int group, int groups, in
     if (m_indices[r0 / kSegment * kSegment] < 0) continue;
     for (int64_t r = r0 + wave; r < r0 + kPadRows; r += waves) {
       if (m_indices[r] >= 0) continue;
-      for (int64_t b = lane * 16; b < row_bytes; b += 1024) store16<false>(a + r * row_bytes + b, uint4{0, 0, 0, 0});
+      for (int64_t b = lane * 16; b < row_bytes; b += 1024) store16<STREAM>(a + r * row_bytes + b, uint4{0, 0, 0, 0});
       for (int b = lane * 4; b < scale_bytes; b += 256) *reinterpret_cast<uint32_t*>(sa + r * scale_bytes + b) = 0;
     }
   }
@@ -282,7 +283,7 @@ struct DispatchParams {
 template <bool STREAM>
 __global__ __launch_bounds__(256) void dispatch_kernel(const DispatchParams p) {
   if ((int)blockIdx.x >= p.copies) {
-    zero_padding(p.m_indices, blockIdx.x - p.copies, gridDim.x - p.copies, p.m, p.a, p.row_bytes, p.sa, p.scale_bytes);
+    zero_padding<STREAM>(p.m_indices, blockIdx.x - p.copies, gridDim.x - p.copies, p.m, p.a, p.row_bytes, p.sa, p.scale_bytes);
     return;
   }
   const int lane = threadIdx.x & 63;
@@ -294,18 +295,22 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const DispatchParams p) {
     const uint8_t* x = p.x + token * p.ldx;
     const int at = piece * 1024 + lane * 16;
     const bool in = at < p.row_bytes;
-    uint4 v{0, 0, 0, 0};
-    if (in) v = load16(x + at);
     // (the rows of the token's slots, one per lane)
     const int32_t own = lane < p.top_k ? p.rows[token * p.top_k + lane] : -1;
+    uint4 v{0, 0, 0, 0};
+    if (in) v = load16(x + at);
+    // the first piece's wave moves the scales too, 256 bytes at a time
+    const uint8_t* s = p.s + token * p.scale_bytes + lane * 4;
+    const int scales = piece == 0 ? p.scale_bytes - lane * 4 : 0;  // bytes from this lane's word on
+    uint32_t first = 0;
+    if (scales > 0) first = *reinterpret_cast<const uint32_t*>(s);
     for (int j = 0; j < p.top_k; ++j) {
       const int64_t row = __builtin_amdgcn_readlane(own, j);
       if (row < 0 || row >= p.m) continue;
       if (in) store16<STREAM>(p.a + row * p.row_bytes + at, v);
-      if (piece == 0)
-        for (int b = lane * 4; b < p.scale_bytes; b += 256)
-          *reinterpret_cast<uint32_t*>(p.sa + row * p.scale_bytes + b) =
-              *reinterpret_cast<const uint32_t*>(p.s + token * p.scale_bytes + b);
+      uint8_t* sa = p.sa + row * p.scale_bytes + lane * 4;
+      if (scales > 0) *reinterpret_cast<uint32_t*>(sa) = first;
+      for (int b = 256; b < scales; b += 256) *reinterpret_cast<uint32_t*>(sa + b) = *reinterpret_cast<const uint32_t*>(s + b);
     }
   }
 }
@@ -400,7 +405,7 @@ template <int K, bool STREAM>
 __global__ __launch_bounds__(512) void combine_backward_kernel(const CombineBackwardParams p) {
   __shared__ float part[2][8][kMaxTopK];
   if ((int)blockIdx.x >= p.copies) {
-    zero_padding(p.m_indices, blockIdx.x - p.copies, gridDim.x - p.copies, p.m, reinterpret_cast<uint8_t*>(p.dout),
+    zero_padding<STREAM>(p.m_indices, blockIdx.x - p.copies, gridDim.x - p.copies, p.m, reinterpret_cast<uint8_t*>(p.dout),
                  2 * (int64_t)p.h, nullptr, 0);
     return;
   }

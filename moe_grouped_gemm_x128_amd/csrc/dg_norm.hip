@@ -431,7 +431,7 @@ __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(const float* part
   const int c = blockIdx.x * 64 + lane, per = (parts + 15) / 16;
   float v = 0.f;
   if (c < h) {
-#pragma unroll 8
+#pragma unroll 16
     for (int k = wave * per; k < min(parts, (wave + 1) * per); ++k) v += partial[(int64_t)k * h + c];
   }
   sum[wave][lane] = v;
