@@ -435,7 +435,8 @@ dg_status dg_moe_few_tokens_bf16(const void* x, const float* logits, int32_t* id
  * Rows are strided: ld_x, ld_residual, ... are the elements between the starts
  * of two rows (at least H).  sum may be x or residual, and y may be any of the
  * three (with the same stride); no other overlap.  A row must keep its sum of
- * squares finite in fp32: one that does not (or holds a NaN) gets NaN scales. */
+ * squares finite in fp32: one that does not (or holds a NaN) gets NaN scales.
+ * The weight must be finite, and a scale's largest |y| 0 or at least 2^-140. */
 typedef struct {
   const void* x;        /* [T,H] bf16                                        */
   int64_t ld_x;

@@ -735,6 +735,7 @@ def _device_stream(dev):
 
 
 _stream_of = _raw_stream or _device_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _refuse(t, dtype, shape, dev, name):
@@ -773,7 +774,10 @@ def _matrix(t, name):
         raise ValueError("tensors must live on the GPU")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    return t.shape, t.get_device()
+    dev = t.get_device()
+    if dev != _current_device():  # (the default stream is the current GPU's)
+        raise ValueError(f"{name} is on GPU {dev}, which is not the current one: call under torch.cuda.device({dev})")
+    return t.shape, dev
 
 
 def _room(workspace, need, dev, like):

@@ -360,3 +360,17 @@ def test_refusals_of_the_binding(dg):
     with pytest.raises(dg.DGError):
         dg.rmsnorm_quantize_fp8_1x128(x[:, 1:129], None, q[:, :128].contiguous().view(torch.uint8),
                                       torch.empty((4, 1), device="cuda"))
+
+
+def test_another_gpu_than_the_current_one(dg, monkeypatch):
+    """The default stream is the current GPU's: tensors of another one are refused."""
+    x, out = inputs(4, 256, False, None)[0], torch.empty((4, 256), dtype=BF16, device="cuda")
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    q, s = torch.zeros((4, 256), dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    monkeypatch.setattr(dg, "_current_device", lambda: 1)
+    for call in (lambda: dg.rmsnorm_bf16(x, None, out), lambda: dg.rmsnorm_bf16_backward(x, x, None, s, out),
+                 lambda: dg.gemm_int8_nt_epilogue((q, s), (q, s), torch.empty((4, 4), device="cuda")),
+                 lambda: dg.quantize_int8_rows(x), lambda: dg.moe_sort_masked(ids, 8, ids[0], ids),
+                 lambda: dg.moe_dispatch_bf16(x, ids, out), lambda: dg.moe_combine_bf16(out, ids, x)):
+        with pytest.raises(ValueError, match="not the current one"):
+            call()
