@@ -7,9 +7,12 @@
 // A workgroup of W waves owns a row and keeps it in registers: a thread holds V
 // consecutive columns (8, or 1 where rows do not start on 16-byte boundaries)
 // of each of I pieces of the row, so x and the residual are read once and z, y
-// are written once, and one barrier separates them.  INT8's scale needs the
-// row's largest |y| too: max |z w| is met at the same barrier as sum z^2 and
-// multiplied by r after it.
+// are written once, and one barrier separates them.  A short row (heads: H <=
+// 512) belongs to L lanes of a wave instead, several rows to a wave, without LDS or
+// barrier (131072 rows of 128: 34 us with a wave each).  INT8's scale needs
+// the row's largest |y| too: max |z w| is met at the same barrier as sum z^2 and
+// multiplied by r after it.  Bound by HBM: 4096 x 7168 with a residual into FP8 is
+// 206 MB in 45 us, 4.6 TB/s, where a copy reaches 5.1.
 #include <initializer_list>
 
 #include "dg_bf16.h"
@@ -115,33 +118,67 @@ __device__ __forceinline__ float max16(float v) {  // over a row of 16 lanes, in
   v = fmaxf(v, round16<2>(v));
   return fmaxf(v, round16<1>(v));
 }
-__device__ __forceinline__ float max64(float v) {
+// The same over the L lanes of a row (0: over the wave).
+template <int L>
+__device__ __forceinline__ float max_row(float v) {
   v = max16(v);
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+  if constexpr (L != 16) v = fmaxf(v, __shfl_xor(v, 16, 64));
+  if constexpr (L == 64 || L == 0) v = fmaxf(v, __shfl_xor(v, 32, 64));
+  return v;
 }
-__device__ __forceinline__ float sum64(float v) {
+template <int L>
+__device__ __forceinline__ float sum_row(float v) {
   v += round16<8>(v);
   v += round16<4>(v);
   v += round16<2>(v);
   v += round16<1>(v);
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  if constexpr (L != 16) v += __shfl_xor(v, 16, 64);
+  if constexpr (L == 64 || L == 0) v += __shfl_xor(v, 32, 64);
+  return v;
 }
 
-template <int OUT, int V, int I>
+// ---- scales ----
+// amax / most as a product and 1 / s by the reciprocal unit: y / s is within
+// 2^-21 of exact, and 2 instructions instead of two divisions' forty (every lane
+// of a group computes them).  |y| <= amax, so no code needs a clamp.  A scale
+// below 2^-60 is raised by 2^64, y alike, so that the reciprocal stays finite.
+struct Factor {
+  float s, k, r;
+};
+__device__ __forceinline__ Factor factor_of(float amax, float inv_most) {
+  const float s = amax == 0.f ? 1.f : amax * inv_most;
+  const float k = s < 0x1p-60f ? 0x1p64f : 1.f;
+  return Factor{s, k, __builtin_amdgcn_rcpf(s * k)};
+}
+// The least E with 2^(E - 127) >= amax / 448 = amax / (1.75 2^8), read off amax's
+// fields, and 2^(127 - E).
+__device__ __forceinline__ uint32_t power_of(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  if (b == 0) return 127;
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(e, 0);
+}
+__device__ __forceinline__ float inverse_power(uint32_t e) {
+  return __uint_as_float(e >= 254 ? 0x400000u : (254u - e) << 23);
+}
+
+// L: lanes per row, 0: a workgroup per row.
+template <int OUT, int V, int I, int L>
 __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
   __shared__ float part[2][2][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int lanes = L ? L : blockDim.x, own = L ? tid % (L ? L : 1) : tid;  // of the row; this thread among them
+  const int rows = L ? blockDim.x / (L ? L : 1) : 1;
   int turn = 0;  // (two sets of sums: a wave writes its next row's while others still read this one's)
-  for (int64_t row = blockIdx.x; row < p.t; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = (int64_t)blockIdx.x * rows + (L ? tid / (L ? L : 1) : 0); row < p.t;
+       row += (int64_t)gridDim.x * rows, turn ^= 1) {
     const uint16_t* x = p.x + row * p.ldx;
     const uint16_t* res = p.res ? p.res + row * p.ldr : nullptr;
     Raw<V> xr[I], rr[I];
     float w[I][V], z[I][V];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * blockDim.x + tid) * V;
+      const int c = (i * lanes + own) * V;
       if (c < p.h) {
         xr[i] = load<V>(x + c);
         if (res) rr[i] = load<V>(res + c);
@@ -151,7 +188,7 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
     float ss = 0.f, most = 0.f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * blockDim.x + tid) * V;
+      const int c = (i * lanes + own) * V;
       if (c < p.h) {
         widen<V>(xr[i], z[i]);
         if (res) {
@@ -168,9 +205,9 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
         }
       }
     }
-    ss = sum64(ss);
-    if constexpr (OUT == kInt8) most = max64(most);
-    if (waves > 1) {
+    ss = sum_row<L>(ss);
+    if constexpr (OUT == kInt8) most = max_row<L>(most);
+    if (L == 0 && waves > 1) {
       if (lane == 0) {
         part[turn][0][wave] = ss;
         if constexpr (OUT == kInt8) part[turn][1][wave] = most;
@@ -187,19 +224,15 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
     // a row with a NaN, or whose sum of squares is not finite: NaN scales, so
     // that what is computed from its codes is NaN too
     const bool bad = !(ss < __builtin_inff());
-    if (p.rstd && tid == 0) p.rstd[row] = r;
-    float is = 1.f, ik = 1.f;  // INT8: 1 / scale, in two factors
+    if (p.rstd && own == 0) p.rstd[row] = r;
+    Factor f{};
     if constexpr (OUT == kInt8) {
-      const float amax = most * r;
-      const float s = amax == 0.f ? 1.f : amax / 127.f;
-      const codec::GroupRecip g = codec::group_recip(s);
-      ik = g.k;
-      is = g.r;
-      if (tid == 0) static_cast<float*>(p.s)[row] = bad ? __builtin_nanf("") : s;
+      f = factor_of(most * r, 1.f / 127.f);
+      if (own == 0) static_cast<float*>(p.s)[row] = bad ? __builtin_nanf("") : f.s;
     }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * blockDim.x + tid) * V;
+      const int c = (i * lanes + own) * V;
       const bool in = c < p.h;
       float y[V];
 #pragma unroll
@@ -209,7 +242,7 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
       } else if constexpr (OUT == kInt8) {
         int q[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) q[e] = (int)__builtin_rintf(fminf(fmaxf(y[e] * ik * is, -127.f), 127.f));
+        for (int e = 0; e < V; ++e) q[e] = (int)__builtin_rintf(y[e] * f.k * f.r);
         int8_t* out = static_cast<int8_t*>(p.y) + row * p.h + c;
         if (in) {
           if constexpr (V == 8) {
@@ -229,17 +262,17 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
 #pragma unroll
         for (int e = 0; e < V; ++e) m = fmaxf(m, fabsf(y[e]));
         m = max16(m);
-        float s;
         uint32_t code = 0;
         if constexpr (OUT == kFp8Ue8m0) {
-          code = codec::ue8m0_code(m);
-          s = codec::ue8m0_value(code);
-        } else {
-          s = codec::scale_of(m);
-        }
-        const codec::GroupRecip g = codec::group_recip(s);
+          code = power_of(m);
+          const float k = inverse_power(code);
 #pragma unroll
-        for (int e = 0; e < V; ++e) y[e] = codec::scaled(y[e], g);
+          for (int e = 0; e < V; ++e) y[e] *= k;
+        } else {
+          f = factor_of(m, 1.f / codec::kE4m3Max);
+#pragma unroll
+          for (int e = 0; e < V; ++e) y[e] = y[e] * f.k * f.r;
+        }
         if (in) {
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.h + c) =
               uint2{codec::encode4(y[0], y[1], y[2], y[3]), codec::encode4(y[4], y[5], y[6], y[7])};
@@ -252,7 +285,7 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
               if (group == groups - 1)
                 for (int k = groups; k < bytes; ++k) at[k] = 0;
             } else {
-              static_cast<float*>(p.s)[row * groups + group] = bad ? __builtin_nanf("") : s;
+              static_cast<float*>(p.s)[row * groups + group] = bad ? __builtin_nanf("") : f.s;
             }
           }
         }
@@ -338,33 +371,37 @@ __device__ __forceinline__ void sum_columns(const BackwardParams& p, int tile, f
   }
 }
 
-template <int V, int I>
+template <int V, int I, int L>
 __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams p) {
   __shared__ float part[2][8];
   __shared__ float columns[8][64];
+  __shared__ float together[L ? 512 : 1][8];  // dw of the rows' lanes
   if ((int)blockIdx.x < p.columns) {
     sum_columns<V>(p, blockIdx.x, columns);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int group = blockIdx.x - p.columns, groups = gridDim.x - p.columns;
+  const int lanes = L ? L : blockDim.x, own = L ? tid % (L ? L : 1) : tid;  // of the row; this thread among them
+  const int rows = L ? blockDim.x / (L ? L : 1) : 1;
   float w[I][V], dw[I][V];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    const int c = (i * blockDim.x + tid) * V;
+    const int c = (i * lanes + own) * V;
 #pragma unroll
     for (int e = 0; e < V; ++e) dw[i][e] = 0.f;
     if (c < p.h) load_weight<V>(p.w, p.w_f32, c, w[i]);
   }
   int turn = 0;
-  for (int64_t row = group; row < p.t; row += groups, turn ^= 1) {
+  for (int64_t row = (int64_t)group * rows + (L ? tid / (L ? L : 1) : 0); row < p.t;
+       row += (int64_t)groups * rows, turn ^= 1) {
     float z[I][V], d[I][V];
     Raw<V> ds[I];
     const float r = p.rstd[row];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * blockDim.x + tid) * V;
+      const int c = (i * lanes + own) * V;
       if (c < p.h) {
         widen<V>(load<V>(p.x + row * p.ldx + c), z[i]);
         widen<V>(load<V>(p.dy + row * p.lddy + c), d[i]);
@@ -373,7 +410,7 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
     }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * blockDim.x + tid) * V;
+      const int c = (i * lanes + own) * V;
       if (c < p.h) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -386,8 +423,8 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
       }
     }
     if (!p.dx) continue;  // (for dw alone; uniform over the workgroup)
-    dot = sum64(dot);
-    if (waves > 1) {
+    dot = sum_row<L>(dot);
+    if (L == 0 && waves > 1) {
       // (two sets: a wave writes its next row's while others still read this one's)
       if (lane == 0) part[turn][wave] = dot;
       __syncthreads();
@@ -397,7 +434,7 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
     const float mean = dot / (float)p.h;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * blockDim.x + tid) * V;
+      const int c = (i * lanes + own) * V;
       if (c < p.h) {
         float o[V], f[V];
 #pragma unroll
@@ -411,10 +448,22 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
       }
     }
   }
-  if (p.partial) {
+  if (L && p.partial) {
+    // the workgroup's rows, in order
+    if constexpr (L != 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) together[tid][e] = dw[0][e];
+      __syncthreads();
+      if (tid < p.h) {
+        float v = 0.f;
+        for (int g = 0; g < rows; ++g) v += together[g * L + tid / 8][tid % 8];
+        p.partial[(int64_t)group * p.h + tid] = v;
+      }
+    }
+  } else if (p.partial) {
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * blockDim.x + tid) * V;
+      const int c = (i * lanes + own) * V;
       if (c < p.h) {
         float* q = p.partial + (int64_t)group * p.h + c;
 #pragma unroll
@@ -424,22 +473,24 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
   }
 }
 
-// dw of columns 64 b .. 64 b + 63: 16 waves sum a sixteenth of the partials each.
+// dw of columns C b .. C b + C - 1: 1024 / C slices of the partials, summed in order.
+template <int C>
 __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(const float* partial, float* dw, int parts, int h) {
-  __shared__ float sum[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane, per = (parts + 15) / 16;
+  constexpr int kSlices = 1024 / C;
+  __shared__ float sum[kSlices][C];
+  const int x = threadIdx.x % C, slice = threadIdx.x / C;
+  const int c = blockIdx.x * C + x, per = (parts + kSlices - 1) / kSlices;
   float v = 0.f;
   if (c < h) {
 #pragma unroll 16
-    for (int k = wave * per; k < min(parts, (wave + 1) * per); ++k) v += partial[(int64_t)k * h + c];
+    for (int k = slice * per; k < min(parts, (slice + 1) * per); ++k) v += partial[(int64_t)k * h + c];
   }
-  sum[wave][lane] = v;
+  sum[slice][x] = v;
   __syncthreads();
-  if (wave == 0 && c < h) {
-    v = sum[0][lane];
+  if (slice == 0 && c < h) {
+    v = sum[0][x];
 #pragma unroll
-    for (int k = 1; k < 16; ++k) v += sum[k][lane];
+    for (int k = 1; k < kSlices; ++k) v += sum[k][x];
     dw[c] = v;
   }
 }
@@ -451,24 +502,28 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // Rows that start on 16-byte boundaries.
 bool rows8(const void* p, int64_t ld, int t) { return aligned(p, 16) && (t == 1 || ld % 8 == 0); }
 
-// Pieces per thread (I) and waves (W) of a row of h columns.
+// Lanes per row (L), or pieces per thread (I) and waves (W) of a row of h columns.
 struct Shape {
-  int pieces, waves;
+  int pieces, waves, lanes;
 };
 Shape shape_of(int h, bool vec) {
+  if (vec && h <= 512) return Shape{1, 4, h <= 128 ? 16 : h <= 256 ? 32 : 64};
   const int per = vec ? 512 : 64;  // columns per wave and piece
   const int units = ceil_div(h, per);
   for (int pieces : vec ? std::initializer_list<int>{1, 2, 4} : std::initializer_list<int>{4, 8, 16, 32}) {
     const int waves = ceil_div(units, pieces);
-    if (waves <= 8) return Shape{pieces, waves};
+    if (waves <= 8) return Shape{pieces, waves, 0};
   }
-  return Shape{0, 0};
+  return Shape{0, 0, 0};
 }
 
 // (a launch holds fewer than 2^32 threads: more rows than that go several to a workgroup)
-template <int OUT, int V, int I>
+constexpr int kMostGroups = 1 << 21;
+
+template <int OUT, int V, int I, int L = 0>
 hipError_t launch_norm(const NormParams& p, int waves, hipStream_t stream) {
-  norm_kernel<OUT, V, I><<<p.t < (1 << 21) ? p.t : 1 << 21, 64 * waves, 0, stream>>>(p);
+  const int groups = ceil_div(p.t, L ? 64 * waves / (L ? L : 1) : 1);
+  norm_kernel<OUT, V, I, L><<<groups < kMostGroups ? groups : kMostGroups, 64 * waves, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -476,6 +531,9 @@ template <int OUT>
 hipError_t launch_out(const NormParams& p, bool vec, hipStream_t stream) {
   const Shape s = shape_of(p.h, vec);
   if (vec) {
+    if (s.lanes == 16) return launch_norm<OUT, 8, 1, 16>(p, s.waves, stream);
+    if (s.lanes == 32) return launch_norm<OUT, 8, 1, 32>(p, s.waves, stream);
+    if (s.lanes == 64) return launch_norm<OUT, 8, 1, 64>(p, s.waves, stream);
     if (s.pieces == 1) return launch_norm<OUT, 8, 1>(p, s.waves, stream);
     if (s.pieces == 2) return launch_norm<OUT, 8, 2>(p, s.waves, stream);
     return launch_norm<OUT, 8, 4>(p, s.waves, stream);
@@ -489,10 +547,25 @@ hipError_t launch_out(const NormParams& p, bool vec, hipStream_t stream) {
   return hipErrorInvalidValue;
 }
 
-template <int V, int I>
+template <int V, int I, int L = 0>
 hipError_t launch_backward(const BackwardParams& p, int grid, int waves, hipStream_t stream) {
-  norm_backward_kernel<V, I><<<grid, 64 * waves, 0, stream>>>(p);
+  norm_backward_kernel<V, I, L><<<grid, 64 * waves, 0, stream>>>(p);
   return hipGetLastError();
+}
+
+hipError_t launch_rows(const BackwardParams& p, bool vec, const Shape& s, int grid, hipStream_t stream) {
+  if (vec) {
+    if (s.lanes == 16) return launch_backward<8, 1, 16>(p, grid, 8, stream);
+    if (s.lanes == 32) return launch_backward<8, 1, 32>(p, grid, 8, stream);
+    if (s.lanes == 64) return launch_backward<8, 1, 64>(p, grid, 8, stream);
+    if (s.pieces == 1) return launch_backward<8, 1>(p, grid, s.waves, stream);
+    if (s.pieces == 2) return launch_backward<8, 2>(p, grid, s.waves, stream);
+    return launch_backward<8, 4>(p, grid, s.waves, stream);
+  }
+  if (s.pieces == 4) return launch_backward<1, 4>(p, grid, s.waves, stream);
+  if (s.pieces == 8) return launch_backward<1, 8>(p, grid, s.waves, stream);
+  if (s.pieces == 16) return launch_backward<1, 16>(p, grid, s.waves, stream);
+  return launch_backward<1, 32>(p, grid, s.waves, stream);
 }
 
 bool bad_weight(const void* w, int type) { return w && type != DG_TYPE_BF16 && type != DG_TYPE_F32; }
@@ -541,8 +614,13 @@ dg_status fp8(const dg_norm* in, void* q, void* s, int t, int h, bool ue8m0, hip
 }
 
 // Workgroups of the backward pass: each keeps a partial dw of h values (4 bytes
-// written and read again), so there are at most 512 of them.
-int backward_parts(int t) { return t < 512 ? t : 512; }
+// written and read again), so there are some 4096 waves of them at most.
+// (Whatever the alignment: the workspace is asked for before it is known.)
+int backward_parts(int t, int h) {
+  const int waves = h <= 512 || h > 2048 ? 8 : ceil_div(h, 512);
+  const int most = 4096 / waves;
+  return t < most ? t : most;
+}
 
 // Whether the memory of two matrices' rows may meet.
 bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int t, int h) {
@@ -604,7 +682,7 @@ dg_status dg_rmsnorm_quantize_int8(const dg_norm* in, void* q, float* s, int tok
 
 dg_status dg_rmsnorm_bf16_backward_workspace(int tokens, int hidden, int64_t* bytes) {
   if (!bytes || tokens <= 0 || hidden <= 0) return DG_ERROR_INVALID_VALUE;
-  *bytes = few(tokens, hidden) ? 0 : 4 * (int64_t)backward_parts(tokens) * hidden;
+  *bytes = few(tokens, hidden) ? 0 : 4 * (int64_t)backward_parts(tokens, hidden) * hidden;
   return DG_SUCCESS;
 }
 
@@ -643,35 +721,28 @@ dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x,
   const bool vec = h % 8 == 0 && rows8(dy, ld_dy, t) && rows8(x, ld_x, t) && (!dx || rows8(dx, ld_dx, t)) &&
                    (!with_dsum || rows8(dsum, ld_dsum, t)) && (!weight || aligned(weight, 16));
   Shape s = shape_of(h, vec);
-  const int parts = backward_parts(t);
+  const int parts = backward_parts(t, h);
   int grid = parts;
   (void)hipGetLastError();
-  hipError_t e;
   if (beside) {
     const int columns = ceil_div(h, vec ? kTileColumns<8> : kTileColumns<1>);
     p.columns = columns;
     s.waves = 8;  // (the rows' workgroups too, where they share the launch)
-    grid = columns + (dx ? t : 0);
+    const int rows = !dx ? 0 : s.lanes ? ceil_div(t, 512 / s.lanes) : t;
+    grid = columns + rows;
     if (dx && (overlap(dx, ld_dx, dy, ld_dy, t, h) || overlap(dx, ld_dx, x, ld_x, t, h))) {
       // dx over what dw's columns are summed from: those first, in a launch of their own
-      e = vec ? launch_backward<8, 1>(p, columns, 8, stream) : launch_backward<1, 4>(p, columns, 8, stream);
-      if (e != hipSuccess) return DG_ERROR_LAUNCH;
+      if (launch_rows(p, vec, s, columns, stream) != hipSuccess) return DG_ERROR_LAUNCH;
       p.columns = 0;
-      grid = t;
+      grid = rows;
     }
   }
-  if (vec)
-    e = s.pieces == 1   ? launch_backward<8, 1>(p, grid, s.waves, stream)
-        : s.pieces == 2 ? launch_backward<8, 2>(p, grid, s.waves, stream)
-                        : launch_backward<8, 4>(p, grid, s.waves, stream);
-  else
-    e = s.pieces == 4   ? launch_backward<1, 4>(p, grid, s.waves, stream)
-        : s.pieces == 8 ? launch_backward<1, 8>(p, grid, s.waves, stream)
-        : s.pieces == 16 ? launch_backward<1, 16>(p, grid, s.waves, stream)
-                        : launch_backward<1, 32>(p, grid, s.waves, stream);
-  if (e != hipSuccess) return DG_ERROR_LAUNCH;
+  if (launch_rows(p, vec, s, grid, stream) != hipSuccess) return DG_ERROR_LAUNCH;
   if (p.partial) {
-    norm_weight_sum_kernel<<<ceil_div(h, 64), 1024, 0, stream>>>(p.partial, dweight, parts, h);
+    if (parts > 512)
+      norm_weight_sum_kernel<16><<<ceil_div(h, 16), 1024, 0, stream>>>(p.partial, dweight, parts, h);
+    else
+      norm_weight_sum_kernel<64><<<ceil_div(h, 64), 1024, 0, stream>>>(p.partial, dweight, parts, h);
     if (hipGetLastError() != hipSuccess) return DG_ERROR_LAUNCH;
   }
   return DG_SUCCESS;

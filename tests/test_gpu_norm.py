@@ -73,7 +73,7 @@ def unpacked(s, groups):
 
 
 SIZES = [(1, 1), (1, 7168), (3, 8), (5, 64), (2, 127), (17, 1000), (4, 2111), (33, 512), (2, 4104), (2, 8200),
-         (3, 16384), (2, 16383), (2, 5001), (700, 136)]
+         (3, 16384), (2, 16383), (2, 5001), (700, 136), (301, 128), (77, 256), (1, 120)]
 
 
 @pytest.mark.parametrize("t,h", SIZES)
@@ -91,7 +91,8 @@ def test_bf16(dg, t, h, residual, weight):
 
 
 @pytest.mark.parametrize("packed", [False, True])
-@pytest.mark.parametrize("t,h", [(1, 128), (1, 7168), (5, 640), (37, 2048), (3, 4224), (2, 8320), (2, 16384)])
+@pytest.mark.parametrize("t,h", [(1, 128), (1, 7168), (5, 640), (37, 2048), (3, 4224), (2, 8320), (2, 16384), (301, 128), (77, 256),
+                                 (9, 384)])
 @pytest.mark.parametrize("residual,weight", [(True, BF16), (False, F32), (True, None)])
 def test_fp8(dg, t, h, residual, weight, packed):
     say(f"norm fp8 {t}x{h} packed={packed} residual={residual} weight={weight}")
@@ -237,7 +238,8 @@ def backward64(dy, z, w, r, ds):
 
 
 @pytest.mark.parametrize("t,h", SIZES + [(513, 264), (1500, 65), (600, 4096), (768, 72), (769, 72), (700, 12000),
-                                             (5000, 256), (777, 33), (130, 999)])
+                                             (5000, 256), (777, 33), (130, 999), (5001, 128), (3000, 40),
+                                             (3001, 512), (2000, 1024), (9000, 600)])
 @pytest.mark.parametrize("ds,weight", [(True, F32), (False, BF16), (True, None)])
 def test_backward(dg, t, h, ds, weight):
     say(f"norm backward {t}x{h} dsum={ds} weight={weight}")
