@@ -450,23 +450,22 @@ typedef struct {
   float* rstd;          /* [T] fp32: r, for the backward pass, or null       */
 } dg_norm;
 
-/* H <= 16384 here and below.  y [T,H] bf16: any H, alignment and stride (16-byte aligned rows
- * and H % 8 == 0 are read 16 bytes at a time). */
+/* y [T,H] bf16.  Here and below: H <= 16384, rows at any address and stride (of
+ * their type's alignment). */
 dg_status dg_rmsnorm_bf16(const dg_norm* in, void* y, int64_t ld_y, int tokens, int hidden, hipStream_t stream);
 
 /* q [T,H] fp8 (8-byte aligned), s [T,H/128] fp32, or int32 words of packed UE8M0
  * [T,ceil(H/512)].  y's few ulp of error and the quotient y RN(1/s) let a code
  * differ from exact evaluation only where y / s lies within about 2^-20
- * (relative) of the midpoint between two e4m3 values.  H % 128 == 0; x, residual
- * and sum 16-byte aligned with strides that are multiples of 8, weight 16-byte
- * aligned.  A NaN scale is E = 255 in UE8M0. */
+ * (relative) of the midpoint between two e4m3 values; scales match to the same
+ * margin.  H % 128 == 0.  A NaN scale is E = 255 in UE8M0. */
 dg_status dg_rmsnorm_quantize_fp8_1x128(const dg_norm* in, void* q, float* s, int tokens, int hidden,
                                         hipStream_t stream);
 dg_status dg_rmsnorm_quantize_fp8_1x128_ue8m0(const dg_norm* in, void* q, int32_t* s, int tokens, int hidden,
                                               hipStream_t stream);
 
 /* q [T,H] int8, s [T] fp32: the operand A of dg_gemm_int8_nt_epilogue (which needs
- * H % 16 == 0; this call takes any H, alignment and stride). */
+ * H % 16 == 0; this call takes any H). */
 dg_status dg_rmsnorm_quantize_int8(const dg_norm* in, void* q, float* s, int tokens, int hidden, hipStream_t stream);
 
 /* Backward pass.  With dy [T,H] bf16, the gradient of y (of the values that were

@@ -4,17 +4,19 @@
 //
 //     z = x + residual,  r = 1 / sqrt(mean(z^2) + eps),  y = z r w
 //
-// A workgroup of W waves owns a row and keeps it in registers: a thread holds V
-// consecutive columns (8, or 1 where rows do not start on 16-byte boundaries)
-// of each of I pieces of the row, so x and the residual are read once and z, y
-// are written once, and one barrier separates them.  A short row (heads: H <=
+// A workgroup of W waves owns a row and keeps it in registers: a thread holds 8
+// consecutive columns of each of I pieces of the row, so x and the residual are
+// read once and z, y are written once, and one barrier separates them.  Rows may
+// start anywhere: 16-byte accesses need no alignment here, and cost what aligned
+// ones do but for a line more per wave (3000 x 7783: 58 us, 89 with one column per
+// lane); only a row's last thread, where H is no multiple of 8, takes its values
+// in pieces of 4, 2 and 1 (TAIL; kernels of their own, since the branch alone costs
+// the others 3%).  A short row (heads: H <=
 // 512) belongs to L lanes of a wave instead, several rows to a wave, without LDS or
 // barrier (131072 rows of 128: 34 us with a wave each).  INT8's scale needs
 // the row's largest |y| too: max |z w| is met at the same barrier as sum z^2 and
 // multiplied by r after it.  Bound by HBM: 4096 x 7168 with a residual into FP8 is
 // 206 MB in 45 us, 4.6 TB/s, where a copy reaches 5.1.
-#include <initializer_list>
-
 #include "dg_bf16.h"
 #include "dg_fp8_codec.h"
 #include "dg_kernel.h"
@@ -43,66 +45,71 @@ struct NormParams {
   float eps;
 };
 
-// ---- a thread's V consecutive values ----
-template <int V>
-struct Raw;
-template <>
-struct Raw<8> {
+// ---- a thread's 8 consecutive values ----
+// `left` values from p to the row's end: with TAIL and fewer than 8 of them there
+// are `h & 7` (the same for every row), the others are zero.
+struct Raw {
   uint4 v;
 };
-template <>
-struct Raw<1> {
-  uint16_t v;
-};
 
-template <int V>
-__device__ __forceinline__ Raw<V> load(const uint16_t* p) {
-  if constexpr (V == 8)
-    return Raw<8>{*reinterpret_cast<const uint4*>(p)};
-  else
-    return Raw<1>{*p};
-}
-template <int V>
-__device__ __forceinline__ void widen(const Raw<V>& r, float* f) {
-  if constexpr (V == 8) {
-    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+template <bool TAIL>
+__device__ __forceinline__ Raw load(const uint16_t* p, int left, int h) {
+  Raw r{uint4{0, 0, 0, 0}};
+  if (!TAIL || left >= 8) {
+    __builtin_memcpy(&r.v, p, 16);  // (one load, whatever the address)
+  } else {
+    uint32_t o[4] = {0, 0, 0, 0}, two = 0, one = 0;
+    if (h & 4) __builtin_memcpy(o, p, 8);
+    if (h & 2) __builtin_memcpy(&two, p + (h & 4), 4);
+    if (h & 1) one = p[h & 6];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[2 * e] = from_bf16(w[e]);
-      f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    for (int d = 0; d < 4; ++d) {
+      if ((h & 2) && d == (h & 4) / 2) o[d] = two;
+      if ((h & 1) && d == (h & 6) / 2) o[d] = one;
     }
-  } else {
-    f[0] = from_bf16(r.v);
+    r.v = uint4{o[0], o[1], o[2], o[3]};
   }
+  return r;
 }
-template <int V>
-__device__ __forceinline__ void store(uint16_t* p, const float* f) {
-  if constexpr (V == 8) {
-    uint32_t o[4];
+__device__ __forceinline__ void widen(const Raw& r, float* f) {
+  const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = (uint32_t)to_bf16(f[2 * e]) | ((uint32_t)to_bf16(f[2 * e + 1]) << 16);
-    *reinterpret_cast<uint4*>(p) = uint4{o[0], o[1], o[2], o[3]};
-  } else {
-    *p = to_bf16(f[0]);
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = from_bf16(w[e]);
+    f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
   }
 }
-// The weight's values of columns c .. c + V - 1.
-template <int V>
-__device__ __forceinline__ void load_weight(const void* w, int f32, int c, float* f) {
+template <bool TAIL>
+__device__ __forceinline__ void store(uint16_t* p, const float* f, int left, int h) {
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = (uint32_t)to_bf16(f[2 * e]) | ((uint32_t)to_bf16(f[2 * e + 1]) << 16);
+  if (!TAIL || left >= 8) {
+    __builtin_memcpy(p, o, 16);
+  } else {
+    if (h & 4) __builtin_memcpy(p, o, 8);
+    const uint32_t two = h & 4 ? o[2] : o[0];
+    if (h & 2) __builtin_memcpy(p + (h & 4), &two, 4);
+    const uint32_t one = h & 4 ? (h & 2 ? o[3] : o[2]) : (h & 2 ? o[1] : o[0]);
+    if (h & 1) p[h & 6] = (uint16_t)one;
+  }
+}
+// The weight's values from column c on.
+template <bool TAIL>
+__device__ __forceinline__ void load_weight(const void* w, int f32, int c, int h, float* f) {
   if (!w) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = 1.f;
+    for (int e = 0; e < 8; ++e) f[e] = 1.f;
   } else if (f32) {
     const float* p = static_cast<const float*>(w) + c;
-    if constexpr (V == 8) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-      f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    if (!TAIL || h - c >= 8) {
+      __builtin_memcpy(f, p, 32);
     } else {
-      f[0] = *p;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = c + e < h ? p[e] : 0.f;
     }
   } else {
-    widen<V>(load<V>(static_cast<const uint16_t*>(w) + c), f);
+    widen(load<TAIL>(static_cast<const uint16_t*>(w) + c, h - c, h), f);
   }
 }
 
@@ -163,7 +170,7 @@ __device__ __forceinline__ float inverse_power(uint32_t e) {
 }
 
 // L: lanes per row, 0: a workgroup per row.
-template <int OUT, int V, int I, int L>
+template <int OUT, int I, int L, bool TAIL>
 __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
   __shared__ float part[2][2][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
@@ -174,32 +181,32 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
        row += (int64_t)gridDim.x * rows, turn ^= 1) {
     const uint16_t* x = p.x + row * p.ldx;
     const uint16_t* res = p.res ? p.res + row * p.ldr : nullptr;
-    Raw<V> xr[I], rr[I];
-    float w[I][V], z[I][V];
+    Raw xr[I], rr[I];
+    float w[I][8], z[I][8];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * lanes + own) * V;
+      const int c = (i * lanes + own) * 8;
       if (c < p.h) {
-        xr[i] = load<V>(x + c);
-        if (res) rr[i] = load<V>(res + c);
-        load_weight<V>(p.w, p.w_f32, c, w[i]);
+        xr[i] = load<TAIL>(x + c, p.h - c, p.h);
+        if (res) rr[i] = load<TAIL>(res + c, p.h - c, p.h);
+        load_weight<TAIL>(p.w, p.w_f32, c, p.h, w[i]);
       }
     }
     float ss = 0.f, most = 0.f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * lanes + own) * V;
+      const int c = (i * lanes + own) * 8;
       if (c < p.h) {
-        widen<V>(xr[i], z[i]);
+        widen(xr[i], z[i]);
         if (res) {
-          float f[V];
-          widen<V>(rr[i], f);
+          float f[8];
+          widen(rr[i], f);
 #pragma unroll
-          for (int e = 0; e < V; ++e) z[i][e] += f[e];
+          for (int e = 0; e < 8; ++e) z[i][e] += f[e];
         }
-        if (p.sum) store<V>(p.sum + row * p.lds + c, z[i]);
+        if (p.sum) store<TAIL>(p.sum + row * p.lds + c, z[i], p.h - c, p.h);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
+        for (int e = 0; e < 8; ++e) {
           ss = __builtin_fmaf(z[i][e], z[i][e], ss);
           if constexpr (OUT == kInt8) most = fmaxf(most, fabsf(z[i][e] * w[i][e]));
         }
@@ -232,46 +239,46 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
     }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * lanes + own) * V;
+      const int c = (i * lanes + own) * 8;
       const bool in = c < p.h;
-      float y[V];
+      float y[8];
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = in ? z[i][e] * r * w[i][e] : 0.f;
+      for (int e = 0; e < 8; ++e) y[e] = in ? z[i][e] * r * w[i][e] : 0.f;
       if constexpr (OUT == kBf16) {
-        if (in) store<V>(static_cast<uint16_t*>(p.y) + row * p.ldy + c, y);
+        if (in) store<TAIL>(static_cast<uint16_t*>(p.y) + row * p.ldy + c, y, p.h - c, p.h);
       } else if constexpr (OUT == kInt8) {
-        int q[V];
+        int q[8];
 #pragma unroll
-        for (int e = 0; e < V; ++e) q[e] = (int)__builtin_rintf(y[e] * f.k * f.r);
+        for (int e = 0; e < 8; ++e) q[e] = (int)__builtin_rintf(y[e] * f.k * f.r);
         int8_t* out = static_cast<int8_t*>(p.y) + row * p.h + c;
-        if (in) {
-          if constexpr (V == 8) {
-            uint32_t o[2];
+        if (TAIL ? c + 8 <= p.h : in) {
+          uint32_t o[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              o[e] = (uint32_t)(q[4 * e] & 0xff) | ((uint32_t)(q[4 * e + 1] & 0xff) << 8) |
-                     ((uint32_t)(q[4 * e + 2] & 0xff) << 16) | ((uint32_t)q[4 * e + 3] << 24);
-            *reinterpret_cast<uint2*>(out) = uint2{o[0], o[1]};
-          } else {
-            *out = (int8_t)q[0];
-          }
+          for (int e = 0; e < 2; ++e)
+            o[e] = (uint32_t)(q[4 * e] & 0xff) | ((uint32_t)(q[4 * e + 1] & 0xff) << 8) |
+                   ((uint32_t)(q[4 * e + 2] & 0xff) << 16) | ((uint32_t)q[4 * e + 3] << 24);
+          __builtin_memcpy(out, o, 8);
+        } else if (TAIL && in) {
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            if (c + e < p.h) out[e] = (int8_t)q[e];
         }
       } else {
         // a group of 128 columns is 16 lanes
         float m = 0.f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) m = fmaxf(m, fabsf(y[e]));
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
         m = max16(m);
         uint32_t code = 0;
         if constexpr (OUT == kFp8Ue8m0) {
           code = power_of(m);
           const float k = inverse_power(code);
 #pragma unroll
-          for (int e = 0; e < V; ++e) y[e] *= k;
+          for (int e = 0; e < 8; ++e) y[e] *= k;
         } else {
           f = factor_of(m, 1.f / codec::kE4m3Max);
 #pragma unroll
-          for (int e = 0; e < V; ++e) y[e] = y[e] * f.k * f.r;
+          for (int e = 0; e < 8; ++e) y[e] = y[e] * f.k * f.r;
         }
         if (in) {
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.h + c) =
@@ -318,102 +325,110 @@ struct BackwardParams {
   int columns;           // few rows: workgroups that sum columns of dw, the first ones
 };
 
-// dw's columns of `tile`: a wave takes 64 V / C rows at a time, C = 64 columns
-// (V = 8) or 32 (whole lines either way are read by the workgroups of both halves).
-template <int V>
-constexpr int kTileColumns = V == 8 ? 64 : 32;
+// Few rows: dw's columns are summed beside the rows.  A tile's rows are read by
+// one workgroup, so the time grows with them, while the partials' way pays a
+// second launch and their traffic (us beside : by partials): 17 x 1161 3.3 : 5.8,
+// 512 x 4096 5.8 : 11.6, 1000 x 2111 9.6 : 14.3, 1024 x 4096 13.9 : 12.7, 2048 x
+// 2048 21.6 : 12.2.
+constexpr int kFewRows = 768;
 
-template <int V>
-__device__ __forceinline__ void sum_columns(const BackwardParams& p, int tile, float (*part)[64]) {
-  constexpr int C = kTileColumns<V>, LPR = C / V, RPW = 64 / LPR, U = V == 8 ? 4 : 8;
+// dw's columns 32 tile .. 32 tile + 31: a wave takes 16 rows at a time (64 columns
+// and 8 rows: 517 x 1161 8.4 us for 6.0).
+constexpr int kTileColumns = 32;
+template <bool TAIL>
+__device__ __forceinline__ void sum_columns(const BackwardParams& p, int tile, float (*part)[kTileColumns]) {
+  constexpr int LPR = kTileColumns / 8, RPW = 64 / LPR;
+  constexpr int U = kFewRows / (8 * RPW);  // 8 waves have all rows in flight at once
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-  const int c = tile * C + (lane % LPR) * V;
+  const int c = tile * kTileColumns + (lane % LPR) * 8, n = p.h - c;  // (n <= 0: none)
   const int step = waves * RPW;
-  float dw[V];
+  float dw[8];
 #pragma unroll
-  for (int e = 0; e < V; ++e) dw[e] = 0.f;
-  // (columns past the last are read from the last ones again and dropped)
-  const int cl = c + V <= p.h ? c : p.h - V;
-  for (int r0 = wave * RPW + lane / LPR; r0 < p.t; r0 += step * U) {
-    Raw<V> x[U], d[U];
-    float r[U];
+  for (int e = 0; e < 8; ++e) dw[e] = 0.f;
+  if (n > 0) {
+    for (int r0 = wave * RPW + lane / LPR; r0 < p.t; r0 += step * U) {
+      Raw x[U], d[U];
+      float r[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t row = min(r0 + u * step, p.t - 1);
-      x[u] = load<V>(p.x + row * p.ldx + cl);
-      d[u] = load<V>(p.dy + row * p.lddy + cl);
-      r[u] = p.rstd[row];
-    }
+      for (int u = 0; u < U; ++u) {
+        const int64_t row = r0 + u * step;
+        x[u] = d[u] = Raw{uint4{0, 0, 0, 0}};
+        r[u] = 0.f;
+        if (row < p.t) {
+          x[u] = load<TAIL>(p.x + row * p.ldx + c, n, p.h);
+          d[u] = load<TAIL>(p.dy + row * p.lddy + c, n, p.h);
+          r[u] = p.rstd[row];
+        }
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float z[V], g[V];
-      widen<V>(x[u], z);
-      widen<V>(d[u], g);
-      if (r0 + u * step < p.t) {
+      for (int u = 0; u < U; ++u) {
+        float z[8], g[8];
+        widen(x[u], z);
+        widen(d[u], g);
 #pragma unroll
-        for (int e = 0; e < V; ++e) dw[e] = __builtin_fmaf(g[e], z[e] * r[u], dw[e]);
+        for (int e = 0; e < 8; ++e) dw[e] = __builtin_fmaf(g[e], z[e] * r[u], dw[e]);
       }
     }
   }
 #pragma unroll
   for (int m = LPR; m < 64; m *= 2)
 #pragma unroll
-    for (int e = 0; e < V; ++e) dw[e] += __shfl_xor(dw[e], m, 64);
+    for (int e = 0; e < 8; ++e) dw[e] += __shfl_xor(dw[e], m, 64);
   if (lane < LPR) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) part[wave][lane * V + e] = dw[e];
+    for (int e = 0; e < 8; ++e) part[wave][lane * 8 + e] = dw[e];
   }
   __syncthreads();
-  if (tid < C && tile * C + tid < p.h) {
+  if (tid < kTileColumns && tile * kTileColumns + tid < p.h) {
     float v = part[0][tid];
     for (int w = 1; w < waves; ++w) v += part[w][tid];
-    p.dw[tile * C + tid] = v;
+    p.dw[tile * kTileColumns + tid] = v;
   }
 }
 
-template <int V, int I, int L>
+template <int I, int L, bool TAIL>
 __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams p) {
   __shared__ float part[2][8];
-  __shared__ float columns[8][64];
+  __shared__ float columns[8][kTileColumns];
   __shared__ float together[L ? 512 : 1][8];  // dw of the rows' lanes
   if ((int)blockIdx.x < p.columns) {
-    sum_columns<V>(p, blockIdx.x, columns);
+    sum_columns<TAIL>(p, blockIdx.x, columns);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int group = blockIdx.x - p.columns, groups = gridDim.x - p.columns;
   const int lanes = L ? L : blockDim.x, own = L ? tid % (L ? L : 1) : tid;  // of the row; this thread among them
   const int rows = L ? blockDim.x / (L ? L : 1) : 1;
-  float w[I][V], dw[I][V];
+  float w[I][8], dw[I][8];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    const int c = (i * lanes + own) * V;
+    const int c = (i * lanes + own) * 8;
 #pragma unroll
-    for (int e = 0; e < V; ++e) dw[i][e] = 0.f;
-    if (c < p.h) load_weight<V>(p.w, p.w_f32, c, w[i]);
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+    if (c < p.h) load_weight<TAIL>(p.w, p.w_f32, c, p.h, w[i]);
   }
   int turn = 0;
   for (int64_t row = (int64_t)group * rows + (L ? tid / (L ? L : 1) : 0); row < p.t;
        row += (int64_t)groups * rows, turn ^= 1) {
-    float z[I][V], d[I][V];
-    Raw<V> ds[I];
+    float z[I][8], d[I][8];
+    Raw ds[I];
     const float r = p.rstd[row];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * lanes + own) * V;
+      const int c = (i * lanes + own) * 8;
       if (c < p.h) {
-        widen<V>(load<V>(p.x + row * p.ldx + c), z[i]);
-        widen<V>(load<V>(p.dy + row * p.lddy + c), d[i]);
-        if (p.dsum) ds[i] = load<V>(p.dsum + row * p.ldds + c);
+        widen(load<TAIL>(p.x + row * p.ldx + c, p.h - c, p.h), z[i]);
+        widen(load<TAIL>(p.dy + row * p.lddy + c, p.h - c, p.h), d[i]);
+        if (p.dsum) ds[i] = load<TAIL>(p.dsum + row * p.ldds + c, p.h - c, p.h);
       }
     }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * lanes + own) * V;
+      const int c = (i * lanes + own) * 8;
       if (c < p.h) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
+        for (int e = 0; e < 8; ++e) {
           const float n = z[i][e] * r;
           dw[i][e] = __builtin_fmaf(d[i][e], n, dw[i][e]);
           d[i][e] *= w[i][e];
@@ -434,17 +449,17 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
     const float mean = dot / (float)p.h;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * lanes + own) * V;
+      const int c = (i * lanes + own) * 8;
       if (c < p.h) {
-        float o[V], f[V];
+        float o[8], f[8];
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = r * __builtin_fmaf(-z[i][e], mean, d[i][e]);
+        for (int e = 0; e < 8; ++e) o[e] = r * __builtin_fmaf(-z[i][e], mean, d[i][e]);
         if (p.dsum) {
-          widen<V>(ds[i], f);
+          widen(ds[i], f);
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] += f[e];
+          for (int e = 0; e < 8; ++e) o[e] += f[e];
         }
-        store<V>(p.dx + row * p.lddx + c, o);
+        store<TAIL>(p.dx + row * p.lddx + c, o, p.h - c, p.h);
       }
     }
   }
@@ -463,11 +478,16 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
   } else if (p.partial) {
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      const int c = (i * lanes + own) * V;
+      const int c = (i * lanes + own) * 8;
       if (c < p.h) {
         float* q = p.partial + (int64_t)group * p.h + c;
+        if (!TAIL || c + 8 <= p.h) {
+          __builtin_memcpy(q, dw[i], 32);
+        } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) q[e] = dw[i][e];
+          for (int e = 0; e < 7; ++e)
+            if (c + e < p.h) q[e] = dw[i][e];
+        }
       }
     }
   }
@@ -499,81 +519,66 @@ __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(const float* part
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Rows that start on 16-byte boundaries.
-bool rows8(const void* p, int64_t ld, int t) { return aligned(p, 16) && (t == 1 || ld % 8 == 0); }
-
 // Lanes per row (L), or pieces per thread (I) and waves (W) of a row of h columns.
 struct Shape {
   int pieces, waves, lanes;
 };
-Shape shape_of(int h, bool vec) {
-  if (vec && h <= 512) return Shape{1, 4, h <= 128 ? 16 : h <= 256 ? 32 : 64};
-  const int per = vec ? 512 : 64;  // columns per wave and piece
-  const int units = ceil_div(h, per);
-  for (int pieces : vec ? std::initializer_list<int>{1, 2, 4} : std::initializer_list<int>{4, 8, 16, 32}) {
-    const int waves = ceil_div(units, pieces);
-    if (waves <= 8) return Shape{pieces, waves, 0};
-  }
-  return Shape{0, 0, 0};
+Shape shape_of(int h) {
+  if (h <= 512) return Shape{1, 4, h <= 128 ? 16 : h <= 256 ? 32 : 64};
+  const int units = ceil_div(h, 512);  // columns of a wave's piece
+  const int pieces = units <= 8 ? 1 : units <= 16 ? 2 : 4;
+  return Shape{pieces, ceil_div(units, pieces), 0};
 }
 
 // (a launch holds fewer than 2^32 threads: more rows than that go several to a workgroup)
 constexpr int kMostGroups = 1 << 21;
 
-template <int OUT, int V, int I, int L = 0>
+template <int OUT, int I, int L>
 hipError_t launch_norm(const NormParams& p, int waves, hipStream_t stream) {
   const int groups = ceil_div(p.t, L ? 64 * waves / (L ? L : 1) : 1);
-  norm_kernel<OUT, V, I, L><<<groups < kMostGroups ? groups : kMostGroups, 64 * waves, 0, stream>>>(p);
+  const int grid = groups < kMostGroups ? groups : kMostGroups;
+  if ((OUT == kBf16 || OUT == kInt8) && p.h % 8)  // (FP8's rows are whole groups of 128)
+    norm_kernel<OUT, I, L, OUT == kBf16 || OUT == kInt8><<<grid, 64 * waves, 0, stream>>>(p);
+  else
+    norm_kernel<OUT, I, L, false><<<grid, 64 * waves, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <int OUT>
-hipError_t launch_out(const NormParams& p, bool vec, hipStream_t stream) {
-  const Shape s = shape_of(p.h, vec);
-  if (vec) {
-    if (s.lanes == 16) return launch_norm<OUT, 8, 1, 16>(p, s.waves, stream);
-    if (s.lanes == 32) return launch_norm<OUT, 8, 1, 32>(p, s.waves, stream);
-    if (s.lanes == 64) return launch_norm<OUT, 8, 1, 64>(p, s.waves, stream);
-    if (s.pieces == 1) return launch_norm<OUT, 8, 1>(p, s.waves, stream);
-    if (s.pieces == 2) return launch_norm<OUT, 8, 2>(p, s.waves, stream);
-    return launch_norm<OUT, 8, 4>(p, s.waves, stream);
-  }
-  if constexpr (OUT == kBf16 || OUT == kInt8) {
-    if (s.pieces == 4) return launch_norm<OUT, 1, 4>(p, s.waves, stream);
-    if (s.pieces == 8) return launch_norm<OUT, 1, 8>(p, s.waves, stream);
-    if (s.pieces == 16) return launch_norm<OUT, 1, 16>(p, s.waves, stream);
-    return launch_norm<OUT, 1, 32>(p, s.waves, stream);
-  }
-  return hipErrorInvalidValue;
+hipError_t launch_out(const NormParams& p, hipStream_t stream) {
+  const Shape s = shape_of(p.h);
+  if (s.lanes == 16) return launch_norm<OUT, 1, 16>(p, s.waves, stream);
+  if (s.lanes == 32) return launch_norm<OUT, 1, 32>(p, s.waves, stream);
+  if (s.lanes == 64) return launch_norm<OUT, 1, 64>(p, s.waves, stream);
+  if (s.pieces == 1) return launch_norm<OUT, 1, 0>(p, s.waves, stream);
+  if (s.pieces == 2) return launch_norm<OUT, 2, 0>(p, s.waves, stream);
+  return launch_norm<OUT, 4, 0>(p, s.waves, stream);
 }
 
-template <int V, int I, int L = 0>
+template <int I, int L>
 hipError_t launch_backward(const BackwardParams& p, int grid, int waves, hipStream_t stream) {
-  norm_backward_kernel<V, I, L><<<grid, 64 * waves, 0, stream>>>(p);
+  if (p.h % 8)
+    norm_backward_kernel<I, L, true><<<grid, 64 * waves, 0, stream>>>(p);
+  else
+    norm_backward_kernel<I, L, false><<<grid, 64 * waves, 0, stream>>>(p);
   return hipGetLastError();
 }
 
-hipError_t launch_rows(const BackwardParams& p, bool vec, const Shape& s, int grid, hipStream_t stream) {
-  if (vec) {
-    if (s.lanes == 16) return launch_backward<8, 1, 16>(p, grid, 8, stream);
-    if (s.lanes == 32) return launch_backward<8, 1, 32>(p, grid, 8, stream);
-    if (s.lanes == 64) return launch_backward<8, 1, 64>(p, grid, 8, stream);
-    if (s.pieces == 1) return launch_backward<8, 1>(p, grid, s.waves, stream);
-    if (s.pieces == 2) return launch_backward<8, 2>(p, grid, s.waves, stream);
-    return launch_backward<8, 4>(p, grid, s.waves, stream);
-  }
-  if (s.pieces == 4) return launch_backward<1, 4>(p, grid, s.waves, stream);
-  if (s.pieces == 8) return launch_backward<1, 8>(p, grid, s.waves, stream);
-  if (s.pieces == 16) return launch_backward<1, 16>(p, grid, s.waves, stream);
-  return launch_backward<1, 32>(p, grid, s.waves, stream);
+hipError_t launch_rows(const BackwardParams& p, const Shape& s, int grid, hipStream_t stream) {
+  if (s.lanes == 16) return launch_backward<1, 16>(p, grid, 8, stream);
+  if (s.lanes == 32) return launch_backward<1, 32>(p, grid, 8, stream);
+  if (s.lanes == 64) return launch_backward<1, 64>(p, grid, 8, stream);
+  if (s.pieces == 1) return launch_backward<1, 0>(p, grid, s.waves, stream);
+  if (s.pieces == 2) return launch_backward<2, 0>(p, grid, s.waves, stream);
+  return launch_backward<4, 0>(p, grid, s.waves, stream);
 }
 
 bool bad_weight(const void* w, int type) { return w && type != DG_TYPE_BF16 && type != DG_TYPE_F32; }
 bool unfit_weight(const void* w, int type) { return w && !aligned(w, type == DG_TYPE_F32 ? 4 : 2); }
 bool unfit_rows(const void* p, int64_t ld) { return !aligned(p, 2) || ld > kMaxLd; }
 
-// Checks `in` and fills `p`; *vec: every row in memory starts on a 16-byte boundary.
-dg_status make_norm(const dg_norm* in, int t, int h, NormParams* p, bool* vec) {
+// Checks `in` and fills `p`.
+dg_status make_norm(const dg_norm* in, int t, int h, NormParams* p) {
   if (!in || !in->x || t <= 0 || h <= 0 || in->ld_x < h || !(in->eps >= 0.f) || in->eps > 3.4e38f)
     return DG_ERROR_INVALID_VALUE;
   if ((in->residual && in->ld_residual < h) || (in->sum && in->ld_sum < h) || bad_weight(in->weight, in->weight_type))
@@ -594,31 +599,27 @@ dg_status make_norm(const dg_norm* in, int t, int h, NormParams* p, bool* vec) {
   p->t = t;
   p->h = h;
   p->eps = in->eps;
-  *vec = h % 8 == 0 && rows8(in->x, in->ld_x, t) && (!in->residual || rows8(in->residual, in->ld_residual, t)) &&
-         (!in->sum || rows8(in->sum, in->ld_sum, t)) && (!in->weight || aligned(in->weight, 16));
   return DG_SUCCESS;
 }
 
 dg_status fp8(const dg_norm* in, void* q, void* s, int t, int h, bool ue8m0, hipStream_t stream) {
   NormParams p;
-  bool vec;
-  const dg_status st = make_norm(in, t, h, &p, &vec);
+  const dg_status st = make_norm(in, t, h, &p);
   if (st != DG_SUCCESS) return st;
   if (!q || !s) return DG_ERROR_INVALID_VALUE;
-  if (h % 128 != 0 || !vec || !aligned(q, 8) || !aligned(s, 4)) return DG_ERROR_UNSUPPORTED;
+  if (h % 128 != 0 || !aligned(q, 8) || !aligned(s, 4)) return DG_ERROR_UNSUPPORTED;
   p.y = q;
   p.s = s;
   (void)hipGetLastError();  // clear a stale error from unrelated work
-  const hipError_t e = ue8m0 ? launch_out<kFp8Ue8m0>(p, true, stream) : launch_out<kFp8>(p, true, stream);
+  const hipError_t e = ue8m0 ? launch_out<kFp8Ue8m0>(p, stream) : launch_out<kFp8>(p, stream);
   return e == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
 // Workgroups of the backward pass: each keeps a partial dw of h values (4 bytes
 // written and read again), so there are some 4096 waves of them at most.
-// (Whatever the alignment: the workspace is asked for before it is known.)
 int backward_parts(int t, int h) {
-  const int waves = h <= 512 || h > 2048 ? 8 : ceil_div(h, 512);
-  const int most = 4096 / waves;
+  const Shape s = shape_of(h);
+  const int most = s.lanes ? 512 : 4096 / s.waves;
   return t < most ? t : most;
 }
 
@@ -628,12 +629,7 @@ bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int t, int 
   return a0 < b0 + 2 * ((uintptr_t)(t - 1) * ldb + h) && b0 < a0 + 2 * ((uintptr_t)(t - 1) * lda + h);
 }
 
-// Few rows: dw's columns are summed beside the rows.  A tile's rows are read by
-// one workgroup, so the time grows with them, while the partials' way pays a
-// second launch and their traffic (us beside : by partials): 17 x 1161 3.3 : 5.8,
-// 512 x 4096 5.8 : 11.6, 1000 x 2111 9.6 : 14.3, 1024 x 4096 13.9 : 12.7, 2048 x
-// 2048 21.6 : 12.2.
-constexpr int kFewRows = 768;
+// (few rows: kFewRows above)
 constexpr int64_t kFewValues = 8 << 20;  // dy and z are read twice: 32 MB of them stay in the caches
 bool few(int t, int h) { return t <= kFewRows && (int64_t)t * h <= kFewValues; }
 
@@ -646,15 +642,14 @@ extern "C" {
 
 dg_status dg_rmsnorm_bf16(const dg_norm* in, void* y, int64_t ld_y, int tokens, int hidden, hipStream_t stream) {
   NormParams p;
-  bool vec;
-  const dg_status st = make_norm(in, tokens, hidden, &p, &vec);
+  const dg_status st = make_norm(in, tokens, hidden, &p);
   if (st != DG_SUCCESS) return st;
   if (!y || ld_y < hidden) return DG_ERROR_INVALID_VALUE;
   if (unfit_rows(y, ld_y)) return DG_ERROR_UNSUPPORTED;
   p.y = y;
   p.ldy = ld_y;
   (void)hipGetLastError();
-  return launch_out<kBf16>(p, vec && rows8(y, ld_y, tokens), stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+  return launch_out<kBf16>(p, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
 dg_status dg_rmsnorm_quantize_fp8_1x128(const dg_norm* in, void* q, float* s, int tokens, int hidden,
@@ -669,15 +664,14 @@ dg_status dg_rmsnorm_quantize_fp8_1x128_ue8m0(const dg_norm* in, void* q, int32_
 
 dg_status dg_rmsnorm_quantize_int8(const dg_norm* in, void* q, float* s, int tokens, int hidden, hipStream_t stream) {
   NormParams p;
-  bool vec;
-  const dg_status st = make_norm(in, tokens, hidden, &p, &vec);
+  const dg_status st = make_norm(in, tokens, hidden, &p);
   if (st != DG_SUCCESS) return st;
   if (!q || !s) return DG_ERROR_INVALID_VALUE;
   if (!aligned(s, 4)) return DG_ERROR_UNSUPPORTED;
   p.y = q;
   p.s = s;
   (void)hipGetLastError();
-  return launch_out<kInt8>(p, vec && aligned(q, 8), stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+  return launch_out<kInt8>(p, stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
 dg_status dg_rmsnorm_bf16_backward_workspace(int tokens, int hidden, int64_t* bytes) {
@@ -718,26 +712,24 @@ dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x,
   p.lddx = ld_dx;
   p.t = t;
   p.h = h;
-  const bool vec = h % 8 == 0 && rows8(dy, ld_dy, t) && rows8(x, ld_x, t) && (!dx || rows8(dx, ld_dx, t)) &&
-                   (!with_dsum || rows8(dsum, ld_dsum, t)) && (!weight || aligned(weight, 16));
-  Shape s = shape_of(h, vec);
+  Shape s = shape_of(h);
   const int parts = backward_parts(t, h);
   int grid = parts;
   (void)hipGetLastError();
   if (beside) {
-    const int columns = ceil_div(h, vec ? kTileColumns<8> : kTileColumns<1>);
+    const int columns = ceil_div(h, kTileColumns);
     p.columns = columns;
     s.waves = 8;  // (the rows' workgroups too, where they share the launch)
     const int rows = !dx ? 0 : s.lanes ? ceil_div(t, 512 / s.lanes) : t;
     grid = columns + rows;
     if (dx && (overlap(dx, ld_dx, dy, ld_dy, t, h) || overlap(dx, ld_dx, x, ld_x, t, h))) {
       // dx over what dw's columns are summed from: those first, in a launch of their own
-      if (launch_rows(p, vec, s, columns, stream) != hipSuccess) return DG_ERROR_LAUNCH;
+      if (launch_rows(p, s, columns, stream) != hipSuccess) return DG_ERROR_LAUNCH;
       p.columns = 0;
       grid = rows;
     }
   }
-  if (launch_rows(p, vec, s, grid, stream) != hipSuccess) return DG_ERROR_LAUNCH;
+  if (launch_rows(p, s, grid, stream) != hipSuccess) return DG_ERROR_LAUNCH;
   if (p.partial) {
     if (parts > 512)
       norm_weight_sum_kernel<16><<<ceil_div(h, 16), 1024, 0, stream>>>(p.partial, dweight, parts, h);

@@ -136,7 +136,8 @@ def test_int8(dg, t, h, residual, weight):
     within(q.to(F64) * se, y, 0.5 * se + 2.0 ** -15 * y.abs(), "codes")
 
 
-@pytest.mark.parametrize("h,stride,offset", [(256, 264, 0), (256, 264, 4), (256, 259, 0), (255, 256, 0), (1000, 1008, 8)])
+@pytest.mark.parametrize("h,stride,offset", [(256, 264, 0), (256, 264, 4), (256, 259, 0), (255, 256, 0), (1000, 1008, 8),
+                                             (128, 129, 1), (5, 7, 3), (2047, 2051, 1), (8191, 8193, 5)])
 def test_strided_rows_and_their_neighbours(dg, h, stride, offset):
     """Rows of longer tensors, on 16-byte boundaries or not; what lies between them stays."""
     say(f"norm strided {h} of {stride} at {offset}")
@@ -154,6 +155,11 @@ def test_strided_rows_and_their_neighbours(dg, h, stride, offset):
     q, s = torch.empty((t, h), dtype=torch.int8, device="cuda"), torch.empty(t, device="cuda")
     dg.rmsnorm_quantize_int8(x, w, q, s, 1e-6, r)
     within(q.to(F64) * s.to(F64)[:, None], y, 0.5 * s.to(F64)[:, None] + 2.0 ** -15 * y.abs(), "codes")
+    if h % 128 == 0:
+        q, s = torch.empty((t, h), dtype=FP8, device="cuda"), torch.empty((t, h // 128), device="cuda")
+        dg.rmsnorm_quantize_fp8_1x128(x, w, q, s, 1e-6, r)
+        se = s.to(F64).repeat_interleave(128, 1)
+        within(q.float().to(F64) * se, y, (2.0 ** -4 + 2.0 ** -15) * y.abs() + 2.0 ** -10 * se, "fp8 codes")
 
 
 @pytest.mark.parametrize("t,h", [(21, 384), (21, 2111), (768, 264), (1600, 2000)])
@@ -360,7 +366,7 @@ def test_refusals_of_the_binding(dg):
     with pytest.raises(dg.DGError):
         dg.rmsnorm_bf16(x, w, out, -1.0)
     with pytest.raises(dg.DGError):
-        dg.rmsnorm_quantize_fp8_1x128(x[:, 1:129], None, q[:, :128].contiguous().view(torch.uint8),
+        dg.rmsnorm_quantize_fp8_1x128(x[:, :192], None, q[:, :192].contiguous().view(torch.uint8),
                                       torch.empty((4, 1), device="cuda"))
 
 
