@@ -615,12 +615,16 @@ dg_status fp8(const dg_norm* in, void* q, void* s, int t, int h, bool ue8m0, hip
   return e == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
-// Workgroups of the backward pass: each keeps a partial dw of h values (4 bytes
-// written and read again), so there are some 4096 waves of them at most.
+// Workgroups of the backward pass.  Each keeps a partial dw of h values, 4 bytes
+// written and read again: 512 of them, and up to 4096 waves where rows are few
+// waves long and every workgroup still has 8 rows (16384 x 1024: 39 us with 512, 24
+// with 2048; 4096 x 1024: 14 and 16).
 int backward_parts(int t, int h) {
   const Shape s = shape_of(h);
+  int parts = t / 8 < 512 ? 512 : t / 8;
   const int most = s.lanes ? 512 : 4096 / s.waves;
-  return t < most ? t : most;
+  if (parts > most) parts = most;
+  return t < parts ? t : parts;
 }
 
 // Whether the memory of two matrices' rows may meet.
