@@ -435,8 +435,9 @@ dg_status dg_moe_few_tokens_bf16(const void* x, const float* logits, int32_t* id
  * Rows are strided: ld_x, ld_residual, ... are the elements between the starts
  * of two rows (at least H).  sum may be x or residual, and y may be any of the
  * three (with the same stride); no other overlap.  A row must keep its sum of
- * squares finite in fp32: one that does not (or holds a NaN) gets NaN scales.
- * The weight must be finite, and a scale's largest |y| 0 or at least 2^-140. */
+ * squares finite in fp32: one that does not (or holds a NaN, or zeros alone
+ * where eps is 0) gets NaN scales.
+ * The weight and y must be finite; scales below 2^-126 are rounded up. */
 typedef struct {
   const void* x;        /* [T,H] bf16                                        */
   int64_t ld_x;
@@ -492,7 +493,8 @@ dg_status dg_rmsnorm_bf16_backward_workspace(int tokens, int hidden, int64_t* by
  * Slot (t, j) is token t's j-th expert, ids[t,j]; an id outside [0,E) has no row
  * (an expert on another device), and an expert named twice by a token has two.
  * rows [T,k] int32: the row of each slot in the layout, -1 for none.
- * T, k >= 1, k <= 16, T k <= 2^23, E <= 1024.  Everything is deterministic. */
+ * T, k >= 1, k <= 16, T k <= 2^23, E <= 1024.  Everything is deterministic.
+ * Buffers overlap only where it is said that they may. */
 
 /* Contiguous layout: expert e's slots take consecutive rows, in slot order, from
  * a multiple of 128 on, the experts in order.
@@ -563,7 +565,7 @@ dg_status dg_gemm_int8_nt_epilogue(const void* a, int64_t lda, const float* sa, 
 
 /* Its operands: one scale per row of x [M,K] (x_type, stride ld_x), s = amax / 127
  * (1 for a row of zeros), q = the whole number nearest to x RN(1/s), ties to even.
- * q [M,K] int8, s [M] fp32.  Any K and alignment.  A row's amax must be 0 or at
+ * q [M,K] int8, s [M] fp32.  K <= 2^30, any alignment.  A row's amax must be 0 or at
  * least 2^-140; a row with a NaN or an infinity gets a NaN scale. */
 dg_status dg_quantize_int8_rows(const void* x, int64_t ld_x, int x_type, void* q, float* s, int m, int k,
                                 hipStream_t stream);

@@ -85,7 +85,8 @@ dg_status dg_quantize_int8_rows(const void* x, int64_t ld_x, int x_type, void* q
   if (!x || !q || !s || m <= 0 || k <= 0 || ld_x < k || (x_type != DG_TYPE_BF16 && x_type != DG_TYPE_F32))
     return DG_ERROR_INVALID_VALUE;
   const bool f32 = x_type == DG_TYPE_F32;
-  if (!aligned(x, f32 ? 4 : 2) || !aligned(s, 4) || ld_x > ((int64_t)1 << 40)) return DG_ERROR_UNSUPPORTED;
+  if (!aligned(x, f32 ? 4 : 2) || !aligned(s, 4) || ld_x > ((int64_t)1 << 40) || k > 1 << 30)
+    return DG_ERROR_UNSUPPORTED;
   (void)hipGetLastError();
   return launch_quantize_int8(x, f32, ld_x, static_cast<int8_t*>(q), s, m, k, stream) == hipSuccess ? DG_SUCCESS
                                                                                                     : DG_ERROR_LAUNCH;

@@ -15,7 +15,8 @@
 // 512) belongs to L lanes of a wave instead, several rows to a wave, without LDS or
 // barrier (131072 rows of 128: 34 us with a wave each).  INT8's scale needs
 // the row's largest |y| too: max |z w| is met at the same barrier as sum z^2 and
-// multiplied by r after it.  Bound by HBM: 4096 x 7168 with a residual into FP8 is
+// multiplied by r after it (where that leaves fp32's range, max |y| is met at a
+// barrier of its own).  Bound by HBM: 4096 x 7168 with a residual into FP8 is
 // 206 MB in 45 us, 4.6 TB/s, where a copy reaches 5.1.
 #include "dg_bf16.h"
 #include "dg_fp8_codec.h"
@@ -147,13 +148,15 @@ __device__ __forceinline__ float sum_row(float v) {
 // ---- scales ----
 // amax / most as a product and 1 / s by the reciprocal unit: y / s is within
 // 2^-21 of exact, and 2 instructions instead of two divisions' forty (every lane
-// of a group computes them).  |y| <= amax, so no code needs a clamp.  A scale
-// below 2^-60 is raised by 2^64, y alike, so that the reciprocal stays finite.
+// of a group computes them).  |y| <= amax and a subnormal s is rounded up, so no
+// code needs a clamp.  A scale below 2^-60 is raised by 2^64, y alike, so that the
+// reciprocal stays finite.
 struct Factor {
   float s, k, r;
 };
 __device__ __forceinline__ Factor factor_of(float amax, float inv_most) {
-  const float s = amax == 0.f ? 1.f : amax * inv_most;
+  float s = amax == 0.f ? 1.f : amax * inv_most;
+  if (s < 0x1p-126f) s += 0x1p-149f;  // (never below amax / most: it was rounded by half of that)
   const float k = s < 0x1p-60f ? 0x1p64f : 1.f;
   return Factor{s, k, __builtin_amdgcn_rcpf(s * k)};
 }
@@ -173,6 +176,7 @@ __device__ __forceinline__ float inverse_power(uint32_t e) {
 template <int OUT, int I, int L, bool TAIL>
 __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
   __shared__ float part[2][2][8];
+  __shared__ float most_y[OUT == kInt8 ? 2 : 1][8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int lanes = L ? L : blockDim.x, own = L ? tid % (L ? L : 1) : tid;  // of the row; this thread among them
   const int rows = L ? blockDim.x / (L ? L : 1) : 1;
@@ -228,13 +232,30 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
       }
     }
     const float r = 1.f / __builtin_sqrtf(ss / (float)p.h + p.eps);
-    // a row with a NaN, or whose sum of squares is not finite: NaN scales, so
-    // that what is computed from its codes is NaN too
-    const bool bad = !(ss < __builtin_inff());
+    // a row with a NaN, whose sum of squares is not finite, or of zeros without an
+    // eps: NaN scales, so that what is computed from its codes is NaN too
+    const bool bad = !(ss < __builtin_inff()) || r == __builtin_inff();
     if (p.rstd && own == 0) p.rstd[row] = r;
     Factor f{};
     if constexpr (OUT == kInt8) {
-      f = factor_of(most * r, 1.f / 127.f);
+      float amax = most * r;
+      // z w so small or large that fp32 does not hold it to full precision (or a
+      // row of zeros), though y may be in range: the largest |y| itself
+      if (!(most > 0x1p-100f && most < 0x1p120f)) {
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+          if ((i * lanes + own) * 8 < p.h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(z[i][e] * r * w[i][e]));
+        amax = max_row<L>(amax);
+        if (L == 0 && waves > 1) {
+          if (lane == 0) most_y[turn][wave] = amax;
+          __syncthreads();
+          for (int k = 0; k < waves; ++k) amax = fmaxf(amax, most_y[turn][k]);
+        }
+      }
+      f = factor_of(amax, 1.f / 127.f);
       if (own == 0) static_cast<float*>(p.s)[row] = bad ? __builtin_nanf("") : f.s;
     }
 #pragma unroll

@@ -261,6 +261,12 @@ def test_quantize_int8(lib, kw, want):
     assert lib.dg_quantize_int8_rows(a["x"], a["ld"], a["kind"], a["q"], a["s"], a["m"], a["k"], None) == want
 
 
+def test_quantize_int8_of_too_long_rows(lib):
+    """Column numbers and the step past the last one stay in 32 bits."""
+    k = (1 << 30) + 1
+    assert lib.dg_quantize_int8_rows(P, k, BF16, P, P, 1, k, None) == UNSUPPORTED
+
+
 def test_binding_wants_the_gpu():
     """Tensors on the host are refused by every call of the binding."""
     import moe_grouped_gemm_x128_amd as dg

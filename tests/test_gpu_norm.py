@@ -220,6 +220,49 @@ def test_rows_of_zeros_and_of_bad_values(dg):
     within(out[:3], y, (2.0 ** -8 + 2.0 ** -16) * y.abs(), "eps 0")
 
 
+# Weights that take z w, or y itself, to the ends of fp32's range.  Besides the bounds above: a product or a scale
+# below 2^-126 is rounded to a multiple of 2^-149 (half of that off), and such a scale is one unit larger.
+@pytest.mark.parametrize("x_scale,w_scale", [(1.0, 2.0 ** -120), (1.0, 2.0 ** -130), (1.0, 2.0 ** -138), (2.0 ** -50, 2.0 ** -100),
+                                             (2.0 ** -55, 2.0 ** -96), (2.0 ** 50, 2.0 ** 85), (1.0, 2.0 ** 110)])
+@pytest.mark.parametrize("t,h", [(5, 384), (9, 128), (3, 4224), (2, 9088)])
+def test_weights_at_the_ends_of_the_range(dg, t, h, x_scale, w_scale):
+    say(f"norm {t}x{h} x {x_scale} w {w_scale}")
+    x, _, w = inputs(t, h, False, F32, 9)
+    x, w = (x.to(F32) * x_scale).to(BF16), w * w_scale
+    w[::7] *= 2.0 ** -9
+    y = ref64(x, None, w, 0.0)[2]
+    unit = 2.0 ** -149
+    q, s = torch.empty((t, h), dtype=torch.int8, device="cuda"), torch.empty(t, device="cuda")
+    dg.rmsnorm_quantize_int8(x, w, q, s, 0.0)
+    want = y.abs().amax(1) / 127
+    within(s, want, 2.0 ** -16 * want + 2 * unit, "int8 scales")
+    se = s.to(F64)[:, None]
+    within(q.to(F64) * se, y, 0.5 * se + 2.0 ** -15 * y.abs() + unit, "int8")
+    f, fs = torch.empty((t, h), dtype=FP8, device="cuda"), torch.empty((t, h // 128), device="cuda")
+    dg.rmsnorm_quantize_fp8_1x128(x, w, f, fs, 0.0)
+    want = y.view(t, h // 128, 128).abs().amax(2) / 448
+    within(fs, want, 2.0 ** -16 * want + 2 * unit, "fp8 scales")
+    se = fs.to(F64).repeat_interleave(128, 1)
+    within(f.to(F64) * se, y, 2.0 ** -4 * y.abs() + 2.0 ** -10 * se + 2.0 ** -15 * y.abs() + unit, "fp8")
+
+
+def test_rows_of_zeros_without_eps(dg):
+    """0 / 0: NaN in every output, as in the formula."""
+    say("norm of zeros, eps 0")
+    x = torch.zeros((3, 256), dtype=BF16, device="cuda")
+    x[1] = 1
+    out, q, s = torch.empty_like(x), torch.empty((3, 256), dtype=torch.int8, device="cuda"), torch.empty(3, device="cuda")
+    dg.rmsnorm_bf16(x, None, out, 0.0)
+    dg.rmsnorm_quantize_int8(x, None, q, s, 0.0)
+    f, fs, p = torch.empty((3, 256), dtype=FP8, device="cuda"), torch.empty((3, 2), device="cuda"), \
+        torch.empty((3, 1), dtype=torch.int32, device="cuda")
+    dg.rmsnorm_quantize_fp8_1x128(x, None, f, fs, 0.0)
+    dg.rmsnorm_quantize_fp8_1x128(x, None, f, p, 0.0)
+    b = p.view(torch.uint8)[:, :2]
+    assert out[[0, 2]].isnan().all() and s[[0, 2]].isnan().all() and fs[[0, 2]].isnan().all() and (b[[0, 2]] == 255).all()
+    assert (out[1] == 1).all() and s[1].isfinite() and fs[1].isfinite().all() and (b[1] != 255).all()
+
+
 def test_more_rows_than_workgroups(dg):
     """2^21 + 3 rows: workgroups take several."""
     say("norm 2^21 + 3 rows")
