@@ -11,13 +11,16 @@
 // ones do but for a line more per wave (3000 x 7783: 58 us, 89 with one column per
 // lane); only a row's last thread, where H is no multiple of 8, takes its values
 // in pieces of 4, 2 and 1 (TAIL; kernels of their own, since the branch alone costs
-// the others 3%).  A short row (heads: H <=
-// 512) belongs to L lanes of a wave instead, several rows to a wave, without LDS or
-// barrier (131072 rows of 128: 34 us with a wave each).  INT8's scale needs
-// the row's largest |y| too: max |z w| is met at the same barrier as sum z^2 and
-// multiplied by r after it (where that leaves fp32's range, max |y| is met at a
-// barrier of its own).  Bound by HBM: 4096 x 7168 with a residual into FP8 is
-// 206 MB in 45 us, 4.6 TB/s, where a copy reaches 5.1.
+// the others 3%).  A short row (heads: H <= 512) belongs to L lanes of a wave
+// instead, several rows to a wave, without LDS or barrier (131072 rows of 128:
+// 34 us with a wave each, 13 so).  INT8's scale needs the row's largest |y| too:
+// max |z w| is met at the same barrier as sum z^2 and multiplied by r after it
+// (where that leaves fp32's range, max |y| is met at a barrier of its own).
+//
+// Bound by HBM: 4096 x 7168 with a residual into FP8 is 206 MB in 43.7 us, 4.7
+// TB/s, where a copy reaches 5.1.  The 300 vector instructions of 16 values are a
+// third of that, so they count: 8192 x 7168 into FP8 took 43.8 us with a square
+// root and a division per thread and two factors per value, 38.7 without.
 #include "dg_bf16.h"
 #include "dg_fp8_codec.h"
 #include "dg_kernel.h"
@@ -43,7 +46,7 @@ struct NormParams {
   void* s;              // scales
   int64_t ldx, ldr, lds, ldy;
   int t, h, w_f32;
-  float eps;
+  float eps, inv_h;
 };
 
 // ---- a thread's 8 consecutive values ----
@@ -145,6 +148,15 @@ __device__ __forceinline__ float sum_row(float v) {
   return v;
 }
 
+// 1 / sqrt(v) by the root unit, within 2^-22 (a square root and a division are 25
+// instructions in every lane).  Small v is raised by 2^64 first: the unit does
+// without subnormal operands.
+__device__ __forceinline__ float inverse_root(float v) {
+  const bool small = v < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v);
+  return small ? r * 0x1p32f : r;
+}
+
 // ---- scales ----
 // amax / most as a product and 1 / s by the reciprocal unit: y / s is within
 // 2^-21 of exact, and 2 instructions instead of two divisions' forty (every lane
@@ -153,6 +165,14 @@ __device__ __forceinline__ float sum_row(float v) {
 // reciprocal stays finite.
 struct Factor {
   float s, k, r;
+  __device__ __forceinline__ void scale(float* y) const {  // 8 values by 1 / s
+    if (k != 1.f) {  // (rare)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= k;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= r;
+  }
 };
 __device__ __forceinline__ Factor factor_of(float amax, float inv_most) {
   float s = amax == 0.f ? 1.f : amax * inv_most;
@@ -231,7 +251,7 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
         for (int k = 1; k < waves; ++k) most = fmaxf(most, part[turn][1][k]);
       }
     }
-    const float r = 1.f / __builtin_sqrtf(ss / (float)p.h + p.eps);
+    const float r = inverse_root(__builtin_fmaf(ss, p.inv_h, p.eps));
     // a row with a NaN, whose sum of squares is not finite, or of zeros without an
     // eps: NaN scales, so that what is computed from its codes is NaN too
     const bool bad = !(ss < __builtin_inff()) || r == __builtin_inff();
@@ -269,8 +289,9 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
         if (in) store<TAIL>(static_cast<uint16_t*>(p.y) + row * p.ldy + c, y, p.h - c, p.h);
       } else if constexpr (OUT == kInt8) {
         int q[8];
+        f.scale(y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = (int)__builtin_rintf(y[e] * f.k * f.r);
+        for (int e = 0; e < 8; ++e) q[e] = (int)__builtin_rintf(y[e]);
         int8_t* out = static_cast<int8_t*>(p.y) + row * p.h + c;
         if (TAIL ? c + 8 <= p.h : in) {
           uint32_t o[2];
@@ -298,8 +319,7 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
           for (int e = 0; e < 8; ++e) y[e] *= k;
         } else {
           f = factor_of(m, 1.f / codec::kE4m3Max);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = y[e] * f.k * f.r;
+          f.scale(y);
         }
         if (in) {
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.h + c) =
@@ -620,6 +640,7 @@ dg_status make_norm(const dg_norm* in, int t, int h, NormParams* p) {
   p->t = t;
   p->h = h;
   p->eps = in->eps;
+  p->inv_h = 1.f / (float)h;
   return DG_SUCCESS;
 }
 
