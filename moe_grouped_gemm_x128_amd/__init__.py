@@ -722,8 +722,9 @@ def moe_few_tokens_bf16(x, w13, w2, out, ids, weights, logits=None, scoring="sof
 
 # ------------------------- norm with the residual's addition, INT8 layer ---
 # Small calls are bound by what happens before the launch, so each tensor is
-# looked at once, natively (csrc/dg_tensors.cpp); the reason for a refusal is
-# worked out only then.
+# looked at once, natively (csrc/dg_tensors.cpp).  The functions in Python that
+# have a native counterpart (_matrix_of for _matrix, ...) answer where that finds
+# anything unexpected: they work out the reason and raise.
 
 _BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
 _norm_fields = struct.Struct("PqPqPifPqP").pack   # dg_norm
@@ -754,13 +755,13 @@ _whole = _tensors.whole  # address of a contiguous tensor of the given type and 
 _rows = _tensors.rows    # address and row stride of a matrix with contiguous rows
 
 
-def _bytes8(t, shape, dev, name):
+def _bytes8_of(t, shape, dev, name):
     """Pointer of a contiguous tensor of FP8 values or their bytes."""
     _fp8(t, name)
     return _whole(t, t.dtype, shape, dev, name)
 
 
-def _vector_type(t, n, dev, name):
+def _vector_of(t, n, dev, name):
     """Pointer and type of a contiguous vector in bf16 or fp32."""
     kind = _TYPE.get(t.dtype)
     if kind is None:
@@ -768,14 +769,14 @@ def _vector_type(t, n, dev, name):
     return _whole(t, t.dtype, (n,), dev, name), kind
 
 
-def _matrix(t, name):
+def _matrix_of(t, name, current):
     """Shape and GPU of a call's first tensor."""
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
     dev = t.get_device()
-    if dev != _current_device():  # (the default stream is the current GPU's)
+    if dev != current():  # (the default stream is the current GPU's)
         raise ValueError(f"{name} is on GPU {dev}, which is not the current one: call under torch.cuda.device({dev})")
     return t.shape, dev
 
@@ -792,12 +793,12 @@ def _room(workspace, need, dev, like):
     return workspace.data_ptr()
 
 
-def _norm(x, shape, weight, eps, residual, sum_out, rstd, dev):
+def _norm_of(x, shape, weight, eps, residual, sum_out, rstd, dev):
     """The call's dg_norm, as bytes."""
     xp, ldx = _rows(x, _BF16, shape, dev, "x")
     wp = rp = sp = dp = wt = ldr = lds = 0
     if weight is not None:
-        wp, wt = _vector_type(weight, shape[1], dev, "weight")
+        wp, wt = _vector_of(weight, shape[1], dev, "weight")
     if residual is not None:
         rp, ldr = _rows(residual, _BF16, shape, dev, "residual")
     if sum_out is not None:
@@ -807,12 +808,38 @@ def _norm(x, shape, weight, eps, residual, sum_out, rstd, dev):
     return _norm_fields(xp, ldx, rp, ldr, wp, wt, eps, sp, lds, dp)
 
 
+def _layout_of(a, dtype, cols, dev, name):
+    """Pointer and row count of a grouped layout's rows [M,cols] or [E,M_max,cols]
+    (dtype None: FP8 values or their bytes)."""
+    if dtype is None:
+        _fp8(a, name)
+        dtype = a.dtype
+    shape = a.shape
+    n = len(shape)
+    if n not in (2, 3) or shape[-1] != cols:
+        raise ValueError(f"{name} must be [M,{cols}] or [E,M_max,{cols}], got {tuple(shape)}")
+    return _whole(a, dtype, shape, dev, name), shape[0] if n == 2 else shape[0] * shape[1]
+
+
+def _slots_of(rows, t, dev):
+    """Pointer and width of the rows int32 [T,k] of the tokens' slots."""
+    shape = rows.shape
+    if len(shape) != 2 or shape[0] != t:
+        raise ValueError(f"rows must be [{t},k], got {tuple(shape)}")
+    return _whole(rows, _I32, shape, dev, "rows"), shape[1]
+
+
+_tensors.otherwise(_matrix_of, _vector_of, _bytes8_of, _layout_of, _slots_of, _norm_of)
+_matrix, _vector, _bytes8 = _tensors.matrix, _tensors.vector, _tensors.bytes8
+_layout, _slots, _norm = _tensors.layout, _tensors.slots, _tensors.norm
+
+
 def rmsnorm_bf16(x, weight, out, eps=1e-6, residual=None, sum_out=None, rstd=None):
     """out bf16 [T,H] = z / sqrt(mean(z^2) + eps) * weight with z = x + residual
     (see dg_rmsnorm_bf16 in include/dg.h).  weight [H] bf16, fp32 or None;
     sum_out bf16 [T,H] receives z (may be x or residual), rstd fp32 [T] the
     factor for the backward pass.  Rows may be strided."""
-    shape, dev = _matrix(x, "x")
+    shape, dev = _matrix(x, "x", _current_device)
     p = _norm(x, shape, weight, eps, residual, sum_out, rstd, dev)
     op, ldo = _rows(out, _BF16, shape, dev, "out")
     st = _lib.dg_rmsnorm_bf16(p, op, ldo, *shape, _stream_of(dev))
@@ -824,7 +851,7 @@ def rmsnorm_bf16(x, weight, out, eps=1e-6, residual=None, sum_out=None, rstd=Non
 def rmsnorm_quantize_fp8_1x128(x, weight, q, s, eps=1e-6, residual=None, sum_out=None, rstd=None):
     """rmsnorm_bf16 with its fp32 result quantised: q fp8 [T,H], s fp32
     [T,H/128], or int32 [T,ceil(H/512)] for packed UE8M0 scales."""
-    shape, dev = _matrix(x, "x")
+    shape, dev = _matrix(x, "x", _current_device)
     t, h = shape
     p = _norm(x, shape, weight, eps, residual, sum_out, rstd, dev)
     qp = _bytes8(q, shape, dev, "q")
@@ -842,7 +869,7 @@ def rmsnorm_quantize_fp8_1x128(x, weight, q, s, eps=1e-6, residual=None, sum_out
 
 def rmsnorm_quantize_int8(x, weight, q, s, eps=1e-6, residual=None, sum_out=None, rstd=None):
     """rmsnorm_bf16 with its fp32 result quantised: q int8 [T,H], s fp32 [T]."""
-    shape, dev = _matrix(x, "x")
+    shape, dev = _matrix(x, "x", _current_device)
     p = _norm(x, shape, weight, eps, residual, sum_out, rstd, dev)
     st = _lib.dg_rmsnorm_quantize_int8(p, _whole(q, _I8, shape, dev, "q"), _whole(s, _F32, shape[:1], dev, "s"), *shape,
                                        _stream_of(dev))
@@ -865,11 +892,11 @@ def rmsnorm_bf16_backward(dout, z, weight, rstd, dx=None, dweight=None, dsum=Non
     (the gradient of x and of residual; dsum bf16 [T,H], the gradient that
     reaches sum_out from elsewhere, is added) and dweight fp32 [H] that are
     given and returns both."""
-    shape, dev = _matrix(dout, "dout")
+    shape, dev = _matrix(dout, "dout", _current_device)
     t, h = shape
     op, ldo = _rows(dout, _BF16, shape, dev, "dout")
     zp, ldz = _rows(z, _BF16, shape, dev, "z")
-    wp, wt = (None, 0) if weight is None else _vector_type(weight, h, dev, "weight")
+    wp, wt = (None, 0) if weight is None else _vector(weight, h, dev, "weight")
     dsp = dxp = dwp = wsp = None
     ldds = lddx = 0
     if dx is not None:
@@ -891,7 +918,7 @@ def gemm_int8_nt_epilogue(lhs, rhs, out, bias=None, activation="none", residual=
     [M,K], fp32 [M]), rhs = (int8 [N,K], fp32 [N]) (see
     dg_gemm_int8_nt_epilogue in include/dg.h)."""
     (a, sa), (b, sb) = lhs, rhs
-    (m, k), dev = _matrix(a, "a")
+    (m, k), dev = _matrix(a, "a", _current_device)
     n = b.shape[0]
     ap, lda = _rows(a, _I8, (m, k), dev, "a")
     bp, ldb = _rows(b, _I8, (n, k), dev, "b")
@@ -901,7 +928,7 @@ def gemm_int8_nt_epilogue(lhs, rhs, out, bias=None, activation="none", residual=
     cp, ldc = _rows(out, out.dtype, (m, n), dev, "out")
     bip = bit = rp = ldr = pp = ldp = 0
     if bias is not None:
-        bip, bit = _vector_type(bias, n, dev, "bias")
+        bip, bit = _vector(bias, n, dev, "bias")
     if residual is not None:
         rp, ldr = _rows(residual, _BF16, (m, n), dev, "residual")
     if pre is not None:
@@ -918,7 +945,7 @@ def gemm_int8_nt_epilogue(lhs, rhs, out, bias=None, activation="none", residual=
 def dg_quantize_int8_rows(x, q, s):
     """x bf16 or fp32 [M,K] -> q int8 [M,K], s fp32 [M]: a scale per row (see
     include/dg.h).  x's rows may be strided."""
-    shape, dev = _matrix(x, "x")
+    shape, dev = _matrix(x, "x", _current_device)
     kind = _TYPE.get(x.dtype)
     if kind is None:
         raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
@@ -951,7 +978,7 @@ def moe_sort_contiguous(ids, num_experts, m_indices, rows, counts=None, workspac
     dg_moe_sort_contiguous in include/dg.h): writes m_indices int32 [M_total]
     (moe_sort_rows gives an M_total for any routing), rows int32 [T,k] and, if
     given, counts int32 [E]; returns m_indices and rows."""
-    shape, dev = _matrix(ids, "ids")
+    shape, dev = _matrix(ids, "ids", _current_device)
     t, k = shape
     m = m_indices.shape[0]
     st = _lib.dg_moe_sort_contiguous(
@@ -967,7 +994,7 @@ def moe_sort_contiguous(ids, num_experts, m_indices, rows, counts=None, workspac
 def moe_sort_masked(ids, m_max, masked_m, rows, workspace=None):
     """Rows of the masked layout [E,M_max,..] for the tokens' experts ids int32
     [T,k]: writes masked_m int32 [E] and rows int32 [T,k] and returns both."""
-    shape, dev = _matrix(ids, "ids")
+    shape, dev = _matrix(ids, "ids", _current_device)
     t, k = shape
     e = masked_m.shape[0]
     st = _lib.dg_moe_sort_masked(
@@ -979,23 +1006,6 @@ def moe_sort_masked(ids, m_max, masked_m, rows, workspace=None):
     return masked_m, rows
 
 
-def _layout(a, dtype, cols, dev, name):
-    """Pointer and row count of a grouped layout's rows [M,cols] or [E,M_max,cols]."""
-    shape = a.shape
-    n = len(shape)
-    if n not in (2, 3) or shape[-1] != cols:
-        raise ValueError(f"{name} must be [M,{cols}] or [E,M_max,{cols}], got {tuple(shape)}")
-    return _whole(a, dtype, shape, dev, name), shape[0] if n == 2 else shape[0] * shape[1]
-
-
-def _slots(rows, t, dev):
-    """Pointer and width of the rows int32 [T,k] of the tokens' slots."""
-    shape = rows.shape
-    if len(shape) != 2 or shape[0] != t:
-        raise ValueError(f"rows must be [{t},k], got {tuple(shape)}")
-    return _whole(rows, _I32, shape, dev, "rows"), shape[1]
-
-
 def _optional(t, dtype, shape, dev, name):
     return None if t is None else _whole(t, dtype, shape, dev, name)
 
@@ -1004,7 +1014,7 @@ def moe_dispatch_bf16(x, rows, a, m_indices=None):
     """a[rows[t,j]] = x[t] for bf16 x [T,H] (see dg_moe_dispatch_bf16 in
     include/dg.h); a bf16 [M,H] or [E,M_max,H].  With m_indices (contiguous
     layout) the padding rows of the segments become zeros."""
-    shape, dev = _matrix(x, "x")
+    shape, dev = _matrix(x, "x", _current_device)
     t, h = shape
     xp, ldx = _rows(x, _BF16, shape, dev, "x")
     ap, m = _layout(a, _BF16, h, dev, "a")
@@ -1021,11 +1031,10 @@ def moe_dispatch_fp8(x, rows, a, m_indices=None):
     [T,H/128] or int32 [T,ceil(H/512)]), a = (fp8 [M,H] or [E,M_max,H], scales
     of the same)."""
     (q, s), (qa, sa) = x, a
-    shape, dev = _matrix(q, "x")
+    shape, dev = _matrix(q, "x", _current_device)
     t, h = shape
     qp = _bytes8(q, shape, dev, "x")
-    _fp8(qa, "a")
-    ap, m = _layout(qa, qa.dtype, h, dev, "a")
+    ap, m = _layout(qa, None, h, dev, "a")
     kind = s.dtype
     if kind is _I32:
         fn, words = _lib.dg_moe_dispatch_fp8_ue8m0, (h + 511) // 512
@@ -1046,7 +1055,7 @@ def moe_combine_bf16(o, rows, out, weights=None, residual=None):
     """out[t] = residual[t] + sum_j weights[t,j] o[rows[t,j]] (see
     dg_moe_combine_bf16 in include/dg.h): o bf16 [M,H] or [E,M_max,H], weights
     fp32 [T,k] or None (ones), residual bf16 [T,H] (may be out)."""
-    shape, dev = _matrix(out, "out")
+    shape, dev = _matrix(out, "out", _current_device)
     t, h = shape
     yp, ldy = _rows(out, _BF16, shape, dev, "out")
     op, m = _layout(o, _BF16, h, dev, "o")
@@ -1069,7 +1078,7 @@ def moe_combine_bf16_backward(dout, o, rows, weights=None, do=None, dweights=Non
     writes those of do bf16, of o's shape (may be o), and dweights fp32 [T,k]
     that are given and returns both.  With m_indices (contiguous layout) the
     padding rows of do become zeros."""
-    shape, dev = _matrix(dout, "dout")
+    shape, dev = _matrix(dout, "dout", _current_device)
     t, h = shape
     dp, ldd = _rows(dout, _BF16, shape, dev, "dout")
     op, m = _layout(o, _BF16, h, dev, "o")

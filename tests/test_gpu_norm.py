@@ -425,3 +425,60 @@ def test_another_gpu_than_the_current_one(dg, monkeypatch):
                  lambda: dg.moe_dispatch_bf16(x, ids, out), lambda: dg.moe_combine_bf16(out, ids, x)):
         with pytest.raises(ValueError, match="not the current one"):
             call()
+
+
+@pytest.mark.parametrize("t,h,stride", [(1, 256, 0), (3, 256, 264), (2, 1, 8)])
+@pytest.mark.parametrize("weight", [BF16, F32, None])
+@pytest.mark.parametrize("eps", [1e-6, 0, 1])
+def test_native_arguments_are_the_binding_s(dg, t, h, stride, weight, eps):
+    """What the native helper makes of a call's tensors is what the functions in Python behind it make."""
+    say(f"native arguments {t}x{h}")
+    x, r, w = inputs(t, h, True, weight, 11, stride)
+    total, rstd = torch.empty_like(x), torch.empty(t, device="cuda")
+    for args in ((x, (t, h), w, eps, r, total, rstd, 0), (x, (t, h), w, eps, None, None, None, 0)):
+        assert dg._norm(*args) == dg._norm_of(*args)
+    current = dg._current_device
+    assert dg._matrix(x, "x", current) == dg._matrix_of(x, "x", current)
+    if w is not None:
+        assert dg._vector(w, h, 0, "w") == dg._vector_of(w, h, 0, "w")
+    q = torch.zeros((t, h), dtype=torch.uint8, device="cuda")
+    a = torch.zeros((2, t, h), dtype=FP8, device="cuda")
+    rows = torch.zeros((t, 3), dtype=torch.int32, device="cuda")
+    for b in (q, q.view(FP8)):
+        assert dg._bytes8(b, (t, h), 0, "q") == dg._bytes8_of(b, (t, h), 0, "q")
+        assert dg._layout(b, None, h, 0, "a") == dg._layout_of(b, None, h, 0, "a")
+    assert dg._layout(a, None, h, 0, "a") == dg._layout_of(a, None, h, 0, "a") == (a.data_ptr(), 2 * t)
+    assert dg._layout(rows, torch.int32, 3, 0, "a") == dg._layout_of(rows, torch.int32, 3, 0, "a")
+    assert dg._slots(rows, t, 0) == dg._slots_of(rows, t, 0)
+
+
+def test_native_arguments_refuse_as_the_binding_does(dg):
+    """Every mismatch ends in the same error as without the native helper."""
+    x, _, w = inputs(4, 256, False, F32, 12)
+    q, rows = torch.zeros((4, 256), dtype=torch.uint8, device="cuda"), torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    n = lambda **kw: tuple({**dict(x=x, shape=(4, 256), weight=w, eps=1e-6, residual=None, sum_out=None, rstd=None, dev=0),
+                            **kw}.values())
+    cases = [("_norm", n(weight=w[:255])), ("_norm", n(weight=w.to(torch.float16))), ("_norm", n(residual=x[:3])),
+             ("_norm", n(sum_out=x.float())), ("_norm", n(rstd=w)), ("_norm", n(dev=1)), ("_norm", n(eps="1")),
+             ("_norm", n(eps=1e39)), ("_norm", n(residual=x.t())), ("_norm", n(weight=w.cpu())), ("_norm", n(residual=3)),
+             ("_matrix", (w, "x", dg._current_device)), ("_matrix", (x.cpu(), "x", dg._current_device)),
+             ("_matrix", (x, "x", lambda: 5)), ("_vector", (w, 255, 0, "w")), ("_vector", (w.double(), 256, 0, "w")),
+             ("_vector", (x, 256, 0, "w")), ("_bytes8", (x, (4, 256), 0, "q")), ("_bytes8", (q, (4, 255), 0, "q")),
+             ("_bytes8", (q[:, ::2], (4, 128), 0, "q")), ("_layout", (q, None, 255, 0, "a")),
+             ("_layout", (x, None, 256, 0, "a")), ("_layout", (x, F32, 256, 0, "a")), ("_layout", (w, F32, 256, 0, "a")),
+             ("_slots", (rows, 3, 0)), ("_slots", (rows.long(), 4, 0)), ("_slots", (rows.t(), 2, 0)), ("_slots", (rows, 4, 1))]
+
+    def outcome(f, args):
+        try:
+            return f(*args)
+        except Exception as e:
+            return type(e), str(e)
+
+    refused = 0
+    for name, args in cases:
+        python = outcome(getattr(dg, name + "_of"), args)
+        assert outcome(getattr(dg, name), args) == python, name
+        refused += isinstance(python, tuple) and isinstance(python[0], type)
+    assert refused == len(cases) - 1  # (an eps past fp32 packs as an infinity, which the library refuses)
+    with pytest.raises(dg.DGError):
+        dg.rmsnorm_bf16(x, w, torch.empty_like(x), 1e39)
