@@ -9,8 +9,8 @@
 // read once and z, y are written once, and one barrier separates them.  Rows may
 // start anywhere: 16-byte accesses need no alignment here, and cost what aligned
 // ones do but for a line more per wave (3000 x 7783: 58 us, 89 with one column per
-// lane); only a row's last thread, where H is no multiple of 8, takes its values
-// in pieces of 4, 2 and 1 (TAIL; kernels of their own, since the branch alone costs
+// lane); only a row's last thread, where H is no multiple of 8, stores its values
+// in pieces of 4, 2 and 1 (kTail; kernels of their own, since the branch alone costs
 // the others 3%).  A short row (heads: H <= 512) belongs to L lanes of a wave
 // instead, several rows to a wave, without LDS or barrier (131072 rows of 128:
 // 34 us with a wave each, 13 so).  INT8's scale needs the row's largest |y| too:
@@ -50,40 +50,50 @@ struct NormParams {
 };
 
 // ---- a thread's 8 consecutive values ----
-// `left` values from p to the row's end: with TAIL and fewer than 8 of them there
-// are `h & 7` (the same for every row), the others are zero.
+// `left` values from p to the row's end.  Where those are fewer than 8 (there are
+// h & 7, the same for every row: kTail) the last 8 of the row are loaded, and the
+// first ones shifted out when they are used: one load for every lane, and no wait
+// between a row's loads (333 x 2111 4.8 -> 4.6 us, backward of 2048 x 1161 13.6 -> 12.5).
+// The values in front may be another lane's, which may be storing them: they are
+// dropped.  kShort: h < 8, a lane per row, value by value.
+enum Tail : int { kNone = 0, kTail = 1, kShort = 2 };
 struct Raw {
   uint4 v;
 };
 
-template <bool TAIL>
+template <int TAIL>
 __device__ __forceinline__ Raw load(const uint16_t* p, int left, int h) {
   Raw r{uint4{0, 0, 0, 0}};
-  if (!TAIL || left >= 8) {
-    __builtin_memcpy(&r.v, p, 16);  // (one load, whatever the address)
-  } else {
-    uint32_t o[4] = {0, 0, 0, 0}, two = 0, one = 0;
-    if (h & 4) __builtin_memcpy(o, p, 8);
-    if (h & 2) __builtin_memcpy(&two, p + (h & 4), 4);
-    if (h & 1) one = p[h & 6];
+  if constexpr (TAIL == kShort) {
+    uint32_t o[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      if ((h & 2) && d == (h & 4) / 2) o[d] = two;
-      if ((h & 1) && d == (h & 6) / 2) o[d] = one;
-    }
+    for (int e = 0; e < 7; ++e)
+      if (e < h) o[e / 2] |= (uint32_t)p[e] << (e % 2 * 16);
     r.v = uint4{o[0], o[1], o[2], o[3]};
+  } else {
+    __builtin_memcpy(&r.v, TAIL ? p + min(left - 8, 0) : p, 16);  // (one load, whatever the address)
   }
   return r;
 }
-__device__ __forceinline__ void widen(const Raw& r, float* f) {
-  const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+template <int TAIL>
+__device__ __forceinline__ void widen(const Raw& r, float* f, int left, int h) {
+  uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+  if (TAIL == kTail && left < 8) {
+    const int out = 8 - (h & 7);
+    if (out & 4) w[0] = w[2], w[1] = w[3], w[2] = w[3] = 0;
+    if (out & 2) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = 0;
+    if (out & 1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_alignbit(e < 3 ? w[e + 1] : 0u, w[e], 16);
+    }
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     f[2 * e] = from_bf16(w[e]);
     f[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
   }
 }
-template <bool TAIL>
+template <int TAIL>
 __device__ __forceinline__ void store(uint16_t* p, const float* f, int left, int h) {
   uint32_t o[4];
 #pragma unroll
@@ -99,7 +109,7 @@ __device__ __forceinline__ void store(uint16_t* p, const float* f, int left, int
   }
 }
 // The weight's values from column c on.
-template <bool TAIL>
+template <int TAIL>
 __device__ __forceinline__ void load_weight(const void* w, int f32, int c, int h, float* f) {
   if (!w) {
 #pragma unroll
@@ -113,7 +123,7 @@ __device__ __forceinline__ void load_weight(const void* w, int f32, int c, int h
       for (int e = 0; e < 8; ++e) f[e] = c + e < h ? p[e] : 0.f;
     }
   } else {
-    widen(load<TAIL>(static_cast<const uint16_t*>(w) + c, h - c, h), f);
+    widen<TAIL>(load<TAIL>(static_cast<const uint16_t*>(w) + c, h - c, h), f, h - c, h);
   }
 }
 
@@ -193,7 +203,7 @@ __device__ __forceinline__ float inverse_power(uint32_t e) {
 }
 
 // L: lanes per row, 0: a workgroup per row.
-template <int OUT, int I, int L, bool TAIL>
+template <int OUT, int I, int L, int TAIL>
 __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
   __shared__ float part[2][2][8];
   __shared__ float most_y[OUT == kInt8 ? 2 : 1][8];
@@ -221,10 +231,10 @@ __global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
     for (int i = 0; i < I; ++i) {
       const int c = (i * lanes + own) * 8;
       if (c < p.h) {
-        widen(xr[i], z[i]);
+        widen<TAIL>(xr[i], z[i], p.h - c, p.h);
         if (res) {
           float f[8];
-          widen(rr[i], f);
+          widen<TAIL>(rr[i], f, p.h - c, p.h);
 #pragma unroll
           for (int e = 0; e < 8; ++e) z[i][e] += f[e];
         }
@@ -369,19 +379,21 @@ struct BackwardParams {
 // Few rows: dw's columns are summed beside the rows.  A tile's rows are read by
 // one workgroup, so the time grows with them, while the partials' way pays a
 // second launch and their traffic (us beside : by partials): 17 x 1161 3.3 : 5.8,
-// 512 x 4096 5.8 : 11.6, 1000 x 2111 9.6 : 14.3, 1024 x 4096 13.9 : 12.7, 2048 x
+// 512 x 4096 5.3 : 11.6, 1000 x 2111 9.6 : 12.1, 1024 x 4096 13.9 : 12.7, 2048 x
 // 2048 21.6 : 12.2.
 constexpr int kFewRows = 768;
 
-// dw's columns 32 tile .. 32 tile + 31: a wave takes 16 rows at a time (64 columns
-// and 8 rows: 517 x 1161 8.4 us for 6.0).
+// dw's columns c0 .. c0 + 31: a wave takes 16 rows at a time (64 columns and 8 rows:
+// 517 x 1161 8.4 us for 6.0).  Where H is no multiple of 32 the last tile starts
+// early and some columns are summed twice, to the same bits: a tail's code for
+// one workgroup cost 517 x 1161 a microsecond, mostly to fetch it.
 constexpr int kTileColumns = 32;
-template <bool TAIL>
-__device__ __forceinline__ void sum_columns(const BackwardParams& p, int tile, float (*part)[kTileColumns]) {
+template <int TAIL>
+__device__ __forceinline__ void sum_columns(const BackwardParams& p, int c0, float (*part)[kTileColumns]) {
   constexpr int LPR = kTileColumns / 8, RPW = 64 / LPR;
   constexpr int U = kFewRows / (8 * RPW);  // 8 waves have all rows in flight at once
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-  const int c = tile * kTileColumns + (lane % LPR) * 8, n = p.h - c;  // (n <= 0: none)
+  const int c = c0 + (lane % LPR) * 8, n = p.h - c;  // (n <= 0: none)
   const int step = waves * RPW;
   float dw[8];
 #pragma unroll
@@ -404,8 +416,8 @@ __device__ __forceinline__ void sum_columns(const BackwardParams& p, int tile, f
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float z[8], g[8];
-        widen(x[u], z);
-        widen(d[u], g);
+        widen<TAIL>(x[u], z, n, p.h);
+        widen<TAIL>(d[u], g, n, p.h);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[e] = __builtin_fmaf(g[e], z[e] * r[u], dw[e]);
       }
@@ -420,20 +432,23 @@ __device__ __forceinline__ void sum_columns(const BackwardParams& p, int tile, f
     for (int e = 0; e < 8; ++e) part[wave][lane * 8 + e] = dw[e];
   }
   __syncthreads();
-  if (tid < kTileColumns && tile * kTileColumns + tid < p.h) {
+  if (tid < kTileColumns && c0 + tid < p.h) {
     float v = part[0][tid];
     for (int w = 1; w < waves; ++w) v += part[w][tid];
-    p.dw[tile * kTileColumns + tid] = v;
+    p.dw[c0 + tid] = v;
   }
 }
 
-template <int I, int L, bool TAIL>
+template <int I, int L, int TAIL>
 __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams p) {
   __shared__ float part[2][8];
   __shared__ float columns[8][kTileColumns];
   __shared__ float together[L ? 512 : 1][8];  // dw of the rows' lanes
   if ((int)blockIdx.x < p.columns) {
-    sum_columns<TAIL>(p, blockIdx.x, columns);
+    if (L == 16 && p.h < kTileColumns)
+      sum_columns<TAIL>(p, 0, columns);
+    else
+      sum_columns<kNone>(p, min((int)blockIdx.x * kTileColumns, p.h - kTileColumns), columns);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
@@ -452,15 +467,15 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
   for (int64_t row = (int64_t)group * rows + (L ? tid / (L ? L : 1) : 0); row < p.t;
        row += (int64_t)groups * rows, turn ^= 1) {
     float z[I][8], d[I][8];
-    Raw ds[I];
+    Raw xr[I], dr[I], ds[I];
     const float r = p.rstd[row];
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int c = (i * lanes + own) * 8;
       if (c < p.h) {
-        widen(load<TAIL>(p.x + row * p.ldx + c, p.h - c, p.h), z[i]);
-        widen(load<TAIL>(p.dy + row * p.lddy + c, p.h - c, p.h), d[i]);
+        xr[i] = load<TAIL>(p.x + row * p.ldx + c, p.h - c, p.h);
+        dr[i] = load<TAIL>(p.dy + row * p.lddy + c, p.h - c, p.h);
         if (p.dsum) ds[i] = load<TAIL>(p.dsum + row * p.ldds + c, p.h - c, p.h);
       }
     }
@@ -468,6 +483,8 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
     for (int i = 0; i < I; ++i) {
       const int c = (i * lanes + own) * 8;
       if (c < p.h) {
+        widen<TAIL>(xr[i], z[i], p.h - c, p.h);
+        widen<TAIL>(dr[i], d[i], p.h - c, p.h);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float n = z[i][e] * r;
@@ -496,7 +513,7 @@ __global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = r * __builtin_fmaf(-z[i][e], mean, d[i][e]);
         if (p.dsum) {
-          widen(ds[i], f);
+          widen<TAIL>(ds[i], f, p.h - c, p.h);
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] += f[e];
         }
@@ -578,10 +595,13 @@ template <int OUT, int I, int L>
 hipError_t launch_norm(const NormParams& p, int waves, hipStream_t stream) {
   const int groups = ceil_div(p.t, L ? 64 * waves / (L ? L : 1) : 1);
   const int grid = groups < kMostGroups ? groups : kMostGroups;
-  if ((OUT == kBf16 || OUT == kInt8) && p.h % 8)  // (FP8's rows are whole groups of 128)
-    norm_kernel<OUT, I, L, OUT == kBf16 || OUT == kInt8><<<grid, 64 * waves, 0, stream>>>(p);
+  constexpr bool kAny = OUT == kBf16 || OUT == kInt8;  // (FP8's rows are whole groups of 128)
+  if (kAny && L == 16 && p.h < 8)
+    norm_kernel<OUT, I, L, kAny && L == 16 ? kShort : kNone><<<grid, 64 * waves, 0, stream>>>(p);
+  else if (kAny && p.h % 8)
+    norm_kernel<OUT, I, L, kAny ? kTail : kNone><<<grid, 64 * waves, 0, stream>>>(p);
   else
-    norm_kernel<OUT, I, L, false><<<grid, 64 * waves, 0, stream>>>(p);
+    norm_kernel<OUT, I, L, kNone><<<grid, 64 * waves, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -598,10 +618,12 @@ hipError_t launch_out(const NormParams& p, hipStream_t stream) {
 
 template <int I, int L>
 hipError_t launch_backward(const BackwardParams& p, int grid, int waves, hipStream_t stream) {
-  if (p.h % 8)
-    norm_backward_kernel<I, L, true><<<grid, 64 * waves, 0, stream>>>(p);
+  if (L == 16 && p.h < 8)
+    norm_backward_kernel<I, L, L == 16 ? kShort : kNone><<<grid, 64 * waves, 0, stream>>>(p);
+  else if (p.h % 8)
+    norm_backward_kernel<I, L, kTail><<<grid, 64 * waves, 0, stream>>>(p);
   else
-    norm_backward_kernel<I, L, false><<<grid, 64 * waves, 0, stream>>>(p);
+    norm_backward_kernel<I, L, kNone><<<grid, 64 * waves, 0, stream>>>(p);
   return hipGetLastError();
 }
 

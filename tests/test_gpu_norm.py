@@ -482,3 +482,35 @@ def test_native_arguments_refuse_as_the_binding_does(dg):
     assert refused == len(cases) - 1  # (an eps past fp32 packs as an infinity, which the library refuses)
     with pytest.raises(dg.DGError):
         dg.rmsnorm_bf16(x, w, torch.empty_like(x), 1e39)
+
+
+@pytest.mark.parametrize("h", [1, 2, 3, 5, 7, 9, 15, 31, 33, 47, 63, 65, 130, 257, 513, 519, 1161, 4097, 8199])
+@pytest.mark.parametrize("t,gap", [(3, 0), (3, 5), (70, 0), (800, 1)])
+def test_rows_of_every_tail(dg, t, h, gap):
+    """Rows that end 1 to 7 values past a multiple of 8, close to each other: nothing beside them is read or written."""
+    say(f"norm tails {t}x{h} gap {gap}")
+    x, r, w = inputs(t, h, True, BF16, 13, h + gap, 3)
+    space = torch.full((t * (h + gap) + 8,), 7.0, dtype=BF16, device="cuda")
+    out = space[4:4 + t * (h + gap)].view(t, h + gap)[:, :h]
+    total, rstd = torch.empty((t, h), dtype=BF16, device="cuda"), torch.empty(t, device="cuda")
+    dg.rmsnorm_bf16(x, w, out, 1e-6, r, total, rstd)
+    z, _, y = ref64(x, r, w, 1e-6)
+    within(out, y, (2.0 ** -8 + 2.0 ** -16) * y.abs(), "y")
+    within(total, z, (2.0 ** -8 + 2.0 ** -24) * z.abs(), "sum")
+    q, s = torch.full((t * h + 8,), 55, dtype=torch.int8, device="cuda"), torch.empty(t, device="cuda")
+    dg.rmsnorm_quantize_int8(x, w, q[:t * h].view(t, h), s, 1e-6, r)
+    se = s.to(F64)[:, None]
+    within(q[:t * h].view(t, h).to(F64) * se, y, 0.5 * se + 2.0 ** -15 * y.abs(), "int8")
+    assert (q[t * h:] == 55).all()
+    dy = inputs(t, h, False, None, 14, h + gap, 1)[0]
+    dw = torch.full((h + 8,), 9.0, device="cuda")
+    back = torch.full_like(space, 7.0)
+    dx = back[4:4 + t * (h + gap)].view(t, h + gap)[:, :h]
+    dg.rmsnorm_bf16_backward(dy, x, w, rstd, dx, dw[:h], r)
+    wx, bx, ww, bw = backward64(dy, x, w, rstd, r)
+    within(dx, wx, bx, "dx")
+    within(dw[:h], ww, bw, "dw")
+    assert (dw[h:] == 9).all()
+    for buf, rows in ((space, out), (back, dx)):
+        rows.fill_(7.0)
+        assert (buf == 7).all()
