@@ -391,7 +391,7 @@ constexpr int kTileColumns = 32;
 template <int TAIL>
 __device__ __forceinline__ void sum_columns(const BackwardParams& p, int c0, float (*part)[kTileColumns]) {
   constexpr int LPR = kTileColumns / 8, RPW = 64 / LPR;
-  constexpr int U = kFewRows / (8 * RPW);  // 8 waves have all rows in flight at once
+  constexpr int U = kFewRows / (8 * RPW);  // 8 waves or more have all rows in flight at once
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int c = c0 + (lane % LPR) * 8, n = p.h - c;  // (n <= 0: none)
   const int step = waves * RPW;
@@ -440,9 +440,9 @@ __device__ __forceinline__ void sum_columns(const BackwardParams& p, int c0, flo
 }
 
 template <int I, int L, int TAIL>
-__global__ __launch_bounds__(512) void norm_backward_kernel(const BackwardParams p) {
-  __shared__ float part[2][8];
-  __shared__ float columns[8][kTileColumns];
+__global__ __launch_bounds__(I == 2 ? 1024 : 512) void norm_backward_kernel(const BackwardParams p) {
+  __shared__ float part[2][16];
+  __shared__ float columns[16][kTileColumns];
   __shared__ float together[L ? 512 : 1][8];  // dw of the rows' lanes
   if ((int)blockIdx.x < p.columns) {
     if (L == 16 && p.h < kTileColumns)
@@ -581,11 +581,18 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 struct Shape {
   int pieces, waves, lanes;
 };
-Shape shape_of(int h) {
+Shape shape_of(int h) {  // forward
   if (h <= 512) return Shape{1, 4, h <= 128 ? 16 : h <= 256 ? 32 : 64};
   const int units = ceil_div(h, 512);  // columns of a wave's piece
   const int pieces = units <= 8 ? 1 : units <= 16 ? 2 : 4;
   return Shape{pieces, ceil_div(units, pieces), 0};
+}
+
+// Backward: a thread holds more (dw, and the weight, beside a row), so long rows have
+// up to 16 waves instead of 4 pieces (8192 x 12288: 166 us with 4, 151 with 2).
+Shape backward_shape(int h) {
+  const Shape s = shape_of(h);
+  return s.pieces < 4 ? s : Shape{2, ceil_div(h, 1024), 0};
 }
 
 // (a launch holds fewer than 2^32 threads: more rows than that go several to a workgroup)
@@ -632,8 +639,7 @@ hipError_t launch_rows(const BackwardParams& p, const Shape& s, int grid, hipStr
   if (s.lanes == 32) return launch_backward<1, 32>(p, grid, 8, stream);
   if (s.lanes == 64) return launch_backward<1, 64>(p, grid, 8, stream);
   if (s.pieces == 1) return launch_backward<1, 0>(p, grid, s.waves, stream);
-  if (s.pieces == 2) return launch_backward<2, 0>(p, grid, s.waves, stream);
-  return launch_backward<4, 0>(p, grid, s.waves, stream);
+  return launch_backward<2, 0>(p, grid, s.waves, stream);
 }
 
 bool bad_weight(const void* w, int type) { return w && type != DG_TYPE_BF16 && type != DG_TYPE_F32; }
@@ -680,15 +686,17 @@ dg_status fp8(const dg_norm* in, void* q, void* s, int t, int h, bool ue8m0, hip
 }
 
 // Workgroups of the backward pass.  Each keeps a partial dw of h values, 4 bytes
-// written and read again: 512 of them, and up to 4096 waves where rows are few
-// waves long and every workgroup still has 8 rows (16384 x 1024: 39 us with 512, 24
-// with 2048; 4096 x 1024: 14 and 16).
+// written and read again.  As many for each of 256 CUs as give it some 16 waves, and
+// no more than it holds at once, since all should end together (two pieces: 2 of 5
+// to 8 waves; 8192 x 7168: 90 us with 512, 123 with 585; 16384 x 4096: 99 with 512, 108
+// with 768; 16384 x 1024: 39 with 512, 24 with 2048), and above 512 only where each
+// still has 8 rows (4096 x 1024: 16 with 2048, 14.6 with 512).
 int backward_parts(int t, int h) {
-  const Shape s = shape_of(h);
-  int parts = t / 8 < 512 ? 512 : t / 8;
-  const int most = s.lanes ? 512 : 4096 / s.waves;
-  if (parts > most) parts = most;
-  return t < parts ? t : parts;
+  const Shape s = backward_shape(h);
+  int each = 2;  // workgroups for a CU
+  if (!s.lanes) each = s.waves > 8 ? 1 : s.pieces > 1 ? 2 : 16 / s.waves;
+  while (each > 2 && t < 8 * 256 * each) --each;
+  return t < 256 * each ? t : 256 * each;
 }
 
 // Whether the memory of two matrices' rows may meet.
@@ -780,14 +788,14 @@ dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x,
   p.lddx = ld_dx;
   p.t = t;
   p.h = h;
-  Shape s = shape_of(h);
+  Shape s = backward_shape(h);
   const int parts = backward_parts(t, h);
   int grid = parts;
   (void)hipGetLastError();
   if (beside) {
     const int columns = ceil_div(h, kTileColumns);
     p.columns = columns;
-    s.waves = 8;  // (the rows' workgroups too, where they share the launch)
+    if (s.waves < 8) s.waves = 8;  // (the rows' workgroups too, where they share the launch)
     const int rows = !dx ? 0 : s.lanes ? ceil_div(t, 512 / s.lanes) : t;
     grid = columns + rows;
     if (dx && (overlap(dx, ld_dx, dy, ld_dy, t, h) || overlap(dx, ld_dx, x, ld_x, t, h))) {
