@@ -33,7 +33,7 @@ using bf16::to_bf16;
 
 enum Out : int { kBf16 = 0, kFp8 = 1, kFp8Ue8m0 = 2, kInt8 = 3 };
 
-constexpr int kMaxHidden = 16384;  // what 8 waves hold in registers
+constexpr int kMaxHidden = 16384;  // what 16 waves hold in two pieces
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
 
 struct NormParams {
@@ -204,9 +204,9 @@ __device__ __forceinline__ float inverse_power(uint32_t e) {
 
 // L: lanes per row, 0: a workgroup per row.
 template <int OUT, int I, int L, int TAIL>
-__global__ __launch_bounds__(512) void norm_kernel(const NormParams p) {
-  __shared__ float part[2][2][8];
-  __shared__ float most_y[OUT == kInt8 ? 2 : 1][8];
+__global__ __launch_bounds__(I == 2 ? 1024 : 512) void norm_kernel(const NormParams p) {
+  __shared__ float part[2][2][16];
+  __shared__ float most_y[OUT == kInt8 ? 2 : 1][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int lanes = L ? L : blockDim.x, own = L ? tid % (L ? L : 1) : tid;  // of the row; this thread among them
   const int rows = L ? blockDim.x / (L ? L : 1) : 1;
@@ -578,21 +578,17 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Lanes per row (L), or pieces per thread (I) and waves (W) of a row of h columns.
+// Two pieces keep twice as much in flight as one (8192 x 7168 into INT8: 101 us with
+// one, 85 with two) and let up to 16 waves hold any row; four in 8 waves are
+// slower (8192 x 12288 into FP8: 205 us with four, 130 with two; backward 166 and 151).
 struct Shape {
   int pieces, waves, lanes;
 };
-Shape shape_of(int h) {  // forward
+Shape shape_of(int h) {
   if (h <= 512) return Shape{1, 4, h <= 128 ? 16 : h <= 256 ? 32 : 64};
   const int units = ceil_div(h, 512);  // columns of a wave's piece
-  const int pieces = units <= 8 ? 1 : units <= 16 ? 2 : 4;
+  const int pieces = units <= 8 ? 1 : 2;
   return Shape{pieces, ceil_div(units, pieces), 0};
-}
-
-// Backward: a thread holds more (dw, and the weight, beside a row), so long rows have
-// up to 16 waves instead of 4 pieces (8192 x 12288: 166 us with 4, 151 with 2).
-Shape backward_shape(int h) {
-  const Shape s = shape_of(h);
-  return s.pieces < 4 ? s : Shape{2, ceil_div(h, 1024), 0};
 }
 
 // (a launch holds fewer than 2^32 threads: more rows than that go several to a workgroup)
@@ -619,8 +615,7 @@ hipError_t launch_out(const NormParams& p, hipStream_t stream) {
   if (s.lanes == 32) return launch_norm<OUT, 1, 32>(p, s.waves, stream);
   if (s.lanes == 64) return launch_norm<OUT, 1, 64>(p, s.waves, stream);
   if (s.pieces == 1) return launch_norm<OUT, 1, 0>(p, s.waves, stream);
-  if (s.pieces == 2) return launch_norm<OUT, 2, 0>(p, s.waves, stream);
-  return launch_norm<OUT, 4, 0>(p, s.waves, stream);
+  return launch_norm<OUT, 2, 0>(p, s.waves, stream);
 }
 
 template <int I, int L>
@@ -692,7 +687,7 @@ dg_status fp8(const dg_norm* in, void* q, void* s, int t, int h, bool ue8m0, hip
 // with 768; 16384 x 1024: 39 with 512, 24 with 2048), and above 512 only where each
 // still has 8 rows (4096 x 1024: 16 with 2048, 14.6 with 512).
 int backward_parts(int t, int h) {
-  const Shape s = backward_shape(h);
+  const Shape s = shape_of(h);
   int each = 2;  // workgroups for a CU
   if (!s.lanes) each = s.waves > 8 ? 1 : s.pieces > 1 ? 2 : 16 / s.waves;
   while (each > 2 && t < 8 * 256 * each) --each;
@@ -788,7 +783,7 @@ dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x,
   p.lddx = ld_dx;
   p.t = t;
   p.h = h;
-  Shape s = backward_shape(h);
+  Shape s = shape_of(h);
   const int parts = backward_parts(t, h);
   int grid = parts;
   (void)hipGetLastError();
