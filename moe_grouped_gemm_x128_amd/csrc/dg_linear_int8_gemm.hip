@@ -58,8 +58,12 @@ __global__ __launch_bounds__(256) void splitk_int8_kernel(const GemmParams p, co
 }
 
 // Rows as INT8: s = amax / 127 (1 for a row of zeros), codes the nearest whole
-// numbers to x / s, ties to even.  A workgroup takes a row and reads it twice,
-// the second time from the caches (a row of up to 128 K values is at most 512 KB).
+// numbers to x / s, ties to even.  L lanes take a row and read it twice, the second
+// time from the caches (a row of up to 128 K values is at most 512 KB).  Short rows
+// are bound by the chain to a row's largest value, so they have fewer lanes and
+// go several to a workgroup: 16 lanes up to 1 KB (bf16, us with 16, 64, 256: 131072 x
+// 128 14, 34, 97; 32768 x 512 12, 15, 31), 64 up to 4 KB where rows are many (16384
+// x 1024 13, 12, 20; 16384 x 2048 27, 23, 26), 256 beyond (7168 x 4096 37, 23, 20).
 template <bool F32>
 __device__ __forceinline__ float value(const void* x, int64_t i) {
   if constexpr (F32)
@@ -84,18 +88,18 @@ __device__ __forceinline__ int code(float x, const codec::GroupRecip& g) {
   return (int)__builtin_rintf(fminf(fmaxf(x * g.k * g.r, -127.f), 127.f));
 }
 
-template <bool F32, bool VEC>
+template <bool F32, bool VEC, int L>
 __global__ __launch_bounds__(256) void quantize_int8_kernel(const void* x, int64_t ldx, int8_t* q, float* s, int m, int k) {
   __shared__ float part[2][4];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, own = tid % L;
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < m; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = blockIdx.x * (256LL / L) + tid / L; row < m; row += gridDim.x * (256LL / L), turn ^= 1) {
     const int64_t at = row * ldx;
     float most = 0.f;
     bool nan = false;
     if constexpr (VEC) {
 #pragma unroll 4
-      for (int c = tid * 4; c < k; c += 1024) {
+      for (int c = own * 4; c < k; c += L * 4) {
         float f[4];
         value4<F32>(x, at + c, f);
 #pragma unroll
@@ -106,7 +110,7 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(const void* x, int64
       }
     } else {
 #pragma unroll 4
-      for (int c = tid; c < k; c += 256) {
+      for (int c = own; c < k; c += L) {
         const float f = value<F32>(x, at + c);
         most = fmaxf(most, fabsf(f));
         nan |= f != f;
@@ -114,18 +118,20 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(const void* x, int64
     }
     most = nan ? __builtin_inff() : most;
 #pragma unroll
-    for (int d = 32; d > 0; d /= 2) most = fmaxf(most, __shfl_xor(most, d, 64));
-    if ((tid & 63) == 0) part[turn][tid >> 6] = most;
-    __syncthreads();
-    most = fmaxf(fmaxf(part[turn][0], part[turn][1]), fmaxf(part[turn][2], part[turn][3]));
+    for (int d = (L < 64 ? L : 64) / 2; d > 0; d /= 2) most = fmaxf(most, __shfl_xor(most, d, 64));
+    if constexpr (L > 64) {
+      if ((tid & 63) == 0) part[turn][tid >> 6] = most;
+      __syncthreads();
+      most = fmaxf(fmaxf(part[turn][0], part[turn][1]), fmaxf(part[turn][2], part[turn][3]));
+    }
     const float scale = most == 0.f ? 1.f : most / 127.f;
     const codec::GroupRecip g = codec::group_recip(scale);
     // (a row with a NaN or an infinity: a NaN scale)
-    if (tid == 0) s[row] = most < __builtin_inff() ? scale : __builtin_nanf("");
+    if (own == 0) s[row] = most < __builtin_inff() ? scale : __builtin_nanf("");
     int8_t* out = q + row * k;
     if constexpr (VEC) {
 #pragma unroll 4
-      for (int c = tid * 4; c < k; c += 1024) {
+      for (int c = own * 4; c < k; c += L * 4) {
         float f[4];
         value4<F32>(x, at + c, f);
         *reinterpret_cast<uint32_t*>(out + c) = (uint32_t)(code(f[0], g) & 0xff) | ((uint32_t)(code(f[1], g) & 0xff) << 8) |
@@ -133,9 +139,24 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(const void* x, int64
       }
     } else {
 #pragma unroll 4
-      for (int c = tid; c < k; c += 256) out[c] = (int8_t)code(value<F32>(x, at + c), g);
+      for (int c = own; c < k; c += L) out[c] = (int8_t)code(value<F32>(x, at + c), g);
     }
   }
+}
+
+template <bool F32, bool VEC>
+hipError_t launch_quantize(const void* x, int64_t ldx, int8_t* q, float* s, int m, int k, hipStream_t stream) {
+  const int64_t bytes = (int64_t)k * (F32 ? 4 : 2);
+  const int lanes = bytes <= 1024 ? 16 : bytes <= 4096 && m >= 1024 ? 64 : 256;
+  const int64_t groups = ((int64_t)m * lanes + 255) / 256;
+  const int grid = (int)(groups < (1 << 20) ? groups : 1 << 20);
+  if (lanes == 16)
+    quantize_int8_kernel<F32, VEC, 16><<<grid, 256, 0, stream>>>(x, ldx, q, s, m, k);
+  else if (lanes == 64)
+    quantize_int8_kernel<F32, VEC, 64><<<grid, 256, 0, stream>>>(x, ldx, q, s, m, k);
+  else
+    quantize_int8_kernel<F32, VEC, 256><<<grid, 256, 0, stream>>>(x, ldx, q, s, m, k);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -166,16 +187,9 @@ hipError_t launch_quantize_int8(const void* x, bool f32, int64_t ldx, int8_t* q,
                                 hipStream_t stream) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(x);
   const bool vec = k % 4 == 0 && (m == 1 || ldx % 4 == 0) && at % (f32 ? 16 : 8) == 0 && reinterpret_cast<uintptr_t>(q) % 4 == 0;
-  const int grid = m < (1 << 20) ? m : 1 << 20;
-  if (f32 && vec)
-    quantize_int8_kernel<true, true><<<grid, 256, 0, stream>>>(x, ldx, q, s, m, k);
-  else if (f32)
-    quantize_int8_kernel<true, false><<<grid, 256, 0, stream>>>(x, ldx, q, s, m, k);
-  else if (vec)
-    quantize_int8_kernel<false, true><<<grid, 256, 0, stream>>>(x, ldx, q, s, m, k);
-  else
-    quantize_int8_kernel<false, false><<<grid, 256, 0, stream>>>(x, ldx, q, s, m, k);
-  return hipGetLastError();
+  if (f32)
+    return vec ? launch_quantize<true, true>(x, ldx, q, s, m, k, stream) : launch_quantize<true, false>(x, ldx, q, s, m, k, stream);
+  return vec ? launch_quantize<false, true>(x, ldx, q, s, m, k, stream) : launch_quantize<false, false>(x, ldx, q, s, m, k, stream);
 }
 
 }  // namespace dg

@@ -249,3 +249,28 @@ def test_refusals_of_the_binding(dg):
         dg.gemm_int8_nt_epilogue((a, sa), (b, sb), c, activation="tanh")
     with pytest.raises(dg.DGError):
         dg.gemm_int8_nt_epilogue((a[:, :40], sa), (b[:, :40], sb), c)
+
+
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("k", [8, 255, 256, 257, 500, 512, 513, 1000, 1024, 1025, 2048, 2049])
+@pytest.mark.parametrize("m", [1, 17, 1023, 1025])
+def test_quantiser_of_short_rows(dg, kind, k, m):
+    """Rows of 16, 64 and 256 lanes, with one that is all zeros and one with a NaN."""
+    say(f"int8 quantiser {m}x{k} {kind}")
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn((m, k), generator=g, device="cuda").to(kind)
+    if m > 9:
+        x[4] = 0
+        x[9, k - 1] = float("nan")
+    q, s = torch.full((m * k + 8,), 77, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+    dg.dg_quantize_int8_rows(x, q[:m * k].view(m, k), s)
+    assert (q[m * k:] == 77).all()
+    if m > 9:
+        assert s[4] == 1 and (q[4 * k:5 * k] == 0).all() and s[9].isnan()
+    fine = [i for i in range(m) if i != 9]
+    x, q, s = x[fine], q[:m * k].view(m, k)[fine], s[fine]
+    need = x.to(F64).abs().amax(1) / 127
+    need = torch.where(need == 0, torch.ones_like(need), need)
+    assert ((s.to(F64) - need).abs() <= 2.0 ** -24 * need).all()
+    assert ((q.to(F64) * s.to(F64)[:, None] - x.to(F64)).abs() <=
+            0.5 * s.to(F64)[:, None] + 2.0 ** -22 * x.to(F64).abs()).all()
