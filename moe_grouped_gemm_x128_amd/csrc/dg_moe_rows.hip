@@ -461,6 +461,7 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(const CombineBack
     if (!p.dweights) continue;  // (uniform over the workgroup)
 #pragma unroll
     for (int j = 0; j < K; ++j) {
+      if (j >= p.top_k) break;
       float v = dot[j];
 #pragma unroll
       for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d, 64);
