@@ -274,3 +274,26 @@ def test_quantiser_of_short_rows(dg, kind, k, m):
     assert ((s.to(F64) - need).abs() <= 2.0 ** -24 * need).all()
     assert ((q.to(F64) * s.to(F64)[:, None] - x.to(F64)).abs() <=
             0.5 * s.to(F64)[:, None] + 2.0 ** -22 * x.to(F64).abs()).all()
+
+
+@pytest.mark.parametrize("m", [3, 600])
+def test_operands_past_32_bits(dg, m):
+    """Rows 4 MB apart, 2.5 GB in all, in either operand; a quantiser's rows 2 GB apart."""
+    say(f"int8 rows far apart {m}")
+    k, stride, n = 256, 1 << 22, 600
+    (a, sa), (b, sb) = operands(m, n, k)
+    far = torch.zeros((n - 1) * stride + k, dtype=torch.int8, device="cuda").as_strided((n, k), (stride, 1))
+    far.copy_(b)
+    c, d = torch.empty((m, n), dtype=BF16, device="cuda"), torch.empty((m, n), dtype=BF16, device="cuda")
+    dg.gemm_int8_nt_epilogue((a, sa), (b, sb), c)
+    dg.gemm_int8_nt_epilogue((a, sa), (far, sb), d)
+    assert torch.equal(c, d)
+    c, d = torch.empty((n, m), dtype=BF16, device="cuda"), torch.empty((n, m), dtype=BF16, device="cuda")
+    dg.gemm_int8_nt_epilogue((b, sb), (a, sa), c)
+    dg.gemm_int8_nt_epilogue((far, sb), (a, sa), d)
+    assert torch.equal(c, d)
+    x = torch.randn((3, 500), device="cuda").to(BF16)
+    rows = torch.zeros(2 * ((1 << 30) + 8) + 500, dtype=BF16, device="cuda").as_strided((3, 500), ((1 << 30) + 8, 1))
+    rows.copy_(x)
+    for p, q in zip(dg.quantize_int8_rows(rows), dg.quantize_int8_rows(x)):
+        assert torch.equal(p, q)

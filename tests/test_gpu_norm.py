@@ -514,3 +514,30 @@ def test_rows_of_every_tail(dg, t, h, gap):
     for buf, rows in ((space, out), (back, dx)):
         rows.fill_(7.0)
         assert (buf == 7).all()
+
+
+def test_offsets_past_32_bits(dg):
+    """Rows two GB apart, forward and backward."""
+    t, h, stride = 4, 1000, (1 << 30) + 8
+    say("norm rows 2 GB apart")
+    far = torch.zeros((t - 1) * stride + h, dtype=BF16, device="cuda").as_strided((t, h), (stride, 1))
+    x, r, w = inputs(t, h, True, F32, 15)
+    far.copy_(x)
+    out, near = torch.empty_like(x), torch.empty_like(x)
+    rstd = torch.empty(t, device="cuda")
+    dg.rmsnorm_bf16(x, w, near, 1e-6, r, rstd=rstd)
+    dg.rmsnorm_bf16(far, w, out, 1e-6, r)
+    assert torch.equal(out, near)
+    q, s, q2, s2 = (torch.empty(n, dtype=d, device="cuda") for n, d in (((t, h), torch.int8), (t, F32)) * 2)
+    dg.rmsnorm_quantize_int8(x, w, q, s)
+    dg.rmsnorm_quantize_int8(far, w, q2, s2)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    dx, dw, dw2 = torch.empty_like(x), torch.empty(h, device="cuda"), torch.empty(h, device="cuda")
+    dg.rmsnorm_bf16_backward(r, x, w, rstd, dx, dw)
+    dg.rmsnorm_bf16_backward(r, far, w, rstd, out, dw2)
+    assert torch.equal(out, dx) and torch.equal(dw, dw2)
+    dg.rmsnorm_bf16(x, w, far, 1e-6, r)
+    assert torch.equal(far, near)
+    far.copy_(x)
+    dg.rmsnorm_bf16_backward(r, x, w, rstd, far)
+    assert torch.equal(far, dx)
