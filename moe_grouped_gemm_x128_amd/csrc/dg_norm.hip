@@ -802,6 +802,9 @@ dg_status dg_rmsnorm_bf16_backward(const void* dy, int64_t ld_dy, const void* x,
   }
   if (launch_rows(p, s, grid, stream) != hipSuccess) return DG_ERROR_LAUNCH;
   if (p.partial) {
+    // (many partials are a long chain for a column: more slices; few: whole lines. In
+    // all, with 64 columns and 16: 16384 x 1024, 2048 partials, 31.5 us and 29.9; 1024 x
+    // 4096, 512 partials, 13.3 and 14.6)
     if (parts > 512)
       norm_weight_sum_kernel<16><<<ceil_div(h, 16), 1024, 0, stream>>>(p.partial, dweight, parts, h);
     else
