@@ -437,7 +437,9 @@ dg_status dg_moe_few_tokens_bf16(const void* x, const float* logits, int32_t* id
  * three (with the same stride); no other overlap.  A row must keep its sum of
  * squares finite in fp32: one that does not (or holds a NaN, or zeros alone
  * where eps is 0) gets NaN scales.
- * The weight and y must be finite; scales below 2^-126 are rounded up. */
+ * The weight and y must be finite; scales below 2^-126 are rounded up.
+ * y's products are (z r) w, for INT8 (z w) r unless a row's largest |z w| lies
+ * outside 2^-100 .. 2^120. */
 typedef struct {
   const void* x;        /* [T,H] bf16                                        */
   int64_t ld_x;
@@ -466,7 +468,8 @@ dg_status dg_rmsnorm_quantize_fp8_1x128_ue8m0(const dg_norm* in, void* q, int32_
                                               hipStream_t stream);
 
 /* q [T,H] int8, s [T] fp32: the operand A of dg_gemm_int8_nt_epilogue (which needs
- * H % 16 == 0; this call takes any H). */
+ * H % 16 == 0; this call takes any H).  Codes and scales are those of
+ * dg_quantize_int8_rows on the fp32 y (but for scales below 2^-126). */
 dg_status dg_rmsnorm_quantize_int8(const dg_norm* in, void* q, float* s, int tokens, int hidden, hipStream_t stream);
 
 /* Backward pass.  With dy [T,H] bf16, the gradient of y (of the values that were
