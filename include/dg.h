@@ -461,7 +461,8 @@ dg_status dg_rmsnorm_bf16(const dg_norm* in, void* y, int64_t ld_y, int tokens, 
  * [T,ceil(H/512)].  y's few ulp of error and the product with the reciprocal
  * of s let a code differ from exact evaluation only where y / s lies within about
  * 2^-20 (relative) of the midpoint between two e4m3 values; scales match to the
- * same margin.  H % 128 == 0.  A NaN scale is E = 255 in UE8M0. */
+ * same margin.  UE8M0 codes and scales are dg_quantize_fp8_1x128_ue8m0's on the fp32
+ * y.  H % 128 == 0.  A NaN scale is E = 255 in UE8M0. */
 dg_status dg_rmsnorm_quantize_fp8_1x128(const dg_norm* in, void* q, float* s, int tokens, int hidden,
                                         hipStream_t stream);
 dg_status dg_rmsnorm_quantize_fp8_1x128_ue8m0(const dg_norm* in, void* q, int32_t* s, int tokens, int hidden,

@@ -209,12 +209,13 @@ __device__ __forceinline__ Factor int8_factor(float amax) {
   const float r = __builtin_amdgcn_rcpf(d);
   return Factor{s, k, __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r)};
 }
-// The least E with 2^(E - 127) >= amax / 448 = amax / (1.75 2^8), read off amax's
-// fields, and 2^(127 - E).
+// codec::ue8m0_code, the least E with 2^(E - 127) >= RN(amax / 448), read off amax's
+// fields: amax / 448 is amax / (1.75 2^8).  (The one value whose subnormal quotient is
+// rounded down to a power is 0x4600001.  Checked for every finite amax.)  And 2^(127 - E).
 __device__ __forceinline__ uint32_t power_of(float amax) {
   const uint32_t b = __float_as_uint(amax);
   if (b == 0) return 127;
-  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u && b != 0x4600001u ? 1 : 0);
   return (uint32_t)max(e, 0);
 }
 __device__ __forceinline__ float inverse_power(uint32_t e) {

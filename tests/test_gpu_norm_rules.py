@@ -65,6 +65,35 @@ def test_int8_where_the_products_leave_the_range(dg, h, exponent):  # noqa: F811
     assert torch.equal(s, s2) and torch.equal(q, q2)
 
 
+@pytest.mark.parametrize("t,h", ROWS)
+@pytest.mark.parametrize("residual,weight", KINDS)
+def test_packed_fp8_is_the_quantiser_s(dg, t, h, residual, weight):  # noqa: F811
+    say(f"norm ue8m0 rule {t}x{h}")
+    x, r, w = inputs(t, h, residual, weight, 21)
+    q, q2 = (torch.zeros((t, h), dtype=torch.uint8, device="cuda") for _ in range(2))
+    s, s2 = (torch.zeros((t, (h + 511) // 512), dtype=torch.int32, device="cuda") for _ in range(2))
+    z, rs, wf = normed(lambda rstd: dg.rmsnorm_quantize_fp8_1x128(x, w, q, s, 1e-6, r, None, rstd), x, r, w)
+    dg.dg_quantize_fp8_1x128_ue8m0(z * rs * wf, q2, s2)
+    assert torch.equal(s, s2) and torch.equal(q, q2)
+
+
+def test_packed_fp8_next_to_the_least_scale(dg):  # noqa: F811
+    """Around amax = 448 2^-127 the quotient is subnormal and is rounded before its power is taken.  Rows of ones:
+    y is the weight."""
+    say("norm ue8m0 least scale")
+    h = 128
+    amax = torch.tensor(448 * 2.0 ** -127, device="cuda").view(torch.int32)
+    x = torch.ones((1, h), dtype=BF16, device="cuda")
+    for step in range(-20, 21):
+        w = torch.full((h,), 2.0 ** -140, device="cuda")
+        w[5] = (amax + step).view(F32)
+        q, q2 = (torch.zeros((1, h), dtype=torch.uint8, device="cuda") for _ in range(2))
+        s, s2 = (torch.zeros((1, 1), dtype=torch.int32, device="cuda") for _ in range(2))
+        dg.rmsnorm_quantize_fp8_1x128(x, w, q, s, 0.0)
+        dg.dg_quantize_fp8_1x128_ue8m0(w[None].contiguous(), q2, s2)
+        assert torch.equal(s, s2) and torch.equal(q, q2), step
+
+
 # Against 64 bits: y carries 2 roundings and z one, amax the same, s two (FP8: a product with 1 / 448), its reciprocal
 # one (FP8: an ulp, two) and the code's product one; r is the same in y and amax.  11 roundings of 2^-24 < 2^-20.
 @pytest.mark.parametrize("t,h", ROWS)
