@@ -436,7 +436,8 @@ dg_status dg_moe_few_tokens_bf16(const void* x, const float* logits, int32_t* id
  * of two rows (at least H).  sum may be x or residual, and y may be any of the
  * three (with the same stride); no other overlap.  A row must keep its sum of
  * squares finite in fp32: one that does not (or holds a NaN, or zeros alone
- * where eps is 0) gets NaN scales.
+ * where eps is 0) gets NaN in the whole row of a bf16 y, or NaN scales; its r is
+ * stored as computed (0, NaN or infinity).
  * The weight and y must be finite; scales below 2^-126 are rounded up.
  * y's products are (z r) w, for INT8 (z w) r unless a row's largest |z w| lies
  * outside 2^-100 .. 2^120. */

@@ -281,11 +281,12 @@ __global__ __launch_bounds__(I == 2 ? 1024 : 512) void norm_kernel(const NormPar
         for (int k = 1; k < waves; ++k) most = fmaxf(most, part[turn][1][k]);
       }
     }
-    const float r = inverse_root(__builtin_fmaf(ss, p.inv_h, p.eps));
+    float r = inverse_root(__builtin_fmaf(ss, p.inv_h, p.eps));
     // a row with a NaN, whose sum of squares is not finite, or of zeros without an
-    // eps: NaN scales, so that what is computed from its codes is NaN too
+    // eps: NaN in y, or NaN scales, so that what is computed from its codes is NaN too
     const bool bad = !(ss < __builtin_inff()) || r == __builtin_inff();
     if (p.rstd && own == 0) p.rstd[row] = r;
+    if (OUT == kBf16 && bad) r = __builtin_nanf("");  // (r = 0 would give zeros)
     Factor f{};
     float last = r;  // INT8: y = z w last
     if constexpr (OUT == kInt8) {

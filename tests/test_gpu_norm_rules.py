@@ -112,3 +112,24 @@ def test_codes_differ_from_64_bits_at_midpoints_alone(dg, t, h, residual, weight
     v = y / (y.view(t, -1, 128).abs().amax(2) / 448).repeat_interleave(128, 1)
     step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
     assert ((f.float().to(F64) - v).abs() <= 0.5 * step + 2.0 ** -20 * v.abs()).all()
+
+
+@pytest.mark.parametrize("h", [5, 128, 300, 2111, 4096, 9000])
+def test_bf16_rows_that_have_no_norm(dg, h):  # noqa: F811
+    """A sum of squares past fp32, an infinity, a NaN, zeros without eps: NaN in the whole row, not zeros; the other
+    rows as without them."""
+    say(f"norm bf16 rows without a norm h={h}")
+    x = inputs(9, h, False, None, 26)[0]
+    alone = torch.empty((9, h), dtype=BF16, device="cuda")
+    dg.rmsnorm_bf16(x, None, alone, 0.0)
+    bad = x.clone()
+    bad[1] = 1e30
+    bad[3, h - 1] = float("inf")
+    bad[4, 0] = float("nan")
+    bad[6] = 0
+    bad[7] = -3e38
+    for total in (None, torch.empty_like(bad)):
+        y = torch.full_like(bad, 7.0)
+        dg.rmsnorm_bf16(bad, None, y, 0.0, None, total)
+        assert y[[1, 3, 4, 6, 7]].isnan().all()
+        assert torch.equal(y[[0, 2, 5, 8]], alone[[0, 2, 5, 8]])
