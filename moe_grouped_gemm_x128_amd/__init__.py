@@ -782,15 +782,16 @@ def _matrix_of(t, name, current):
 
 
 def _room(workspace, need, dev, like):
-    """Pointer of a workspace of at least `need` bytes, made if there is none."""
+    """A workspace of at least `need` bytes, made if there is none, and its pointer.  The caller holds it until the
+    library has launched: freed before, another thread's tensor could take its place."""
     if not need:
-        return None
+        return None, None
     if workspace is None:
         workspace = like.new_empty(need, dtype=torch.uint8)
     elif workspace.get_device() != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be contiguous, on the same GPU, with at least {need} bytes")
-    return workspace.data_ptr()
+    return workspace, workspace.data_ptr()
 
 
 def _norm_of(x, shape, weight, eps, residual, sum_out, rstd, dev):
@@ -905,7 +906,7 @@ def rmsnorm_bf16_backward(dout, z, weight, rstd, dx=None, dweight=None, dsum=Non
             dsp, ldds = _rows(dsum, _BF16, shape, dev, "dsum")
     if dweight is not None:
         dwp = _whole(dweight, _F32, (h,), dev, "dweight")
-        wsp = _room(workspace, rmsnorm_bf16_backward_workspace(t, h), dev, dout)
+        workspace, wsp = _room(workspace, rmsnorm_bf16_backward_workspace(t, h), dev, dout)
     st = _lib.dg_rmsnorm_bf16_backward(op, ldo, zp, ldz, wp, wt, _whole(rstd, _F32, (t,), dev, "rstd"), dsp, ldds, dxp,
                                        lddx, dwp, wsp, t, h, _stream_of(dev))
     if st:
@@ -981,11 +982,12 @@ def moe_sort_contiguous(ids, num_experts, m_indices, rows, counts=None, workspac
     shape, dev = _matrix(ids, "ids", _current_device)
     t, k = shape
     m = m_indices.shape[0]
+    workspace, wsp = _room(workspace, moe_sort_workspace(t, k, num_experts), dev, ids)
     st = _lib.dg_moe_sort_contiguous(
         _whole(ids, _I32, shape, dev, "ids"), _whole(m_indices, _I32, (m,), dev, "m_indices"),
         _whole(rows, _I32, shape, dev, "rows"),
-        None if counts is None else _whole(counts, _I32, (num_experts,), dev, "counts"),
-        _room(workspace, moe_sort_workspace(t, k, num_experts), dev, ids), t, k, num_experts, m, _stream_of(dev))
+        None if counts is None else _whole(counts, _I32, (num_experts,), dev, "counts"), wsp, t, k, num_experts, m,
+        _stream_of(dev))
     if st:
         raise DGError(st, "dg_moe_sort_contiguous")
     return m_indices, rows
@@ -997,10 +999,10 @@ def moe_sort_masked(ids, m_max, masked_m, rows, workspace=None):
     shape, dev = _matrix(ids, "ids", _current_device)
     t, k = shape
     e = masked_m.shape[0]
+    workspace, wsp = _room(workspace, moe_sort_workspace(t, k, e), dev, ids)
     st = _lib.dg_moe_sort_masked(
         _whole(ids, _I32, shape, dev, "ids"), _whole(masked_m, _I32, (e,), dev, "masked_m"),
-        _whole(rows, _I32, shape, dev, "rows"), _room(workspace, moe_sort_workspace(t, k, e), dev, ids), t, k, e, m_max,
-        _stream_of(dev))
+        _whole(rows, _I32, shape, dev, "rows"), wsp, t, k, e, m_max, _stream_of(dev))
     if st:
         raise DGError(st, "dg_moe_sort_masked")
     return masked_m, rows
