@@ -17,6 +17,7 @@ import ctypes
 import functools
 import os
 import struct
+import warnings
 
 import torch  # loads torch's HIP runtime first, so the library binds to it
 
@@ -30,11 +31,14 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-try:
+try:  # the binding's checks of tensors, natively: not needed, but 2.5 us of a call
     from . import _tensors
-except ImportError as e:
-    raise ImportError(f"the binding's native helper cannot be loaded ({e}): build it with the library "
-                      "(python moe_grouped_gemm_x128_amd/build.py); there is no fallback path") from e
+    if getattr(_tensors, "built_with", None) != str(torch.__version__):
+        raise ImportError(f"it was built with torch {getattr(_tensors, 'built_with', 'of another version')}")
+except ImportError as _e:
+    _tensors = None
+    warnings.warn(f"the binding's native helper cannot be used ({_e}), so small calls take longer; "
+                  "python moe_grouped_gemm_x128_amd/build.py builds it", RuntimeWarning)
 
 _vp, _i32 = ctypes.c_void_p, ctypes.c_int
 _lib.dg_gemm_fp8_nt.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp]
@@ -724,7 +728,8 @@ def moe_few_tokens_bf16(x, w13, w2, out, ids, weights, logits=None, scoring="sof
 # Small calls are bound by what happens before the launch, so each tensor is
 # looked at once, natively (csrc/dg_tensors.cpp).  The functions in Python that
 # have a native counterpart (_matrix_of for _matrix, ...) answer where that finds
-# anything unexpected: they work out the reason and raise.
+# anything unexpected: they work out the reason and raise.  Without the native
+# module they do all of it.
 
 _BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
 _norm_fields = struct.Struct("PqPqPifPqP").pack   # dg_norm
@@ -750,9 +755,35 @@ def _refuse(t, dtype, shape, dev, name):
                      f"overlap), got strides {t.stride()}")
 
 
-_tensors.refuse_with(_refuse)
-_whole = _tensors.whole  # address of a contiguous tensor of the given type and shape on GPU `dev`
-_rows = _tensors.rows    # address and row stride of a matrix with contiguous rows
+def _fitting(t, dtype, shape, dev, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t)}")
+    return (t.layout is torch.strided and t.dtype is dtype and t.shape == tuple(shape) and t.is_cuda
+            and t.get_device() == dev)
+
+
+def _whole_of(t, dtype, shape, dev, name):
+    """Address of a contiguous tensor of the given type and shape on GPU `dev`."""
+    if not _fitting(t, dtype, shape, dev, name) or not t.is_contiguous():
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr()
+
+
+def _rows_of(t, dtype, shape, dev, name):
+    """Address and row stride of a matrix with contiguous rows (one row: its stride may be anything)."""
+    if not _fitting(t, dtype, shape, dev, name) or t.dim() != 2:
+        _refuse(t, dtype, shape, dev, name)
+    (m, cols), (ld, one) = shape, t.stride()
+    if (one != 1 and cols > 1) or (ld < cols and m > 1):
+        _refuse(t, dtype, shape, dev, name)
+    return t.data_ptr(), ld if m > 1 else cols
+
+
+if _tensors is not None:
+    _tensors.refuse_with(_refuse)
+    _whole, _rows = _tensors.whole, _tensors.rows
+else:
+    _whole, _rows = _whole_of, _rows_of
 
 
 def _bytes8_of(t, shape, dev, name):
@@ -830,9 +861,12 @@ def _slots_of(rows, t, dev):
     return _whole(rows, _I32, shape, dev, "rows"), shape[1]
 
 
-_tensors.otherwise(_matrix_of, _vector_of, _bytes8_of, _layout_of, _slots_of, _norm_of)
-_matrix, _vector, _bytes8 = _tensors.matrix, _tensors.vector, _tensors.bytes8
-_layout, _slots, _norm = _tensors.layout, _tensors.slots, _tensors.norm
+if _tensors is not None:
+    _tensors.otherwise(_matrix_of, _vector_of, _bytes8_of, _layout_of, _slots_of, _norm_of)
+    _matrix, _vector, _bytes8 = _tensors.matrix, _tensors.vector, _tensors.bytes8
+    _layout, _slots, _norm = _tensors.layout, _tensors.slots, _tensors.norm
+else:
+    _matrix, _vector, _bytes8, _layout, _slots, _norm = _matrix_of, _vector_of, _bytes8_of, _layout_of, _slots_of, _norm_of
 
 
 def rmsnorm_bf16(x, weight, out, eps=1e-6, residual=None, sum_out=None, rstd=None):

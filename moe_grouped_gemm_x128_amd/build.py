@@ -1,5 +1,6 @@
 """Build the gfx950 HIP library (libdg_mi355x.so) in-tree with hipcc, and the
-binding's native helper (_tensors.so) with the host compiler.
+binding's native helper (_tensors) with the host compiler.  The binding works
+without the helper, only slower, so a failure of that part is a warning.
 
     python moe_grouped_gemm_x128_amd/build.py        # or build() from Python
 
@@ -11,6 +12,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -21,7 +23,8 @@ LIB = os.path.join(HERE, "libdg_mi355x.so")
 SOURCES = ["dg_api.hip", "dg_shapes.hip", "dg_kernels.hip", "dg_quant.hip", "dg_noalloc.hip", "dg_moe.hip",
            "dg_linear.hip", "dg_linear_rows.hip", "dg_linear_gemm.hip", "dg_linear_int8.hip", "dg_linear_int8_gemm.hip",
            "dg_norm.hip", "dg_moe_rows.hip"]
-TENSORS = os.path.join(HERE, "_tensors.so")
+# (named for this Python: another one does not take it for its own)
+TENSORS = os.path.join(HERE, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))
 CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -52,8 +55,6 @@ def _hipcc(args, verbose):
 
 def build_tensors(verbose: bool = False) -> str:
     """Compile csrc/dg_tensors.cpp against the installed torch."""
-    import sysconfig
-
     import torch
     from torch.utils import cpp_extension
 
@@ -61,7 +62,10 @@ def build_tensors(verbose: bool = False) -> str:
     tmp = TENSORS + ".tmp"
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           *(f"-I{p}" for p in [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]),
+           f'-DDG_TORCH_VERSION="{torch.__version__}"', "-D__HIP_PLATFORM_AMD__=1",
+           *(f"-I{p}" for p in [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+                                os.path.join(ROOT, "include"),
+                                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(HIPCC))), "include")]),
            os.path.join(CSRC, "dg_tensors.cpp"), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
            "-lc10"]
     if verbose:
@@ -76,8 +80,7 @@ def build_tensors(verbose: bool = False) -> str:
 
 def build(verbose: bool = False, extra=None) -> str:
     """Compile every source (one hipcc each, in parallel) and link the shared
-    library; always recompiles."""
-    build_tensors(verbose)
+    library, then the binding's helper; always recompiles."""
     tmp = LIB + ".tmp"
     flags = [*FLAGS, *(extra or [])]
     with tempfile.TemporaryDirectory() as objs:
@@ -86,6 +89,12 @@ def build(verbose: bool = False, extra=None) -> str:
             list(pool.map(lambda s: _hipcc([*flags, "-c", "-o", out[s], os.path.join(CSRC, s)], verbose), SOURCES))
         _hipcc([f"--offload-arch={ARCH}", "-shared", "-fPIC", *(extra or []), "-o", tmp, *out.values()], verbose)
     os.replace(tmp, LIB)
+    try:
+        build_tensors(verbose)
+    except Exception as e:
+        if os.path.exists(TENSORS):
+            os.remove(TENSORS)  # (of other sources than the library's)
+        sys.stderr.write(f"warning: the binding's native helper was not built ({e}): small calls take longer\n")
     return LIB
 
 

@@ -5,7 +5,8 @@
 // Python, the five questions about one tensor take 0.45 us, and a call has five
 // to ten tensors.  The answers and the refusals are the same as in Python: where
 // anything does not match, the functions that refuse_with() and otherwise() were
-// given are called with the same arguments, and raise.
+// given are called with the same arguments, and raise.  The binding does the same in
+// Python alone where this module is missing or was built with another torch.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -15,6 +16,8 @@
 
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include "dg.h"
 
 namespace {
 
@@ -196,18 +199,6 @@ PyObject* slots(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // (x, shape, weight, eps, residual, sum_out, rstd, GPU) -> dg_norm's bytes
-struct Norm {
-  const void* x;
-  int64_t ld_x;
-  const void* residual;
-  int64_t ld_residual;
-  const void* weight;
-  int weight_type;
-  float eps;
-  void* sum;
-  int64_t ld_sum;
-  void* rstd;
-};
 // The address and row stride of bf16 rows [m, cols] (None: null); false: something else.
 bool bf16_rows(PyObject* o, int64_t m, int64_t cols, long dev, const void** p, int64_t* ld) {
   if (o == Py_None) return true;
@@ -225,7 +216,7 @@ PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return otherwise(kNorm, args, n);
   const int64_t m = PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], 0)), h = PyLong_AsLongLong(PyTuple_GET_ITEM(args[1], 1));
   const long dev = device_of(args[7]);
-  Norm out{};
+  dg_norm out{};
   const void* sum = nullptr;
   bool fits = m >= 0 && h >= 0 && bf16_rows(args[0], m, h, dev, &out.x, &out.ld_x) &&
               bf16_rows(args[4], m, h, dev, &out.residual, &out.ld_residual) &&
@@ -241,7 +232,7 @@ PyObject* norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (fits && args[6] != Py_None) {
     const at::Tensor* r = tensor_on(args[6], dev);
     fits = r && r->dim() == 1 && r->scalar_type() == at::kFloat && r->size(0) == m && r->is_contiguous();
-    if (fits) out.rstd = r->data_ptr();
+    if (fits) out.rstd = static_cast<float*>(r->data_ptr());
   }
   if (!fits) return otherwise(kNorm, args, n);
   out.sum = const_cast<void*>(sum);
@@ -291,4 +282,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", "The binding's checks o
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject* PyInit__tensors(void) { return PyModule_Create(&module); }
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__tensors(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_with", DG_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}
