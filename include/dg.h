@@ -549,8 +549,10 @@ dg_status dg_moe_combine_bf16(const void* o, const int32_t* rows, const float* w
 /* Backward pass, with dy [T,H] bf16 the gradient of y:
  *     dout[rows[t,j]] = weights[t,j] dy[t]    [M,H] bf16 (may be o)
  *     dweights[t,j]   = <dy[t], o[rows[t,j]]> [T,k] fp32 (0 for a slot without a row)
- * (the residual's gradient is dy).  Outputs that are null are not computed, and o
- * is read for dweights only.  m_indices as in the dispatch, for dout. */
+ * (the residual's gradient is dy).  dweights are fp32 sums, off by at most
+ * (ceil(H / 4096) + 21) 2^-24 of the sum of the products' sizes.  Outputs that are null
+ * are not computed, and o is read for dweights only.  m_indices as in the dispatch,
+ * for dout. */
 dg_status dg_moe_combine_bf16_backward(const void* dy, int64_t ld_dy, const void* o, const int32_t* rows,
                                        const float* weights, const int32_t* m_indices, void* dout, float* dweights,
                                        int tokens, int top_k, int hidden, int64_t m, hipStream_t stream);

@@ -446,8 +446,11 @@ __global__ __launch_bounds__(512) void combine_backward_kernel(const CombineBack
           if (p.dweights) {
             float f[8];
             widen8(v[j], f);
+            // (8 products on their own, then one addition: a chain of H / 4096 + 7, not of 8 H / 4096)
+            float piece = d[0] * f[0];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dot[j0 + j] = __builtin_fmaf(d[e], f[e], dot[j0 + j]);
+            for (int e = 1; e < 8; ++e) piece = __builtin_fmaf(d[e], f[e], piece);
+            dot[j0 + j] += piece;
           }
           if (p.dout) {
             float f[8];
