@@ -78,7 +78,8 @@ class Training:
         new = lambda *s, dtype=BF16: torch.empty(s, dtype=dtype, device=device)
         self.m_indices, self.rows = new(m, dtype=I32), new(t, top_k, dtype=I32)
         self.n, self.y, self.dn, self.dx = (new(t, h) for _ in range(4))
-        # rows behind the last segment are never written: zeros keep them out of the weights' gradients
+        # rows behind the last segment keep what an earlier step with more segments left there: products of whole
+        # buffers leave them out by m_indices (as the grouped GEMMs and expert_gradient do)
         self.a, self.o, self.do, self.da = (torch.zeros((m, h), dtype=BF16, device=device) for _ in range(4))
         self.rstd, self.dnorm, self.dweights = new(t, dtype=F32), new(h, dtype=F32), new(t, top_k, dtype=F32)
 
@@ -91,7 +92,7 @@ class Training:
 
     def backward(self, x, weights, dy):
         """From dy bf16 [T,H]: the gradients of x, the norm's weight, the routing weights, and (as pairs of operands
-        `do`, `a` in the contiguous layout, zeros in its padding) those of the experts' weights."""
+        `do`, `a` in the contiguous layout, zeros in its segments' padding) those of the experts' weights."""
         dg.moe_combine_bf16_backward(dy, self.o, self.rows, weights, self.do, self.dweights, self.m_indices)
         dg.dg_grouped_bf16_contiguous(self.do, self.wt, self.da, self.m_indices)
         dg.moe_dispatch_bf16_backward(self.da, self.rows, self.dn)
