@@ -201,8 +201,7 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
   // LDS that a wave's sums pass through, and (WK > 1) its rows that others finish
   constexpr int kRows = 16 * RS, kGiven = (FM - FR) * FN * 1024;
   static_assert(kOwnRows || (kRows <= PART / NW && kGiven <= PART / NW), "a wave's rows fit its share of the slot");
-  constexpr int kCounted = (S - 2) * LOADS + 2 * kStores < 64 ? 2 : 1;  // kStores that a wait may leave in flight
-  static_assert((S - 2) * LOADS + kCounted * kStores < 64, "vmcnt range");
+  static_assert((S - 2) * LOADS + 2 * kStores < 64, "vmcnt range");
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = (int)uniform((tid >> 6) % NW), wk = WK == 1 ? 0 : (int)uniform((tid >> 6) / NW);
@@ -353,8 +352,8 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
       // stores are younger than the blocks that were loaded before them)
       if (kb < kBehind && stores == 1)
         dma::wait<(S - 2) * LOADS + kStores>();
-      else if (kCounted == 2 && kb < kBehind && stores == 2)
-        dma::wait<(S - 2) * LOADS + kCounted * kStores>();
+      else if (kb < kBehind && stores == 2)
+        dma::wait<(S - 2) * LOADS + 2 * kStores>();
       else
         dma::wait<(S - 2) * LOADS>();
       dma::barrier();
@@ -602,7 +601,7 @@ __device__ __forceinline__ void run_items(const GemmParams& p, int wg, int nwg, 
         issue(last);
       }
       const int per = !LINES ? 0 : (ep.out_f32 ? 2 : 1) + (ep.pre ? 1 : 0);
-      stores = per <= kCounted ? per : 0;
+      stores = per <= 2 ? per : 0;
     }
     cur = next(ct);
   }
