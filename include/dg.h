@@ -565,7 +565,8 @@ dg_status dg_moe_combine_bf16_backward(const void* dy, int64_t ld_dy, const void
  *   [N] fp32; c, epi as dg_gemm_bf16_nt_epilogue.
  * K % 16 == 0, K < 2^17 (so that no sum leaves int32); a, b 16-byte aligned with
  * strides that are multiples of 16 up to 2^22.  K is split over workgroups, and
- * not while capturing, as there; either way the result is the same. */
+ * not while capturing, as there; either way the result is the same.  pre's products
+ * are (sum sb) sa, and the first of them must stay in fp32's range too. */
 dg_status dg_gemm_int8_nt_epilogue(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
                                    const float* sb, void* c, int64_t ldc, int c_type, const dg_epilogue* epi, int m,
                                    int n, int k, hipStream_t stream);

@@ -414,7 +414,9 @@ struct BackwardParams {
 // one workgroup, so the time grows with them, while the partials' way pays a
 // second launch and their traffic (us beside : by partials): 17 x 1161 3.3 : 5.8,
 // 512 x 4096 5.3 : 11.6, 1000 x 2111 9.6 : 12.1, 1024 x 4096 13.9 : 12.7, 2048 x
-// 2048 21.6 : 12.2.
+// 2048 21.6 : 12.2.  The two meet between 768 rows and 1024, sooner where rows are
+// wide; 768 is the side of that where beside is faster at every width, so narrow
+// ones of up to some 1000 rows give away 2 us.
 constexpr int kFewRows = 768;
 
 // dw's columns c0 .. c0 + 31: a wave takes 16 rows at a time (64 columns and 8 rows:
