@@ -411,13 +411,19 @@ struct BackwardParams {
 };
 
 // Few rows: dw's columns are summed beside the rows.  A tile's rows are read by
-// one workgroup, so the time grows with them, while the partials' way pays a
-// second launch and their traffic (us beside : by partials): 17 x 1161 3.3 : 5.8,
-// 512 x 4096 5.3 : 11.6, 1000 x 2111 9.6 : 12.1, 1024 x 4096 13.9 : 12.7, 2048 x
-// 2048 21.6 : 12.2.  The two meet between 768 rows and 1024, sooner where rows are
-// wide; 768 is the side of that where beside is faster at every width, so narrow
-// ones of up to some 1000 rows give away 2 us.
-constexpr int kFewRows = 768;
+// one workgroup, so the time grows with them, and dy and z are read twice, while the
+// partials' way pays a second launch and their traffic.  GPU time, us, beside : by
+// partials, at rows of
+//             512         768         1024        1280        1536
+//     264  3.6 : 6.3   3.9 : 6.4   4.5 : 6.4   4.6 : 6.4   5.5 : 6.5
+//    1161  5.3 : 8.5   6.8 : 9.2   8.3 : 9.7   9.4 : 10.7 10.5 : 11.2
+//    2111  6.6 : 10.6  7.9 : 11.2  9.4 : 12.2 10.5 : 12.8 11.6 : 13.6
+//    4096  7.1 : 12.1  9.1 : 12.9 11.2 : 13.6 13.2 : 13.9 15.4 : 13.9
+//    7168 10.6 : 16.2 14.1 : 15.8 18.1 : 16.6 21.4 : 18.1 24.9 : 19.9
+//   10240 15.6 : 14.9 21.1 : 16.9 26.4 : 19.6 31.4 : 21.5 38.1 : 27.0
+constexpr int kFewRows = 1536;
+constexpr int64_t kFewValues = 11 << 19;
+bool few(int t, int h) { return t <= kFewRows && (int64_t)t * h <= kFewValues; }
 
 // dw's columns c0 .. c0 + 31: a wave takes 16 rows at a time (64 columns and 8 rows:
 // 517 x 1161 8.4 us for 6.0).  Where H is no multiple of 32 the last tile starts
@@ -427,7 +433,7 @@ constexpr int kTileColumns = 32;
 template <int TAIL>
 __device__ __forceinline__ void sum_columns(const BackwardParams& p, int c0, float (*part)[kTileColumns]) {
   constexpr int LPR = kTileColumns / 8, RPW = 64 / LPR;
-  constexpr int U = kFewRows / (8 * RPW);  // 8 waves or more have all rows in flight at once
+  constexpr int U = 6;  // 8 waves have 768 rows in flight at once
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int c = c0 + (lane % LPR) * 8, n = p.h - c;  // (n <= 0: none)
   const int step = waves * RPW;
@@ -735,10 +741,6 @@ bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int t, int 
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
   return a0 < b0 + 2 * ((uintptr_t)(t - 1) * ldb + h) && b0 < a0 + 2 * ((uintptr_t)(t - 1) * lda + h);
 }
-
-// (few rows: kFewRows above)
-constexpr int64_t kFewValues = 8 << 20;  // dy and z are read twice: 32 MB of them stay in the caches
-bool few(int t, int h) { return t <= kFewRows && (int64_t)t * h <= kFewValues; }
 
 }  // namespace
 }  // namespace dg
